@@ -295,7 +295,7 @@ def run_fork(s):
         import long_context_sparse_index_gb300 as dsa
         taken = dsa.dsa_cache_fork(s.cache, s.pages, s.src, s.dst)
         table, count, lens = s.table[s.case["B"]:].clone(), s.count.clone(), s.lens.clone()
-        dsa.dsa_cache_free(s.pages, s.dst)
+        dsa.dsa_cache_free(s.cache, s.pages, s.dst)
         return [taken, table, count, lens, s.table, s.count, s.lens, s.k, s.v, s.k_idx, s.khat]
     src, dst = s.src.long(), s.dst.long()
     P, width = s.P, s.table.shape[1]
