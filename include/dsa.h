@@ -292,6 +292,181 @@ dsa_status_t dsa_sparse_attn_bwd_varlen(const void* dO, const void* q, const voi
                                         void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Serving: the layer over a paged cache.  (The source pages train; they
+ * mention generation only as the engine whose log-probabilities the trainer is
+ * checked against [SkyRL-1M].  These calls run the same layer token by token
+ * or chunk by chunk, on keys and values kept in pages.)
+ *
+ * One layer's cache is `num_pages` pages of `page_size` tokens (a power of
+ * two, 16..1024); a pool of four tokens never crosses a page:
+ *   k, v    bf16 [num_pages, page_size, 128]
+ *   k_idx   bf16 [num_pages, page_size, 64]
+ *   khat    bf16 [num_pages, page_size / 4, 128]  pooled indexer keys of the
+ *           complete pools as a pair: columns 0..63 hi = bf16(Khat), columns
+ *           64..127 lo = bf16(Khat - hi)
+ * *_stride is the distance in elements from one page to the next (a multiple
+ * of 8, at least a page), so the pages of several layers may alternate in one
+ * allocation; within a page everything is contiguous.  Pointers are 16-byte
+ * aligned; num_pages * page_size <= 2^31 - 1.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_idx;
+  void* khat;
+  int64_t k_stride, v_stride, k_idx_stride, khat_stride;
+  int64_t num_pages;
+  int page_size;
+  int D;   /* 128 */
+  int Di;  /* 64 */
+} dsa_paged_cache_t;
+
+/*
+ * The sequences of a call and their new tokens.  Everything here is on the
+ * DEVICE, so that a captured graph of the calls can be replayed with other
+ * contents.
+ *   block_table  int32 [batch, max_pages], rows table_stride elements apart:
+ *                page x of sequence s holds its tokens x * page_size, ...
+ *   seq_lens     int32 [batch]  tokens of each sequence, its new ones included
+ *   cu_q         int32 [batch + 1]  ascending from 0: rows cu_q[s] ..
+ *                cu_q[s+1]-1 of the call's tensors are sequence s's new tokens,
+ *                the last of the sequence, in order (none is allowed)
+ *   rows         rows of the call's tensors, at least cu_q[batch]; the rows
+ *                behind the last sequence are padding: neither read nor written
+ * batch 1..8192; max_pages * page_size <= 2^31 - 1.  Row r of sequence s has
+ * position i = seq_lens[s] - cu_q[s+1] + r.
+ * These arrays are read when the kernels run, so they cannot be checked before
+ * a launch.  The kernels follow no length, offset or page number that is out
+ * of range: such a row's outputs are undefined (never written outside the row),
+ * and dsa_sync_status reports DSA_ERR_INTERNAL.  Page numbers inside the cache
+ * are trusted.
+ */
+typedef struct {
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  int64_t rows;
+  int max_pages;
+  int batch;
+} dsa_paged_batch_t;
+
+/*
+ * The page bookkeeping of a cache: device arrays that the page operators
+ * write.
+ *   block_table  int32 [max_seqs, max_pages], rows table_stride apart; entries
+ *                past a sequence's pages are -1 or anything
+ *   seq_lens     int32 [max_seqs]  0: the row is free
+ *   page_count   int32 [num_pages] how many sequences hold the page (0: free)
+ */
+typedef struct {
+  int32_t* block_table;
+  int64_t table_stride;
+  int32_t* seq_lens;
+  int32_t* page_count;
+  int64_t num_pages;
+  int max_pages;
+  int max_seqs;
+  int page_size;
+} dsa_page_table_t;
+
+/*
+ * Writes new tokens into their pages: k, v bf16 [rows, 128] and k_idx bf16
+ * [rows, 64] (rows *_stride elements apart, multiples of 8; 16-byte aligned)
+ * to the slots of their positions, and khat of every pool that they complete,
+ * from its four indexer keys (older ones from the page).  Appending again at
+ * earlier positions (a rejected draft) rewrites the slots and recomputes the
+ * pools.  No two sequences of the batch may write the same page.
+ */
+dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                              int64_t k_idx_stride, void* stream);
+
+/* Copies page src[j] onto page dst[j], all four buffers, for j < n (device
+ * int32 arrays).  The copies run in any order: no page may be named in dst
+ * twice, or in dst and (for another pair) in src. */
+dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
+                                  void* stream);
+
+/* Bytes of workspace the calls below need for a cache of num_pages pages, a
+ * table of max_seqs rows and, for the fork, n children (0 for bad sizes).
+ * Calls that share a workspace must be ordered on the device. */
+size_t dsa_cache_workspace(int64_t num_pages, int max_seqs, int64_t n);
+
+/*
+ * Grows every sequence s by add[s] >= 0 tokens (device int32 [max_seqs]):
+ * seq_lens[s] += add[s], and the pages it then needs are taken, the lowest
+ * free ones in the order of sequences and of positions.  *result (device
+ * int32) is the number of pages taken.  When too few are free, nothing
+ * changes and *result is minus the number lacking; for a length that max_pages
+ * cannot hold, or a negative one, nothing changes, *result is INT32_MIN and
+ * the status reports DSA_ERR_INTERNAL.
+ */
+dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add, int32_t* result, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * Forks sequences: row dst[j] becomes a copy of sequence src[j] for j < n
+ * (device int32 arrays).  Full pages are shared (page_count + 1); a partly
+ * filled last page is copied to a free one of the child's own, the lowest free
+ * ones in the order of j.  A parent may have several children.  Every row
+ * dst[j] must be free (length 0) and named once.  *result as above.
+ */
+dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, const int32_t* src,
+                            const int32_t* dst, int64_t n, int32_t* result, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/* Frees sequences seqs[0 .. n-1] (device int32): their pages' counts go down
+ * by one, their table entries become -1, their lengths 0.  Freeing a free row,
+ * or the same row twice, does nothing. */
+dsa_status_t dsa_cache_free(const dsa_page_table_t* pages, const int32_t* seqs, int64_t n, void* stream);
+
+/*
+ * Compacts the cache: with U pages in use, those numbered U or more move into
+ * the free ones below U (the k-th of them to the k-th free one, both
+ * ascending); page_count and every entry of block_table that names a moved
+ * page follow.  Afterwards pages 0 .. U-1 are in use.  result (device int32
+ * [2]): U, and the number of pages moved.  The cache must be the one whose
+ * pages the table counts.
+ */
+dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, int32_t* result,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace dsa_paged_index_topk is best given: 4 B per row and pool
+ * of max_pages pages, in passes of rows that together stay under 1 GiB.  It
+ * accepts less, down to the bytes for min(rows, 8) rows, with the same result.
+ * Returns 0 for invalid sizes (and for rows = 0, which needs none). */
+size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size);
+
+/*
+ * Indexer + top-k of the new tokens over the paged pooled keys: pool_idx int32
+ * [rows, topk], for the row at position i the min(topk, floor(i/4)) pools p <
+ * floor(i/4) with the largest
+ *   score(i,p) = sum_h w[h] * ReLU(q_idx[h] . Khat_p)
+ * ascending, ties to the lower pool, then -1, as dsa_index_topk writes them.
+ *   q_idx  bf16 [rows, Hi, Di]   w  fp32 [rows, Hi]   (Hi 1..64, Di = 64)
+ * The new tokens must have been appended.  Scores are fp32 sums over the bf16
+ * pair; the selection is exact with respect to them, and the same on every run.
+ */
+dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
+                                  const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * Sparse attention of the new tokens over the paged cache: the row at position
+ * i attends to the four keys of each pool in its row of pool_idx (int32 [rows,
+ * topk], ascending, -1 padded, every entry < floor(i/4)) and to its own partial
+ * pool {4*floor(i/4), ..., i}; the new tokens must have been appended.
+ *   q  bf16 [rows, Hq, D]   o  bf16 [rows, Hq, D]   lse  fp32 [rows, Hq]
+ * Hq = 16, D = 128; scale and lse as in dsa_sparse_attn_fwd.  Needs no
+ * workspace; the same bits on every run.
+ */
+dsa_status_t dsa_paged_sparse_attn_fwd(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q,
+                                       const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o,
+                                       float* lse, void* stream);
+
+/*
  * Indexer + top-k for callers that cannot allocate device memory.  (The
  * source pages have no counterpart to this call; it exists for users of the
  * library.)

@@ -32,7 +32,9 @@ EXPORTED = ("dsa_index_topk_workspace", "dsa_index_topk", "dsa_sparse_attn_fwd",
             "dsa_sparse_attn_bwd_deterministic_workspace", "dsa_sparse_attn_bwd_deterministic",
             "dsa_index_topk_stats", "dsa_measure_l2", "dsa_index_topk_workspace_slots", "dsa_trace_configure",
             "dsa_last_kernel_config", "dsa_sparse_attn_fwd_tc", "dsa_measure_umma",
-            "dsa_fwd_tc_profile", "dsa_measure_fold")
+            "dsa_fwd_tc_profile", "dsa_measure_fold", "dsa_cache_append", "dsa_cache_copy_pages",
+            "dsa_cache_workspace", "dsa_cache_reserve", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
+            "dsa_paged_index_topk_workspace", "dsa_paged_index_topk", "dsa_paged_sparse_attn_fwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -111,6 +113,8 @@ def _configure(lib):
     lib.dsa_measure_fold.restype = ctypes.c_double
     lib.dsa_last_kernel_config.argtypes = [ctypes.c_char_p, sz]
     lib.dsa_last_kernel_config.restype = ctypes.c_int
+    from ._paged import _configure_paged
+    _configure_paged(lib)
     return lib
 
 

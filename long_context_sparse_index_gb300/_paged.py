@@ -1,0 +1,347 @@
+"""Serving a DSA layer from a paged cache (argument marshalling only).
+
+``PagedCache`` holds one layer's pages, ``PagedBatch`` the sequences of a call
+and ``PageTable`` the page bookkeeping; each checks its tensors once and keeps
+them, so that the calls themselves stay short.  As in ``_binding``, all
+arithmetic runs in libdsa's CUDA kernels on the current CUDA stream (or the
+one given), and outputs and workspaces that the caller does not pass are
+allocated with torch, on the stream that the call runs on.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._binding import _check, _need, _out, _shape, load
+
+_vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_idx", _vp), ("khat", _vp), ("k_stride", _i64), ("v_stride", _i64),
+                ("k_idx_stride", _i64), ("khat_stride", _i64), ("num_pages", _i64), ("page_size", _i32), ("D", _i32),
+                ("Di", _i32)]
+
+
+class _BatchStruct(ctypes.Structure):
+    _fields_ = [("block_table", _vp), ("table_stride", _i64), ("seq_lens", _vp), ("cu_q", _vp), ("rows", _i64),
+                ("max_pages", _i32), ("batch", _i32)]
+
+
+class _TableStruct(ctypes.Structure):
+    _fields_ = [("block_table", _vp), ("table_stride", _i64), ("seq_lens", _vp), ("page_count", _vp),
+                ("num_pages", _i64), ("max_pages", _i32), ("max_seqs", _i32), ("page_size", _i32)]
+
+
+def _on_device(t, name: str, dtype, ndim: int):
+    """_need without contiguity: a CUDA tensor on the current device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the kernels run on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions (got shape {tuple(t.shape)})")
+
+
+def _rows_strided(t, name: str, dtype, row: int):
+    """[rows, row] whose rows are contiguous; the distance between rows is free."""
+    _on_device(t, name, dtype, 2)
+    if t.shape[1] != row or (t.shape[0] > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must have contiguous rows of {row} elements (got shape {tuple(t.shape)}, "
+                         f"strides {t.stride()})")
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _table(t, name: str):
+    _on_device(t, name, torch.int32, 2)
+    if t.numel() == 0 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be int32 with contiguous rows (got shape {tuple(t.shape)}, "
+                         f"strides {t.stride()})")
+
+
+def _same_device(owner, what: str):
+    if owner.device_index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on cuda:{owner.device_index}, but the kernels run on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+class PagedCache:
+    """One layer's cache in pages of ``page_size`` tokens (a power of two, 16..1024).
+
+    k, v [pages, page_size, 128], k_idx [pages, page_size, 64] and khat
+    [pages, page_size / 4, 128] (pooled indexer keys: hi in columns 0..63, lo
+    in 64..127), all bf16.  Within a page everything is contiguous; the
+    distance between pages is free (a multiple of 8 elements)."""
+
+    def __init__(self, k, v, k_idx, khat):
+        for t, n, d in ((k, "k", 128), (v, "v", 128), (k_idx, "k_idx", 64), (khat, "khat", 128)):
+            _on_device(t, n, torch.bfloat16, 3)
+            if t.shape[2] != d or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+                raise ValueError(f"{n} must be [pages, tokens, {d}] with contiguous pages (got shape "
+                                 f"{tuple(t.shape)}, strides {t.stride()})")
+        pages, page_size = k.shape[0], k.shape[1]
+        _shape(v, "v", (pages, page_size, 128))
+        _shape(k_idx, "k_idx", (pages, page_size, 64))
+        _shape(khat, "khat", (pages, page_size // 4, 128))
+        self.k, self.v, self.k_idx, self.khat = k, v, k_idx, khat
+        self.num_pages, self.page_size = pages, page_size
+        self.device = k.device
+        self.device_index = k.device.index
+
+        def stride(t):
+            return t.stride(0) if pages > 1 else t.shape[1] * t.shape[2]
+
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_idx.data_ptr(), khat.data_ptr(), stride(k),
+                                    stride(v), stride(k_idx), stride(khat), pages, page_size, 128, 64)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, device="cuda"):
+        """A cache of uninitialised pages."""
+        def new(tokens, d):
+            return torch.empty(num_pages, tokens, d, dtype=torch.bfloat16, device=device)
+        return cls(new(page_size, 128), new(page_size, 128), new(page_size, 64), new(page_size // 4, 128))
+
+
+class PagedBatch:
+    """The sequences of a call and their new tokens, as int32 device tensors:
+    block_table [batch, max_pages], seq_lens [batch] (new tokens included) and
+    cu_q [batch + 1] (rows cu_q[s] .. cu_q[s+1]-1 of the call's tensors are
+    sequence s's new tokens).  The contents are read when the kernels run."""
+
+    def __init__(self, block_table, seq_lens, cu_q):
+        _table(block_table, "block_table")
+        _need(seq_lens, "seq_lens", torch.int32, 1)
+        _need(cu_q, "cu_q", torch.int32, 1)
+        self.batch, self.max_pages = cu_q.shape[0] - 1, block_table.shape[1]
+        if self.batch < 1 or block_table.shape[0] < self.batch or seq_lens.shape[0] < self.batch:
+            raise ValueError("cu_q must have batch + 1 entries, block_table and seq_lens at least batch rows")
+        self.block_table, self.seq_lens, self.cu_q = block_table, seq_lens, cu_q
+        self.device_index = block_table.device.index
+        self._fields = (block_table.data_ptr(), block_table.stride(0) if block_table.shape[0] > 1 else self.max_pages,
+                        seq_lens.data_ptr(), cu_q.data_ptr())
+
+    def _with_rows(self, rows: int):
+        # a struct of its own for every call: threads may share a batch
+        return ctypes.byref(_BatchStruct(*self._fields, rows, self.max_pages, self.batch))
+
+
+class PageTable:
+    """The page bookkeeping of a cache, as int32 device tensors that the page
+    operators write: block_table [max_seqs, max_pages], seq_lens [max_seqs] (0:
+    the row is free) and page_count [num_pages] (sequences holding the page, 0:
+    free)."""
+
+    def __init__(self, block_table, seq_lens, page_count):
+        _table(block_table, "block_table")
+        _need(seq_lens, "seq_lens", torch.int32, 1)
+        _need(page_count, "page_count", torch.int32, 1)
+        self.max_seqs, self.max_pages = block_table.shape
+        _shape(seq_lens, "seq_lens", (self.max_seqs,))
+        if page_count.shape[0] < 1:
+            raise ValueError("page_count must have an entry per page")
+        self.block_table, self.seq_lens, self.page_count = block_table, seq_lens, page_count
+        self.num_pages = page_count.shape[0]
+        self.device, self.device_index = block_table.device, block_table.device.index
+        self._fields = (block_table.data_ptr(), block_table.stride(0) if self.max_seqs > 1 else self.max_pages,
+                        seq_lens.data_ptr(), page_count.data_ptr(), self.num_pages, self.max_pages, self.max_seqs)
+
+    @classmethod
+    def empty(cls, cache: PagedCache, max_seqs: int, max_pages: int):
+        """The table of a cache in which every page is free."""
+        dev = cache.device
+        return cls(torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=dev),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=dev),
+                   torch.zeros(cache.num_pages, dtype=torch.int32, device=dev))
+
+    def _with_page(self, page_size: int):
+        return ctypes.byref(_TableStruct(*self._fields, page_size))
+
+
+def _configure_paged(lib):
+    f32, sz, i64, i32, vp = ctypes.c_float, ctypes.c_size_t, _i64, _i32, _vp
+    lib.dsa_cache_append.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.dsa_cache_copy_pages.argtypes = [vp, vp, vp, i64, vp]
+    lib.dsa_cache_workspace.argtypes = [i64, i32, i64]
+    lib.dsa_cache_workspace.restype = sz
+    lib.dsa_cache_reserve.argtypes = [vp, vp, vp, vp, sz, vp]
+    lib.dsa_cache_fork.argtypes = [vp, vp, vp, vp, i64, vp, vp, sz, vp]
+    lib.dsa_cache_free.argtypes = [vp, vp, i64, vp]
+    lib.dsa_cache_compact.argtypes = [vp, vp, vp, vp, sz, vp]
+    lib.dsa_paged_index_topk_workspace.argtypes = [i64, i32, i32]
+    lib.dsa_paged_index_topk_workspace.restype = sz
+    lib.dsa_paged_index_topk.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, sz, vp]
+    lib.dsa_paged_sparse_attn_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp]
+    for f in (lib.dsa_cache_append, lib.dsa_cache_copy_pages, lib.dsa_cache_reserve, lib.dsa_cache_fork,
+              lib.dsa_cache_free, lib.dsa_cache_compact, lib.dsa_paged_index_topk, lib.dsa_paged_sparse_attn_fwd):
+        f.restype = ctypes.c_int
+
+
+class _On:
+    """The call's stream, and allocations that belong to it."""
+
+    def __init__(self, stream, device):
+        self.stream, self.device = stream, device
+        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+    def new(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def out(self, given, name, shape, dtype):
+        return self.new(shape, dtype) if given is None else _out(given, name, shape, dtype, self.device)
+
+    def workspace(self, nbytes, given):
+        if given is None:
+            given = self.new(max(nbytes, 256), torch.uint8)
+        else:
+            _need(given, "workspace", given.dtype, given.dim())
+        return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _ids(t, name: str):
+    _need(t, name, torch.int32, 1)
+
+
+def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=None):
+    """Writes the new tokens' k, v [rows, 128] and k_idx [rows, 64] (bf16, rows
+    any distance apart) into their pages, and the pooled key of every pool that
+    they complete."""
+    _same_device(cache, "cache")
+    _same_device(batch, "batch")
+    _rows_strided(k, "k", torch.bfloat16, 128)
+    _rows_strided(v, "v", torch.bfloat16, 128)
+    _rows_strided(k_idx, "k_idx", torch.bfloat16, 64)
+    rows = k.shape[0]
+    _shape(v, "v", (rows, 128))
+    _shape(k_idx, "k_idx", (rows, 64))
+    _check(load().dsa_cache_append(cache._ref, batch._with_rows(rows), k.data_ptr(), _row_stride(k), v.data_ptr(),
+                                   _row_stride(v), k_idx.data_ptr(), _row_stride(k_idx),
+                                   _On(stream, cache.device).handle))
+
+
+def dsa_cache_copy_pages(cache: PagedCache, src, dst, stream=None):
+    """Copies page src[j] onto page dst[j] (int32 tensors), all four buffers."""
+    _same_device(cache, "cache")
+    _ids(src, "src")
+    _ids(dst, "dst")
+    _shape(dst, "dst", tuple(src.shape))
+    _check(load().dsa_cache_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(), src.shape[0],
+                                       _On(stream, cache.device).handle))
+
+
+def cache_workspace_size(num_pages: int, max_seqs: int, n: int = 0) -> int:
+    """Bytes of workspace of the page operators (n: children of a fork)."""
+    return int(load().dsa_cache_workspace(num_pages, max_seqs, n))
+
+
+def _of_cache(cache: PagedCache, pages: PageTable):
+    _same_device(cache, "cache")
+    if pages.device_index != cache.device_index or pages.num_pages != cache.num_pages:
+        raise ValueError(f"the page table counts {pages.num_pages} pages on cuda:{pages.device_index}, the cache has "
+                         f"{cache.num_pages} on cuda:{cache.device_index}")
+
+
+def dsa_cache_reserve(cache: PagedCache, pages: PageTable, add, result=None, workspace=None, stream=None):
+    """Grows every sequence s by add[s] tokens (int32 [max_seqs]), taking the
+    lowest free pages; returns a device word: pages taken, or minus the number
+    lacking (then nothing changed)."""
+    _of_cache(cache, pages)
+    _ids(add, "add")
+    _shape(add, "add", (pages.max_seqs,))
+    on, lib = _On(stream, cache.device), load()
+    result = on.out(result, "result", (1,), torch.int32)
+    ws, ptr, size = on.workspace(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace)
+    _check(lib.dsa_cache_reserve(pages._with_page(cache.page_size), add.data_ptr(), result.data_ptr(), ptr, size,
+                                 on.handle))
+    return result
+
+
+def dsa_cache_fork(cache: PagedCache, pages: PageTable, src, dst, result=None, workspace=None, stream=None):
+    """Row dst[j] becomes a copy of sequence src[j] (int32 tensors): full pages
+    shared, a partly filled last page copied; returns a device word: pages
+    taken, or minus the number lacking (then nothing changed)."""
+    _of_cache(cache, pages)
+    _ids(src, "src")
+    _ids(dst, "dst")
+    n = src.shape[0]
+    _shape(dst, "dst", (n,))
+    on, lib = _On(stream, cache.device), load()
+    result = on.out(result, "result", (1,), torch.int32)
+    ws, ptr, size = on.workspace(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, n), workspace)
+    _check(lib.dsa_cache_fork(cache._ref, pages._with_page(cache.page_size), src.data_ptr(), dst.data_ptr(), n,
+                              result.data_ptr(), ptr, size, on.handle))
+    return result
+
+
+def dsa_cache_free(cache: PagedCache, pages: PageTable, seqs, stream=None):
+    """Frees the sequences named in seqs (int32 tensor)."""
+    _of_cache(cache, pages)
+    _ids(seqs, "seqs")
+    _check(load().dsa_cache_free(pages._with_page(cache.page_size), seqs.data_ptr(), seqs.shape[0],
+                                 _On(stream, cache.device).handle))
+
+
+def dsa_cache_compact(cache: PagedCache, pages: PageTable, result=None, workspace=None, stream=None):
+    """Moves the used pages down over the free ones; returns device words
+    [pages in use, pages moved]."""
+    _of_cache(cache, pages)
+    on, lib = _On(stream, cache.device), load()
+    result = on.out(result, "result", (2,), torch.int32)
+    ws, ptr, size = on.workspace(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace)
+    _check(lib.dsa_cache_compact(cache._ref, pages._with_page(cache.page_size), result.data_ptr(), ptr, size,
+                                 on.handle))
+    return result
+
+
+def paged_index_topk_workspace_size(rows: int, max_pages: int, page_size: int) -> int:
+    return int(load().dsa_paged_index_topk_workspace(rows, max_pages, page_size))
+
+
+def dsa_paged_index_topk(cache: PagedCache, batch: PagedBatch, q_idx, w, topk: int, pool_idx=None, workspace=None,
+                         stream=None):
+    """pool_idx [rows, topk] int32 of the new tokens' selected pools (ascending,
+    -1 padded), for q_idx [rows, Hi, 64] bf16 and w [rows, Hi] fp32."""
+    _same_device(cache, "cache")
+    _same_device(batch, "batch")
+    _need(q_idx, "q_idx", torch.bfloat16, 3)
+    _need(w, "w", torch.float32, 2)
+    rows, Hi, Di = q_idx.shape
+    _shape(w, "w", (rows, Hi))
+    on, lib = _On(stream, cache.device), load()
+    pool_idx = on.out(pool_idx, "pool_idx", (rows, max(topk, 0)), torch.int32)
+    ws, ptr, size = on.workspace(lib.dsa_paged_index_topk_workspace(rows, batch.max_pages, cache.page_size), workspace)
+    _check(lib.dsa_paged_index_topk(cache._ref, batch._with_rows(rows), q_idx.data_ptr(), w.data_ptr(), Hi, Di, topk,
+                                    pool_idx.data_ptr(), ptr, size, on.handle))
+    return pool_idx
+
+
+def dsa_paged_sparse_attn_fwd(cache: PagedCache, batch: PagedBatch, q, pool_idx, scale: float = 0.0, o=None, lse=None,
+                              stream=None):
+    """(o [rows, 16, 128] bf16, lse [rows, 16] fp32) of the new tokens' attention
+    over their selected pools and their own partial pool."""
+    _same_device(cache, "cache")
+    _same_device(batch, "batch")
+    _need(q, "q", torch.bfloat16, 3)
+    _need(pool_idx, "pool_idx", torch.int32, 2)
+    rows, Hq, D = q.shape
+    if pool_idx.shape[0] != rows:
+        raise ValueError(f"pool_idx must have {rows} rows (got {pool_idx.shape[0]})")
+    on = _On(stream, cache.device)
+    o = on.out(o, "o", (rows, Hq, D), torch.bfloat16)
+    lse = on.out(lse, "lse", (rows, Hq), torch.float32)
+    _check(load().dsa_paged_sparse_attn_fwd(cache._ref, batch._with_rows(rows), q.data_ptr(), pool_idx.data_ptr(), Hq,
+                                            D, pool_idx.shape[1], float(scale), o.data_ptr(), lse.data_ptr(),
+                                            on.handle))
+    return o, lse

@@ -8,6 +8,7 @@
 // [Anyscale, the lesson on checking that every layer runs the kernel one
 // expects] a shape the kernels do not implement is an error, never a silent
 // fallback; dsa_last_kernel_config reports what each call launched.
+#include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -25,6 +26,7 @@
 #include "../../include/dsa.h"
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
+#include "paged_kernels.h"
 
 namespace dsa {
 // Unique id of the calling thread's current CUDA context, or 0 when there is
@@ -1193,5 +1195,378 @@ int dsa_profile_read(char* names, int name_len, double* ms, int64_t* launches, i
 int64_t dsa_launch_count(void) { return g_launches.load(); }
 
 void dsa_launch_count_reset(void) { g_launches.store(0); }
+
+// ---------------------------------------------------------------- paged cache
+namespace {
+
+constexpr int kMaxPagedBatch = 8192;  // the sequences' work prefix lies in shared memory
+constexpr int64_t kIntMax = 0x7FFFFFFFLL;
+constexpr int64_t kPagedScratch = int64_t{1} << 28;  // scores of a pass in the recommended workspace (1 GiB)
+constexpr int64_t kPagedPassMax = int64_t{1} << 31;  // scores of a pass however large the workspace
+constexpr int kPagedMinRows = 8;
+
+bool page_size_ok(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+dsa_status_t cache_view(const char* fn, const dsa_paged_cache_t* c, dsa::CacheView* out) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "%s: null cache", fn);
+  if (!c->k || !c->v || !c->k_idx || !c->khat) return fail(DSA_ERR_INVALID_ARG, "%s: null cache pointer", fn);
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_idx) || !aligned16(c->khat))
+    return fail(DSA_ERR_INVALID_ARG, "%s: cache buffers must be 16-byte aligned", fn);
+  if (c->D != kD || c->Di != kDi)
+    return fail(DSA_ERR_UNSUPPORTED, "%s: D=%d, Di=%d unsupported (kernels implement D=128, Di=64)", fn, c->D, c->Di);
+  if (!page_size_ok(c->page_size))
+    return fail(DSA_ERR_UNSUPPORTED, "%s: page_size=%d unsupported (a power of two, 16..1024)", fn, c->page_size);
+  if (c->num_pages < 1 || c->num_pages > kIntMax / c->page_size)
+    return fail(DSA_ERR_INVALID_ARG, "%s: num_pages=%lld out of range (num_pages * page_size <= 2^31 - 1)", fn,
+                (long long)c->num_pages);
+  const int64_t page = c->page_size;
+  const struct { int64_t stride, least; const char* name; } strides[4] = {
+      {c->k_stride, page * kD, "k"}, {c->v_stride, page * kD, "v"}, {c->k_idx_stride, page * kDi, "k_idx"},
+      {c->khat_stride, page / 4 * 2 * kDi, "khat"}};
+  for (const auto& st : strides)
+    if (st.stride < st.least || (st.stride & 7) != 0)
+      return fail(DSA_ERR_INVALID_ARG, "%s: %s page stride of %lld elements (a multiple of 8, at least %lld)", fn,
+                  st.name, (long long)st.stride, (long long)st.least);
+  *out = dsa::CacheView{static_cast<__nv_bfloat16*>(c->k), static_cast<__nv_bfloat16*>(c->v),
+                        static_cast<__nv_bfloat16*>(c->k_idx), static_cast<__nv_bfloat16*>(c->khat), c->k_stride,
+                        c->v_stride, c->k_idx_stride, c->khat_stride, static_cast<int>(c->num_pages),
+                        log2_of(c->page_size)};
+  return DSA_OK;
+}
+
+dsa_status_t batch_view(const char* fn, const dsa_paged_batch_t* b, int page_size, dsa::BatchView* out) {
+  if (!b) return fail(DSA_ERR_INVALID_ARG, "%s: null batch", fn);
+  if (!b->block_table || !b->seq_lens || !b->cu_q) return fail(DSA_ERR_INVALID_ARG, "%s: null batch pointer", fn);
+  if (!aligned4(b->block_table) || !aligned4(b->seq_lens) || !aligned4(b->cu_q))
+    return fail(DSA_ERR_INVALID_ARG, "%s: block_table, seq_lens and cu_q must be 4-byte aligned", fn);
+  if (b->batch < 1) return fail(DSA_ERR_INVALID_ARG, "%s: batch=%d must be >= 1", fn, b->batch);
+  if (b->batch > kMaxPagedBatch)
+    return fail(DSA_ERR_UNSUPPORTED, "%s: batch=%d unsupported (max %d)", fn, b->batch, kMaxPagedBatch);
+  if (b->max_pages < 1 || b->max_pages > kIntMax / page_size)
+    return fail(DSA_ERR_INVALID_ARG, "%s: max_pages=%d out of range (max_pages * page_size <= 2^31 - 1)", fn,
+                b->max_pages);
+  if (b->table_stride < b->max_pages)
+    return fail(DSA_ERR_INVALID_ARG, "%s: table_stride=%lld is less than max_pages=%d", fn,
+                (long long)b->table_stride, b->max_pages);
+  if (b->rows < 0 || b->rows > (int64_t{1} << 27))
+    return fail(DSA_ERR_INVALID_ARG, "%s: rows=%lld out of range (0..2^27)", fn, (long long)b->rows);
+  *out = dsa::BatchView{b->block_table, b->table_stride, b->max_pages, b->seq_lens, b->cu_q, b->batch, b->rows};
+  return DSA_OK;
+}
+
+dsa_status_t table_view(const char* fn, const dsa_page_table_t* t, dsa::PageTableView* out) {
+  if (!t) return fail(DSA_ERR_INVALID_ARG, "%s: null page table", fn);
+  if (!t->block_table || !t->seq_lens || !t->page_count)
+    return fail(DSA_ERR_INVALID_ARG, "%s: null page table pointer", fn);
+  if (!aligned4(t->block_table) || !aligned4(t->seq_lens) || !aligned4(t->page_count))
+    return fail(DSA_ERR_INVALID_ARG, "%s: block_table, seq_lens and page_count must be 4-byte aligned", fn);
+  if (!page_size_ok(t->page_size))
+    return fail(DSA_ERR_UNSUPPORTED, "%s: page_size=%d unsupported (a power of two, 16..1024)", fn, t->page_size);
+  if (t->num_pages < 1 || t->num_pages > kIntMax / t->page_size)
+    return fail(DSA_ERR_INVALID_ARG, "%s: num_pages=%lld out of range (num_pages * page_size <= 2^31 - 1)", fn,
+                (long long)t->num_pages);
+  if (t->max_seqs < 1) return fail(DSA_ERR_INVALID_ARG, "%s: max_seqs=%d must be >= 1", fn, t->max_seqs);
+  if (t->max_pages < 1 || t->max_pages > kIntMax / t->page_size)
+    return fail(DSA_ERR_INVALID_ARG, "%s: max_pages=%d out of range (max_pages * page_size <= 2^31 - 1)", fn,
+                t->max_pages);
+  if (t->table_stride < t->max_pages)
+    return fail(DSA_ERR_INVALID_ARG, "%s: table_stride=%lld is less than max_pages=%d", fn,
+                (long long)t->table_stride, t->max_pages);
+  *out = dsa::PageTableView{t->block_table, t->table_stride, t->max_pages, t->seq_lens, t->max_seqs, t->page_count};
+  return DSA_OK;
+}
+
+dsa_status_t check_ws(const char* fn, const void* workspace, size_t ws_bytes, size_t need) {
+  if (!workspace || ws_bytes < need)
+    return fail(DSA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? ws_bytes : (size_t)0);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+  return DSA_OK;
+}
+
+int64_t paged_score_ld(int max_pages, int page_size) {
+  return static_cast<int64_t>(max_pages) * (page_size / 4);  // a multiple of 4: page_size >= 16
+}
+
+}  // namespace
+
+dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                              int64_t k_idx_stride, void* stream) try {
+  const char* fn = "dsa_cache_append";
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa::BatchView b;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st == DSA_OK) st = batch_view(fn, batch, cache->page_size, &b);
+  if (st != DSA_OK) return st;
+  if (b.rows == 0) return DSA_OK;
+  if (!k || !v || !k_idx) return fail(DSA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_idx))
+    return fail(DSA_ERR_INVALID_ARG, "%s: k, v and k_idx must be 16-byte aligned", fn);
+  if (k_stride < kD || v_stride < kD || k_idx_stride < kDi || ((k_stride | v_stride | k_idx_stride) & 7) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: row strides must be multiples of 8 elements, at least a row", fn);
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("rows", b.rows);
+  dsa::call_param("batch", b.batch);
+  dsa::call_variant("a warp per four rows");
+  const dsa::AppendArgs a{static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+                          static_cast<const __nv_bfloat16*>(k_idx), k_stride, v_stride, k_idx_stride};
+  cudaError_t e = timed_launch("cache_append", ctx.stream, [&] { return dsa::launch_cache_append(c, b, a, ctx); });
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_append: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
+                                  void* stream) try {
+  const char* fn = "dsa_cache_copy_pages";
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st != DSA_OK) return st;
+  if (n < 0 || n > kIntMax) return fail(DSA_ERR_INVALID_ARG, "%s: n=%lld out of range", fn, (long long)n);
+  if (n == 0) return DSA_OK;
+  if (!src || !dst || !aligned4(src) || !aligned4(dst))
+    return fail(DSA_ERR_INVALID_ARG, "%s: src and dst must be 4-byte aligned device arrays", fn);
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("n", n);
+  dsa::call_variant("a block per 32 KB of a page");
+  cudaError_t e = timed_launch("copy_pages", ctx.stream, [&] { return dsa::launch_copy_pages(c, src, dst, n, ctx); });
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_copy_pages: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+size_t dsa_cache_workspace(int64_t num_pages, int max_seqs, int64_t n) {
+  if (num_pages < 1 || num_pages > kIntMax || max_seqs < 1 || n < 0 || n > kIntMax) return 0;
+  // the fork's list holds one page per child
+  int64_t w = dsa::fork_ws_words(n, max_seqs);
+  const int64_t r = dsa::reserve_ws_words(max_seqs, static_cast<int>(num_pages));
+  const int64_t z = dsa::compact_ws_words(static_cast<int>(num_pages));
+  w = w > r ? w : r;
+  w = w > z ? w : z;
+  return round_up(static_cast<size_t>(w) * 4, 256);
+}
+
+dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add, int32_t* result, void* workspace,
+                               size_t ws_bytes, void* stream) try {
+  const char* fn = "dsa_cache_reserve";
+  const dsa::CallScope scope(fn);
+  dsa::PageTableView t;
+  dsa_status_t st = table_view(fn, pages, &t);
+  if (st != DSA_OK) return st;
+  if (!add || !result || !aligned4(add) || !aligned4(result))
+    return fail(DSA_ERR_INVALID_ARG, "%s: add and result must be 4-byte aligned device arrays", fn);
+  const int np = static_cast<int>(pages->num_pages);
+  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(dsa::reserve_ws_words(t.max_seqs, np)) * 4);
+  if (st != DSA_OK) return st;
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("max_seqs", t.max_seqs);
+  dsa::call_param("num_pages", np);
+  dsa::call_variant("one cluster: plan and take");
+  cudaError_t e = timed_launch("cache_reserve", ctx.stream, [&] {
+    return dsa::launch_cache_reserve(t, log2_of(pages->page_size), np, add, result, static_cast<int32_t*>(workspace),
+                                     ctx);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_reserve: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, const int32_t* src,
+                            const int32_t* dst, int64_t n, int32_t* result, void* workspace, size_t ws_bytes,
+                            void* stream) try {
+  const char* fn = "dsa_cache_fork";
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa::PageTableView t;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st == DSA_OK) st = table_view(fn, pages, &t);
+  if (st != DSA_OK) return st;
+  if (pages->num_pages != cache->num_pages || pages->page_size != cache->page_size)
+    return fail(DSA_ERR_INVALID_ARG, "%s: the page table is another cache's (pages or page size differ)", fn);
+  if (n < 0 || n > t.max_seqs)
+    return fail(DSA_ERR_INVALID_ARG, "%s: n=%lld children out of range (0..max_seqs=%d)", fn, (long long)n, t.max_seqs);
+  if (!result || !aligned4(result)) return fail(DSA_ERR_INVALID_ARG, "%s: result must be a 4-byte aligned device word", fn);
+  if (n > 0 && (!src || !dst || !aligned4(src) || !aligned4(dst)))
+    return fail(DSA_ERR_INVALID_ARG, "%s: src and dst must be 4-byte aligned device arrays", fn);
+  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(dsa::fork_ws_words(n, t.max_seqs)) * 4);
+  if (st != DSA_OK) return st;
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("n", n);
+  dsa::call_param("max_seqs", t.max_seqs);
+  dsa::call_variant("one cluster plans, then a block per 32 KB of a last page");
+  cudaError_t e = timed_launch("cache_fork", ctx.stream, [&] {
+    return dsa::launch_cache_fork(c, t, src, dst, static_cast<int>(n), result, static_cast<int32_t*>(workspace), ctx);
+  }, n > 0 ? 2 : 1);
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_fork: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+dsa_status_t dsa_cache_free(const dsa_page_table_t* pages, const int32_t* seqs, int64_t n, void* stream) try {
+  const char* fn = "dsa_cache_free";
+  const dsa::CallScope scope(fn);
+  dsa::PageTableView t;
+  dsa_status_t st = table_view(fn, pages, &t);
+  if (st != DSA_OK) return st;
+  if (n < 0 || n > kIntMax) return fail(DSA_ERR_INVALID_ARG, "%s: n=%lld out of range", fn, (long long)n);
+  if (n == 0) return DSA_OK;
+  if (!seqs || !aligned4(seqs)) return fail(DSA_ERR_INVALID_ARG, "%s: seqs must be a 4-byte aligned device array", fn);
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("n", n);
+  dsa::call_variant("a block per sequence");
+  cudaError_t e = timed_launch("cache_free", ctx.stream, [&] {
+    return dsa::launch_cache_free(t, log2_of(pages->page_size), static_cast<int>(pages->num_pages), seqs,
+                                  static_cast<int>(n), ctx);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_free: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, int32_t* result,
+                               void* workspace, size_t ws_bytes, void* stream) try {
+  const char* fn = "dsa_cache_compact";
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa::PageTableView t;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st == DSA_OK) st = table_view(fn, pages, &t);
+  if (st != DSA_OK) return st;
+  if (pages->num_pages != cache->num_pages || pages->page_size != cache->page_size)
+    return fail(DSA_ERR_INVALID_ARG, "%s: the page table is another cache's (pages or page size differ)", fn);
+  if (!result || !aligned4(result)) return fail(DSA_ERR_INVALID_ARG, "%s: result must be 4-byte aligned device words", fn);
+  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(dsa::compact_ws_words(c.num_pages)) * 4);
+  if (st != DSA_OK) return st;
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("num_pages", c.num_pages);
+  dsa::call_param("max_seqs", t.max_seqs);
+  dsa::call_variant("one cluster plans, then copies in 32 KB slices");
+  cudaError_t e = timed_launch("cache_compact", ctx.stream, [&] {
+    return dsa::launch_cache_compact(c, t, result, static_cast<int32_t*>(workspace), ctx);
+  }, 2);
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_compact: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size) {
+  if (rows < 1 || max_pages < 1 || !page_size_ok(page_size) || max_pages > kIntMax / page_size) return 0;
+  const int64_t ld = paged_score_ld(max_pages, page_size);
+  int64_t r = kPagedScratch / ld;
+  r = r < kPagedMinRows ? kPagedMinRows : r;
+  r = r < rows ? r : rows;
+  return round_up(static_cast<size_t>(r * ld) * 4, 256);
+}
+
+dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
+                                  const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,
+                                  size_t ws_bytes, void* stream) try {
+  const char* fn = "dsa_paged_index_topk";
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa::BatchView b;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st == DSA_OK) st = batch_view(fn, batch, cache->page_size, &b);
+  if (st != DSA_OK) return st;
+  if (topk < 1) return fail(DSA_ERR_INVALID_ARG, "%s: topk=%d must be >= 1", fn, topk);
+  if (Hi < 1) return fail(DSA_ERR_INVALID_ARG, "%s: Hi=%d must be >= 1", fn, Hi);
+  if (Di != kDi) return fail(DSA_ERR_UNSUPPORTED, "%s: Di=%d unsupported (kernels implement Di=64)", fn, Di);
+  if (Hi > kMaxHi) return fail(DSA_ERR_UNSUPPORTED, "%s: Hi=%d unsupported (max %d)", fn, Hi, kMaxHi);
+  if (topk > kMaxTopk) return fail(DSA_ERR_UNSUPPORTED, "%s: topk=%d unsupported (max %d)", fn, topk, kMaxTopk);
+  if (b.rows == 0) return DSA_OK;
+  if (!q_idx || !w || !pool_idx) return fail(DSA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!aligned16(q_idx) || !aligned4(w) || !aligned4(pool_idx))
+    return fail(DSA_ERR_INVALID_ARG, "%s: q_idx must be 16-byte aligned, w and pool_idx 4-byte aligned", fn);
+  const int64_t ld = paged_score_ld(b.max_pages, cache->page_size);
+  const int64_t least = b.rows < kPagedMinRows ? b.rows : kPagedMinRows;
+  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(least * ld) * 4);
+  if (st != DSA_OK) return st;
+  int64_t pass = static_cast<int64_t>(ws_bytes / 4) / ld;
+  if (pass > kPagedPassMax / ld) pass = kPagedPassMax / ld < least ? least : kPagedPassMax / ld;
+  if (pass > b.rows) pass = b.rows;
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("rows", b.rows);
+  dsa::call_param("batch", b.batch);
+  dsa::call_param("Hi", Hi);
+  dsa::call_param("topk", topk);
+  dsa::call_param("rows_per_pass", pass);
+  dsa::call_variant("scores from the pages, then a row's top-k per cluster");
+  float* scores = static_cast<float*>(workspace);
+  for (int64_t r = 0; r < b.rows; r += pass) {
+    const int64_t n = b.rows - r < pass ? b.rows - r : pass;
+    cudaError_t e = timed_launch("paged_scores", ctx.stream, [&] {
+      return dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, scores, ld, ctx);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: scores launch");
+    e = timed_launch("paged_select", ctx.stream, [&] {
+      return dsa::launch_paged_select(b, c.shift, r, n, scores, ld, topk, pool_idx, ctx);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: selection launch");
+  }
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+dsa_status_t dsa_paged_sparse_attn_fwd(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q,
+                                       const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o,
+                                       float* lse, void* stream) try {
+  const char* fn = "dsa_paged_sparse_attn_fwd";
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa::BatchView b;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st == DSA_OK) st = batch_view(fn, batch, cache->page_size, &b);
+  if (st == DSA_OK) st = check_attn_args(fn, 1, Hq, D, topk);
+  if (st != DSA_OK) return st;
+  if (b.rows == 0) return DSA_OK;
+  if (!q || !pool_idx || !o || !lse) return fail(DSA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!aligned16(q) || !aligned16(o) || !aligned4(pool_idx) || !aligned4(lse))
+    return fail(DSA_ERR_INVALID_ARG, "%s: q and o must be 16-byte aligned, pool_idx and lse 4-byte aligned", fn);
+  if (!(scale > 0.f)) scale = 1.0f / sqrtf(static_cast<float>(D));
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("rows", b.rows);
+  dsa::call_param("batch", b.batch);
+  dsa::call_param("topk", topk);
+  dsa::call_variant("a cluster per row: cp.async gather through the block table, mma.sync, online softmax");
+  cudaError_t e = timed_launch("paged_attn", ctx.stream, [&] {
+    return dsa::launch_paged_attn(c, b, q, pool_idx, topk, scale, o, lse, ctx);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_sparse_attn_fwd: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
 
 }  // extern "C"

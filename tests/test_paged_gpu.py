@@ -1,0 +1,861 @@
+"""The layer over a paged cache on the GPU, against a plain model in 64-bit CPU arithmetic."""
+import math
+
+import numpy as np
+import pytest
+
+from tests._paged import (D, DI, HQ, Model, attention_bounds, pool_mean, random_selection, split_hi_lo, top_pools)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import long_context_sparse_index_gb300 as dsa
+DEV = "cuda"
+
+
+def same_bits(a, b):
+    return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+
+def check_cache(cache, m):
+    for n in ("k", "v", "k_idx", "khat"):
+        assert same_bits(getattr(cache, n).cpu(), getattr(m, n)), n
+
+
+# new and old tokens of the sequences: one token, a chunk, ends inside pages and pools, an idle sequence, first tokens
+LAYOUTS = {
+    "one": ([1], [0]),
+    "second": ([1], [1]),
+    "decode": ([1, 1, 1, 1, 1], [3, 16, 15, 62, 131]),
+    "idle": ([1, 0, 2, 0, 7], [30, 5, 0, 0, 9]),
+    "chunks": ([37, 130, 5], [0, 61, 3]),
+    "pool_ends": ([2, 3, 4, 5, 6], [2, 1, 3, 7, 14]),
+}
+
+
+# --------------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_append_bit_exact(layout, page):
+    m = Model(*LAYOUTS[layout], page, seed=1)
+    cache, batch = m.to_gpu(dsa)
+    k, v, ki = m.fill(m.T, D), m.fill(m.T, D), m.fill(m.T, DI)
+    dsa.dsa_cache_append(cache, batch, k.to(DEV), v.to(DEV), ki.to(DEV))
+    dsa.dsa_sync_status()
+    m.append(k, v, ki)
+    check_cache(cache, m)
+
+
+def test_append_strided_rows_and_pages_and_padding():
+    """Rows out of a fused projection, pages of layers that alternate, and rows behind the last sequence."""
+    m = Model([5, 40, 1], [2, 7, 100], 32, seed=2, pages_apart=72)
+    cache, batch = m.to_gpu(dsa)
+    assert cache.k.stride(0) == 32 * D + 72
+    fused = m.fill(m.T + 9, 2 * D + DI + 16)
+    gpu = fused.to(DEV)
+    k, v, ki = fused[:, 8:8 + D], fused[:, 8 + D:8 + 2 * D], fused[:, 16 + 2 * D:]
+    dsa.dsa_cache_append(cache, batch, gpu[:, 8:8 + D], gpu[:, 8 + D:8 + 2 * D], gpu[:, 16 + 2 * D:])
+    dsa.dsa_sync_status()
+    m.append(k, v, ki)
+    check_cache(cache, m)
+
+
+def test_append_again_after_a_rejected_draft():
+    """Tokens written again at earlier positions replace the slots and the pooled keys that depend on them."""
+    m = Model([7], [6], 16, seed=3)
+    cache, batch = m.to_gpu(dsa)
+    draft = [m.fill(7, d) for d in (D, D, DI)]
+    dsa.dsa_cache_append(cache, batch, *[t.to(DEV) for t in draft])
+    m.append(*draft)
+    m.new, m.lens, m.cu, m.T, m.old = [3], [11], [0, 3], 3, [8]
+    again = [m.fill(3, d) for d in (D, D, DI)]
+    batch = dsa.PagedBatch(m.table.to(DEV), torch.tensor([11], dtype=torch.int32, device=DEV),
+                           torch.tensor([0, 3], dtype=torch.int32, device=DEV))
+    dsa.dsa_cache_append(cache, batch, *[t.to(DEV) for t in again])
+    dsa.dsa_sync_status()
+    m.append(*again)
+    check_cache(cache, m)
+
+
+def test_append_of_infinities_and_nan():
+    """Rows are copied whatever they hold; a pool with an infinity has hi = inf and lo = inf - inf."""
+    m = Model([4], [0], 16, seed=4)
+    cache, batch = m.to_gpu(dsa)
+    k, v, ki = m.fill(4, D), m.fill(4, D), m.fill(4, DI)
+    k[1, 5], v[2, 7], ki[0, 3], ki[1, 9] = math.inf, math.nan, math.inf, -math.inf
+    dsa.dsa_cache_append(cache, batch, k.to(DEV), v.to(DEV), ki.to(DEV))
+    dsa.dsa_sync_status()
+    m.append(k, v, ki)
+    for n in ("k", "k_idx", "v", "khat"):
+        torch.testing.assert_close(getattr(cache, n).cpu(), getattr(m, n), rtol=0, atol=0, equal_nan=True)
+
+
+# --------------------------------------------------------------------------- pages
+
+class Pages:
+    """The bookkeeping as plain Python."""
+
+    def __init__(self, lens, page, num_pages, width, seed):
+        rng = np.random.default_rng(seed)
+        order = rng.permutation(num_pages)
+        self.page, self.width = page, width
+        self.lens = list(lens)
+        self.table = np.full((len(lens), width), -1, np.int32)
+        self.count = np.zeros(num_pages, np.int32)
+        at = 0
+        for s, n in enumerate(lens):
+            for x in range(-(-n // page)):
+                self.table[s, x] = order[at]
+                self.count[order[at]] += 1
+                at += 1
+
+    def free_pages(self):
+        return [int(p) for p in np.nonzero(self.count == 0)[0]]
+
+    def reserve(self, add):
+        free, need = self.free_pages(), []
+        for s, a in enumerate(add):
+            need.append(-(-(self.lens[s] + a) // self.page) - -(-self.lens[s] // self.page))
+        if sum(need) > len(free):
+            return len(free) - sum(need)
+        for s, a in enumerate(add):
+            have = -(-self.lens[s] // self.page)
+            for x in range(need[s]):
+                p = free.pop(0)
+                self.table[s, have + x] = p
+                self.count[p] = 1
+            self.lens[s] += a
+        return sum(need)
+
+    def fork(self, src, dst):
+        """(pages taken, [(from, to)])"""
+        free = self.free_pages()
+        need = sum(1 for s in src if self.lens[s] % self.page)
+        if need > len(free):
+            return len(free) - need, []
+        moves, lens = [], list(self.lens)
+        for s, d in zip(src, dst):
+            full, part = lens[s] // self.page, lens[s] % self.page
+            self.table[d] = -1
+            for x in range(full):
+                self.table[d, x] = self.table[s, x]
+                self.count[self.table[s, x]] += 1
+            if part:
+                p = free.pop(0)
+                self.table[d, full] = p
+                self.count[p] = 1
+                moves.append((int(self.table[s, full]), p))
+            self.lens[d] = lens[s]
+        return need, moves
+
+    def free(self, seqs):
+        for s in seqs:
+            for x in range(-(-self.lens[s] // self.page)):
+                self.count[self.table[s, x]] -= 1
+                self.table[s, x] = -1
+            self.lens[s] = 0
+
+    def compact(self):
+        used = int((self.count != 0).sum())
+        high = [p for p in range(used, len(self.count)) if self.count[p]]
+        hole = [p for p in range(used) if not self.count[p]]
+        to = dict(zip(high, hole))
+        for p, q in to.items():
+            self.count[q], self.count[p] = self.count[p], 0
+        for s in range(self.table.shape[0]):
+            for x in range(self.width):
+                self.table[s, x] = to.get(int(self.table[s, x]), self.table[s, x])
+        return used, list(to.items())
+
+    def to_gpu(self):
+        return dsa.PageTable(torch.from_numpy(self.table.copy()).to(DEV),
+                             torch.tensor(self.lens, dtype=torch.int32, device=DEV),
+                             torch.from_numpy(self.count.copy()).to(DEV))
+
+    def check(self, t):
+        assert np.array_equal(t.page_count.cpu().numpy(), self.count)
+        assert t.seq_lens.tolist() == self.lens
+        assert np.array_equal(t.block_table.cpu().numpy(), self.table)
+
+
+def random_cache(num_pages, page, seed=5, apart=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def new(tokens, d):
+        n = tokens * d
+        x = torch.randn(num_pages, n + apart, generator=g, device=DEV).to(torch.bfloat16)
+        return x.as_strided((num_pages, tokens, d), (n + apart, d, 1))
+    return dsa.PagedCache(new(page, D), new(page, D), new(page, DI), new(page // 4, D))
+
+
+def buffers(cache):
+    return [getattr(cache, n) for n in ("k", "v", "k_idx", "khat")]
+
+
+def i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("page,apart", [(16, 0), (64, 40), (256, 0), (1024, 8)])
+def test_copy_pages(page, apart):
+    cache = random_cache(11, page, apart=apart)
+    want = [b.clone() for b in buffers(cache)]
+    src, dst = [3, 3, 0, 10, 7], [1, 4, 2, 9, 7]
+    dsa.dsa_cache_copy_pages(cache, i32(src), i32(dst))
+    dsa.dsa_sync_status()
+    for b, w in zip(buffers(cache), want):
+        w[dst] = w[src]
+        assert same_bits(b, w)
+
+
+def test_copy_of_no_pages_does_nothing():
+    cache = random_cache(2, 16)
+    dsa.dsa_cache_copy_pages(cache, i32([]), i32([]))
+    dsa.dsa_sync_status()
+
+
+def test_copy_of_a_page_that_is_none_is_reported():
+    cache = random_cache(4, 16)
+    want = [b.clone() for b in buffers(cache)]
+    dsa.dsa_cache_copy_pages(cache, i32([0, 4, 1]), i32([2, 1, -1]))
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_sync_status()
+    assert e.value.status == dsa.DSA_ERR_INTERNAL
+    dsa.dsa_clear_status()
+    for b, w in zip(buffers(cache), want):
+        w[2] = w[0]
+        assert same_bits(b, w)
+
+
+@pytest.mark.parametrize("num_pages", [40, 255, 8200, 70001])
+@pytest.mark.parametrize("page", [16, 128])
+def test_reserve(num_pages, page):
+    p = Pages([5 * page, 0, 3, page, 2 * page - 1], page, num_pages, 12, seed=num_pages)
+    t, cache = p.to_gpu(), random_cache(num_pages, 16) if page == 16 else dsa.PagedCache.empty(num_pages, page)
+    for add in ([0, 0, 0, 0, 0], [1, 1, 1, 1, 1], [0, 4 * page, 2, 0, page + 1], [page, 0, 0, 0, 0]):
+        got = dsa.dsa_cache_reserve(cache, t, i32(add))
+        dsa.dsa_sync_status()
+        assert got.item() == p.reserve(add)
+        p.check(t)
+
+
+def test_reserve_without_room_changes_nothing():
+    p = Pages([30, 64], 16, 8, 20, seed=1)
+    t, cache = p.to_gpu(), random_cache(8, 16)
+    assert dsa.dsa_cache_reserve(cache, t, i32([3, 33])).item() == p.reserve([3, 33]) == -2
+    p.check(t)
+    # a length the table cannot hold, and a negative one
+    for add in ([320, 0], [0, -1]):
+        assert dsa.dsa_cache_reserve(cache, t, i32(add)).item() == -2 ** 31
+        with pytest.raises(dsa.DsaError):
+            dsa.dsa_sync_status()
+        dsa.dsa_clear_status()
+        p.check(t)
+
+
+def test_reserve_of_many_sequences():
+    """More sequences than a block has threads."""
+    lens = [(7 * s) % 40 for s in range(2500)]
+    p = Pages(lens, 16, 9000, 6, seed=9)
+    t, cache = p.to_gpu(), random_cache(9000, 16)
+    add = [(11 * s) % 23 for s in range(2500)]
+    assert dsa.dsa_cache_reserve(cache, t, i32(add)).item() == p.reserve(add)
+    dsa.dsa_sync_status()
+    p.check(t)
+
+
+def check_moves(cache, before, moves):
+    for b, w in zip(buffers(cache), before):
+        for s, d in moves:
+            w[d] = w[s]
+        assert same_bits(b, w)
+
+
+@pytest.mark.parametrize("page,apart", [(16, 0), (64, 8), (1024, 0)])
+@pytest.mark.parametrize("lens", [[1], [40, 16, 0, 33], [2048, 1000, 1]])
+def test_fork_then_free(lens, page, apart):
+    """Children of the same parent, of a parent that ends with a page, of an empty one."""
+    n = len(lens)
+    p = Pages(lens + [0] * (2 * n + 1), page, 300, -(-max(lens) // page) + 2, seed=3)
+    cache = random_cache(300, page, apart=apart)
+    t, before = p.to_gpu(), [b.clone() for b in buffers(cache)]
+    src, dst = list(range(n)) + list(range(n)), list(range(n + 1, 3 * n + 1))
+    got = dsa.dsa_cache_fork(cache, t, i32(src), i32(dst))
+    dsa.dsa_sync_status()
+    taken, moves = p.fork(src, dst)
+    assert got.item() == taken
+    p.check(t)
+    check_moves(cache, before, moves)
+    gone = [dst[0], 0, dst[-1], dst[0]]  # one of them twice
+    dsa.dsa_cache_free(cache, t, i32(gone))
+    dsa.dsa_sync_status()
+    p.free(gone)
+    p.check(t)
+
+
+def test_fork_without_room_and_bad_requests_change_nothing():
+    p = Pages([20, 36, 0, 0, 0], 16, 6, 5, seed=4)
+    cache = random_cache(6, 16)
+    t, before = p.to_gpu(), [b.clone() for b in buffers(cache)]
+    assert dsa.dsa_cache_fork(cache, t, i32([0, 1]), i32([2, 3])).item() == -1  # 5 of 6 pages are used
+    dsa.dsa_sync_status()
+    p.check(t)
+    # a child twice, a child that lives, rows that do not exist
+    for src, dst in (([0, 1], [2, 2]), ([0], [1]), ([5], [2]), ([0], [5]), ([-1], [2])):
+        assert dsa.dsa_cache_fork(cache, t, i32(src), i32(dst)).item() == -2 ** 31, (src, dst)
+        with pytest.raises(dsa.DsaError):
+            dsa.dsa_sync_status()
+        dsa.dsa_clear_status()
+        p.check(t)
+    check_moves(cache, before, [])
+    assert dsa.dsa_cache_fork(cache, t, i32([]), i32([])).item() == 0
+
+
+def test_free_of_rows_that_do_not_exist_is_reported():
+    p = Pages([20, 36], 16, 6, 5, seed=4)
+    t, cache = p.to_gpu(), random_cache(6, 16)
+    dsa.dsa_cache_free(cache, t, i32([1, 2, -1]))
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_sync_status()
+    dsa.dsa_clear_status()
+    p.free([1])
+    p.check(t)
+
+
+@pytest.mark.parametrize("num_pages", [1, 7, 32, 257, 8192, 9001])
+@pytest.mark.parametrize("fill", [0.0, 0.3, 0.9, 1.0])
+def test_compact(num_pages, fill):
+    rng = np.random.default_rng(num_pages)
+    lens = [16 * int(rng.integers(1, 5)) - int(rng.integers(0, 16)) for _ in range(max(1, num_pages // 2))]
+    while sum(-(-n // 16) for n in lens) > num_pages * fill:
+        lens.pop()
+        if not lens:
+            break
+    p = Pages(lens + [0, 0, 0], 16, num_pages, 6, seed=num_pages)
+    if fill == 1.0:  # sequences of one page fill the rest
+        for q in p.free_pages():
+            p.table = np.vstack([p.table, np.full((1, 6), -1, np.int32)])
+            p.table[-1, 0], p.count[q] = q, 1
+            p.lens.append(16)
+    cache = random_cache(num_pages, 16)
+    t, before = p.to_gpu(), [b.clone() for b in buffers(cache)]
+    got = dsa.dsa_cache_compact(cache, t)
+    dsa.dsa_sync_status()
+    used, moves = p.compact()
+    assert got.tolist() == [used, len(moves)]
+    p.check(t)
+    for b, w in zip(buffers(cache), before):
+        if moves:
+            src, dst = (list(x) for x in zip(*moves))
+            w[dst] = w[src]
+        assert same_bits(b, w)
+    again = dsa.dsa_cache_compact(cache, t)  # nothing left to move
+    assert again.tolist() == [used, 0]
+    p.check(t)
+
+
+def test_compact_shared_pages_and_large_pages():
+    p = Pages([700, 300, 513, 0, 0], 256, 40, 4, seed=8)
+    cache = random_cache(40, 256, apart=16)
+    t = p.to_gpu()
+    dsa.dsa_cache_fork(cache, t, i32([0, 2]), i32([3, 4]))
+    p.fork([0, 2], [3, 4])
+    dsa.dsa_cache_free(cache, t, i32([1]))
+    p.free([1])
+    before = [b.clone() for b in buffers(cache)]
+    dsa.dsa_cache_compact(cache, t)
+    dsa.dsa_sync_status()
+    _, moves = p.compact()
+    p.check(t)
+    check_moves(cache, before, moves)
+
+
+# --------------------------------------------------------------------------- indexer + top-k
+
+def index_inputs(m, Hi, ints=True, seed=7, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    if ints:
+        q = torch.randint(-3, 4, (m.T + pad, Hi, DI), generator=g).to(torch.bfloat16)
+        w = torch.randint(-1, 4, (m.T + pad, Hi), generator=g).float()
+    else:
+        q = torch.randn(m.T + pad, Hi, DI, generator=g).to(torch.bfloat16)
+        w = torch.randn(m.T + pad, Hi, generator=g)
+    return q, w
+
+
+def check_topk(m, q, w, topk, got):
+    scores, _ = m.scores(q, w)
+    got = got.cpu().numpy()
+    for r, b, i in m.rows():
+        want = top_pools(scores[r], topk)
+        assert np.array_equal(got[r], want), (r, b, i, got[r], want)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("Hi,topk", [(1, 1), (3, 5), (16, 8), (17, 30), (32, 512), (64, 3)])
+def test_index_small_bit_exact(layout, page, Hi, topk):
+    """Integer inputs: every sum is exact, ties are many, and the selection is one and the same."""
+    m = Model(*LAYOUTS[layout], page, seed=11, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, Hi)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+    dsa.dsa_sync_status()
+    check_topk(m, q, w, topk, got)
+
+
+@pytest.mark.parametrize("new,old,page,Hi,topk", [
+    ([1], [40000], 64, 8, 512), ([1, 1], [9001, 30003], 16, 32, 100), ([1] * 90, [2000 + 13 * j for j in range(90)], 64, 4, 64),
+    ([3, 9, 1], [20000, 16383, 5000], 256, 16, 2048), ([130], [8191], 64, 8, 512), ([300, 20], [1000, 0], 32, 32, 77),
+    ([1] * 20, [12000 + j for j in range(20)], 1024, 8, 511)])
+def test_index_long_bit_exact(new, old, page, Hi, topk):
+    m = Model(new, old, page, seed=13, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, Hi)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+    dsa.dsa_sync_status()
+    check_topk(m, q, w, topk, got)
+
+
+@pytest.mark.parametrize("case", ["zeros", "two_values", "huge", "one_high", "overflow", "negative"])
+def test_index_ties_and_extreme_scores(case):
+    """All scores equal; nearly all equal; magnitudes near the type's end; one score far above the rest (the bins of
+    equal steps then hold everything else in one); scores that overflow to infinity; only negative scores."""
+    m = Model([1, 1, 2], [30000, 9000, 17001], 64, seed=17, ints=True)
+    q, w = index_inputs(m, 2, seed=18)
+    w = torch.ones_like(w)
+    if case == "zeros":
+        w.zero_()
+    elif case == "two_values":
+        q.zero_()
+        q[:, 0, 0] = 1
+        m.k_idx.fill_(0)
+        m.k_idx.view(-1, 4, DI)[::5, :, 0] = 2
+    elif case == "huge":
+        w *= 1e30
+    elif case == "one_high":
+        m.k_idx.view(-1, DI)[m.slot(0, 12345 // 4 * 4)] *= 2 ** 40
+        q[:, 0, :] = 1
+    elif case == "overflow":
+        w *= 3e37
+    else:
+        w *= -1
+    m.khat = split_hi_lo(pool_mean(m.k_idx.view(-1, 4, DI))).view(m.khat.shape)
+    cache, batch = m.to_gpu(dsa)
+    for topk in (1, 64, 700):
+        got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+        dsa.dsa_sync_status()
+        if case in ("zeros", "two_values", "overflow", "negative"):
+            check_topk(m, q, w, topk, got)
+        else:
+            check_selected(m, q, w, topk, got)
+
+
+def check_selected(m, q, w, topk, got):
+    """Each row is a valid selection, and nothing left out scores more than a kept pool does beyond what the rounding
+    of both allows.  A score's rounding: the pair holds Khat to 2^-18 of it at most (already in the 64-bit scores'
+    operands here, so nothing), 128 products summed in fp32 (2 * 128 * 2^-24, twice for truncating accumulators), Hi
+    more additions."""
+    scores, mag = m.scores(q, w)
+    got = got.cpu().numpy()
+    for r, b, i in m.rows():
+        n, row = i // 4, got[r]
+        k = min(topk, n)
+        assert np.all(row[k:] == -1) and np.all(np.diff(row[:k]) > 0) and (k == 0 or (row[0] >= 0 and row[k - 1] < n))
+        if k == 0 or k == n:
+            continue
+        slack = (2 * 128 + q.shape[1] + 1) * 2.0 ** -24 * mag[r]
+        s = scores[r]
+        kept = torch.zeros(n, dtype=torch.bool)
+        kept[row[:k].astype(np.int64)] = True
+        assert ((s + slack)[kept].min() >= (s - slack)[~kept].max()), (r, b, i)
+
+
+@pytest.mark.parametrize("Hi,topk", [(32, 512), (5, 100)])
+@pytest.mark.parametrize("new,old", [([1, 1, 1], [33000, 4097, 12003]), ([140], [10000])])
+def test_index_real_values(new, old, Hi, topk):
+    m = Model(new, old, 64, seed=19)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, Hi, ints=False)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+    again = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+    dsa.dsa_sync_status()
+    assert torch.equal(got, again)
+    check_selected(m, q, w, topk, got)
+
+
+def test_index_does_not_depend_on_the_workspace_and_leaves_padding():
+    """The least workspace (8 rows at a time) and the recommended one; rows behind the last sequence stay."""
+    m = Model([30, 1, 8], [3000, 777, 5000], 64, seed=23, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 8, pad=6)
+    q, w = q.to(DEV), w.to(DEV)
+    out = torch.full((m.T + 6, 50), 77, dtype=torch.int32, device=DEV)
+    full = dsa.dsa_paged_index_topk(cache, batch, q, w, 50, pool_idx=out.clone())
+    least = torch.empty(8 * m.width * 16 * 4, dtype=torch.uint8, device=DEV)
+    small = dsa.dsa_paged_index_topk(cache, batch, q, w, 50, pool_idx=out.clone(), workspace=least)
+    dsa.dsa_sync_status()
+    assert torch.equal(full, small)
+    assert torch.all(full[m.T:] == 77)
+    check_topk(m, q.cpu(), w.cpu(), 50, full)
+
+
+def test_index_equals_the_contiguous_call():
+    """A whole prompt as one chunk: the same pools as dsa_index_topk."""
+    m = Model([3001], [0], 64, seed=29, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    k, v, ki = m.fill(m.T, D), m.fill(m.T, D), m.fill(m.T, DI)
+    dsa.dsa_cache_append(cache, batch, k.to(DEV), v.to(DEV), ki.to(DEV))
+    q, w = index_inputs(m, 8)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 64)
+    want = dsa.dsa_index_topk(q.to(DEV), ki.to(DEV), w.to(DEV), chunk=256, topk=64)
+    dsa.dsa_sync_status()
+    assert torch.equal(got, want)
+
+
+# --------------------------------------------------------------------------- attention
+
+def check_attention(m, q, sel, scale, o, lse):
+    ro, rl, av, mag = m.attention(q, sel, scale)
+    bo, bl = attention_bounds(ro, av, rl, mag)
+    T = m.T
+    err = (o[:T].cpu().double() - ro).abs()
+    assert torch.all(err <= bo), (err / bo).max()
+    err = (lse[:T].cpu().double() - rl).abs()
+    assert torch.all(err <= bl), (err / bl).max()
+
+
+@pytest.mark.parametrize("page", [16, 64, 1024])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("topk", [1, 15, 16, 64])
+def test_attention_small(layout, page, topk):
+    m = Model(*LAYOUTS[layout], page, seed=31)
+    cache, batch = m.to_gpu(dsa)
+    q, sel = m.fill(m.T, HQ, D), random_selection(m, topk, seed=1)
+    o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV))
+    dsa.dsa_sync_status()
+    check_attention(m, q, sel, 1 / math.sqrt(D), o, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 38, 39, 152, 153, 400])
+@pytest.mark.parametrize("topk", [512, 300])
+def test_attention_every_split(rows, topk):
+    """Every number of CTAs per row; rows that keep fewer pools than the others leave CTAs without keys."""
+    m = Model([1] * rows, [50 + 37 * j % 3000 for j in range(rows)], 64, seed=37)
+    cache, batch = m.to_gpu(dsa)
+    q, sel = m.fill(m.T, HQ, D), random_selection(m, topk, seed=rows, fewer=True)
+    o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV))
+    o2, lse2 = dsa.dsa_paged_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV))
+    dsa.dsa_sync_status()
+    assert same_bits(o, o2) and torch.equal(lse, lse2)
+    check_attention(m, q, sel, 1 / math.sqrt(D), o, lse)
+
+
+@pytest.mark.parametrize("new,old,topk", [([1], [9000], 2048), ([3], [70000], 1000), ([200], [8200], 2048)])
+def test_attention_long(new, old, topk):
+    m = Model(new, old, 128, seed=41, pages_apart=24)
+    cache, batch = m.to_gpu(dsa)
+    q, sel = m.fill(m.T, HQ, D) * 2, random_selection(m, topk, seed=2)
+    o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV), scale=0.1)
+    dsa.dsa_sync_status()
+    check_attention(m, q, sel, 0.1, o, lse)
+
+
+@pytest.mark.parametrize("rows", [3, 100, 500])
+def test_attention_reads_nothing_it_does_not_attend_to(rows):
+    """NaN and infinities in every slot that no row attends to, positions behind the last token among them."""
+    m = Model([1] * rows, [40 + 3 * j for j in range(rows)], 16, seed=43)
+    sel = random_selection(m, 8, seed=3)
+    seen = torch.zeros(m.pages * m.page, dtype=torch.bool)
+    for r, b, i in m.rows():
+        for t in [4 * p + e for p in sel[r].tolist() if p >= 0 for e in range(4)] + list(range(i // 4 * 4, i + 1)):
+            seen[m.slot(b, t)] = True
+    m.k.view(-1, D)[~seen] = math.nan
+    m.v.view(-1, D)[~seen] = math.inf
+    cache, batch = m.to_gpu(dsa)
+    q = m.fill(m.T, HQ, D)
+    o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV))
+    dsa.dsa_sync_status()
+    check_attention(m, q, sel, 1 / math.sqrt(D), o, lse)
+
+
+@pytest.mark.parametrize("rows", [2, 200])
+def test_attention_leaves_padding_and_given_outputs(rows):
+    m = Model([1] * rows, [100] * rows, 32, seed=47)
+    cache, batch = m.to_gpu(dsa)
+    q = m.fill(m.T + 5, HQ, D)
+    sel = torch.cat([random_selection(m, 16, seed=4), torch.zeros(5, 16, dtype=torch.int32)])
+    o = torch.full((m.T + 5, HQ, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((m.T + 5, HQ), 5.0, device=DEV)
+    dsa.dsa_paged_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV), o=o, lse=lse)
+    dsa.dsa_sync_status()
+    assert torch.all(o[m.T:] == 3.0) and torch.all(lse[m.T:] == 5.0)
+    check_attention(m, q, sel, 1 / math.sqrt(D), o, lse)
+
+
+@pytest.mark.parametrize("what", ["page", "page_high", "length", "offsets", "selection", "order"])
+@pytest.mark.parametrize("rows", [4, 300])
+def test_what_is_out_of_range_is_reported_and_not_followed(what, rows):
+    """A page number that is none, a length past the table, offsets against lengths, a pool that is not eligible: the
+    status says so, the other rows are right."""
+    m = Model([1] * rows, [200 + j % 50 for j in range(rows)], 16, seed=53)
+    bad = 2
+    sel = random_selection(m, 16, seed=5)
+    q = m.fill(m.T, HQ, D)
+    good = Model([1] * rows, [200 + j % 50 for j in range(rows)], 16, seed=53)
+    if what == "page":
+        m.table[bad, int(sel[bad, 0]) // 4] = -1
+    elif what == "page_high":
+        m.table[bad, int(sel[bad, 0]) // 4] = m.pages
+    elif what == "length":
+        m.lens[bad] = m.width * 16 + 1
+    elif what == "offsets":
+        m.lens[bad] = 0
+    elif what == "selection":
+        sel[bad, 15] = (m.lens[bad] - 1) // 4
+    else:
+        sel[bad, 1] = sel[bad, 0]
+    cache, batch = m.to_gpu(dsa)
+    o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV))
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_sync_status()
+    assert e.value.status == dsa.DSA_ERR_INTERNAL
+    dsa.dsa_clear_status()
+    ok = [r for r in range(rows) if r != bad]
+    sel[bad] = -1
+    ro, rl, av, mag = good.attention(q, sel, 1 / math.sqrt(D))
+    bo, bl = attention_bounds(ro, av, rl, mag)
+    assert torch.all((o.cpu().double() - ro).abs()[ok] <= bo[ok])
+    assert torch.all((lse.cpu().double() - rl).abs()[ok] <= bl[ok])
+    if what in ("page", "page_high", "length", "offsets"):  # the indexer and the append follow the same numbers
+        qi, w = index_inputs(m, 4)
+        if what in ("page", "page_high"):
+            m.table[bad] = -1 if what == "page" else m.pages
+            batch.block_table.copy_(m.table)
+        dsa.dsa_paged_index_topk(cache, batch, qi.to(DEV), w.to(DEV), 16)
+        with pytest.raises(dsa.DsaError):
+            dsa.dsa_sync_status()
+        dsa.dsa_clear_status()
+        dsa.dsa_cache_append(cache, batch, *[m.fill(m.T, d).to(DEV) for d in (D, D, DI)])
+        with pytest.raises(dsa.DsaError):
+            dsa.dsa_sync_status()
+        dsa.dsa_clear_status()
+
+
+# --------------------------------------------------------------------------- together
+
+def test_prompts_in_chunks_then_tokens_with_forks_and_compaction():
+    """As a server runs it: prompts arrive in chunks, tokens follow one by one, sequences are forked and freed, the
+    cache is compacted; every step's selection and attention are those of the contiguous calls on the same tokens."""
+    page, topk, Hi = 16, 24, 4
+    cache = random_cache(120, page)
+    t = dsa.PageTable.empty(cache, max_seqs=4, max_pages=20)
+    g = torch.Generator().manual_seed(3)
+
+    def tokens(n):
+        k, v = (torch.randn(n, D, generator=g).to(torch.bfloat16) for _ in range(2))
+        ki = torch.randint(-3, 4, (n, DI), generator=g).to(torch.bfloat16)
+        qi = torch.randint(-3, 4, (n, Hi, DI), generator=g).to(torch.bfloat16)
+        w = torch.randint(0, 4, (n, Hi), generator=g).float()
+        return [x.to(DEV) for x in (k, v, ki, qi, w, torch.randn(n, HQ, D, generator=g).to(torch.bfloat16))]
+
+    hist = {s: None for s in range(4)}
+
+    def step(adds):
+        add = [adds.get(s, 0) for s in range(4)]
+        assert dsa.dsa_cache_reserve(cache, t, i32(add)).item() >= 0
+        cu = i32(np.concatenate([[0], np.cumsum(add)]))
+        new = tokens(sum(add))
+        batch = dsa.PagedBatch(t.block_table, t.seq_lens, cu)
+        dsa.dsa_cache_append(cache, batch, *new[:3])
+        pool_idx = dsa.dsa_paged_index_topk(cache, batch, new[3], new[4], topk)
+        o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, new[5], pool_idx)
+        dsa.dsa_sync_status()
+        at = 0
+        for s, n in enumerate(add):
+            if n == 0:
+                continue
+            mine = [x[at:at + n] for x in new]
+            hist[s] = mine if hist[s] is None else [torch.cat(p) for p in zip(hist[s], mine)]
+            k, v, ki, qi, w, q = hist[s]
+            S = k.shape[0]
+            want = dsa.dsa_index_topk(qi, ki, w, chunk=64, topk=topk)
+            assert torch.equal(pool_idx[at:at + n], want[S - n:])
+            wo, wl = dsa.dsa_sparse_attn_fwd(q, k, v, want)
+            torch.testing.assert_close(o[at:at + n].float(), wo[S - n:].float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+            torch.testing.assert_close(lse[at:at + n], wl[S - n:], rtol=1e-5, atol=1e-5)
+            at += n
+
+    step({0: 50, 1: 3})
+    step({0: 61, 1: 17})
+    for _ in range(6):
+        step({0: 1, 1: 1})
+    dsa.dsa_cache_fork(cache, t, i32([0, 0]), i32([2, 3]))
+    hist[2] = hist[3] = hist[0]
+    for _ in range(9):
+        step({0: 1, 1: 1, 2: 1, 3: 1})
+    dsa.dsa_cache_free(cache, t, i32([0, 1]))
+    hist[0] = hist[1] = None
+    used, moved = dsa.dsa_cache_compact(cache, t).tolist()
+    assert used == int((t.page_count != 0).sum()) and torch.all(t.page_count[:used] > 0)
+    for _ in range(5):
+        step({2: 1, 3: 2})
+    step({0: 30, 2: 5, 3: 1})
+    dsa.dsa_cache_free(cache, t, i32([0, 2, 3]))
+    assert torch.all(t.page_count == 0) and torch.all(t.block_table == -1) and torch.all(t.seq_lens == 0)
+
+
+def test_decoding_step_in_a_replayed_graph():
+    """reserve, append, indexer and attention captured once and replayed with new tokens and growing lengths; two
+    graphs share one workspace."""
+    m = Model([1] * 5, [20, 333, 64, 63, 100], 16, seed=59, ints=True, spare=40, width_extra=4)
+    cache, batch = m.to_gpu(dsa)
+    B, Hi, topk = 5, 8, 16
+    lens0 = torch.tensor(m.old, dtype=torch.int32, device=DEV)
+    count = torch.zeros(m.pages, dtype=torch.int32)
+    table = m.table.clone()
+    for b, n in enumerate(m.old):
+        table[b, -(-n // 16):] = -1
+    for p in table.flatten().tolist():
+        if p >= 0:
+            count[p] += 1
+    t = dsa.PageTable(table.to(DEV), lens0.clone(), count.to(DEV))
+    cu = i32(range(B + 1))
+    batch = dsa.PagedBatch(t.block_table, t.seq_lens, cu)
+    k, v, ki = (torch.empty(B, d, dtype=torch.bfloat16, device=DEV) for d in (D, D, DI))
+    qi = torch.empty(B, Hi, DI, dtype=torch.bfloat16, device=DEV)
+    w, q = torch.empty(B, Hi, device=DEV), torch.empty(B, HQ, D, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(max(dsa.paged_index_topk_workspace_size(B, t.max_pages, 16),
+                         dsa.cache_workspace_size(m.pages, B)), dtype=torch.uint8, device=DEV)
+    outs = [(torch.empty(B, topk, dtype=torch.int32, device=DEV), torch.empty_like(q),
+             torch.empty(B, HQ, device=DEV), i32([0])) for _ in range(2)]
+    one = i32([1] * B)
+
+    def step(out):
+        dsa.dsa_cache_reserve(cache, t, one, result=out[3], workspace=ws)
+        dsa.dsa_cache_append(cache, batch, k, v, ki)
+        dsa.dsa_paged_index_topk(cache, batch, qi, w, topk, pool_idx=out[0], workspace=ws)
+        dsa.dsa_paged_sparse_attn_fwd(cache, batch, q, out[0], o=out[1], lse=out[2])
+
+    keep = [x.clone() for x in (t.block_table, t.seq_lens, t.page_count)]
+    for x in (k, v, ki, qi, w, q):
+        x.zero_()
+    step(outs[0])  # warm-up
+    torch.cuda.synchronize()
+    for x, y in zip((t.block_table, t.seq_lens, t.page_count), keep):
+        x.copy_(y)
+    graphs = []
+    for out in outs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            step(out)
+        graphs.append(gr)
+    for it in range(24):
+        new = [m.fill(B, D), m.fill(B, D), m.fill(B, DI), m.fill(B, Hi, DI), m.fill(B, Hi).float().abs(), m.fill(B, HQ, D)]
+        for dst, src in zip((k, v, ki, qi, w, q), new):
+            dst.copy_(src)
+        graphs[it % 2].replay()
+        dsa.dsa_sync_status()
+        m.table = t.block_table.cpu()
+        m.append(*new[:3])
+        out = outs[it % 2]
+        check_topk(m, new[3], new[4], topk, out[0])
+        check_attention(m, new[5], out[0].cpu(), 1 / math.sqrt(D), out[1], out[2])
+        m.old = [n + 1 for n in m.old]
+        m.lens = [n + 1 for n in m.lens]
+
+
+def test_calls_on_a_stream_of_their_own():
+    m = Model([1, 40], [5000, 100], 64, seed=61, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 8)
+    q, w, qa = q.to(DEV), w.to(DEV), m.fill(m.T, HQ, D).to(DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    pool_idx = dsa.dsa_paged_index_topk(cache, batch, q, w, 64, stream=side)
+    o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, qa, pool_idx, stream=side)
+    side.synchronize()
+    dsa.dsa_sync_status(side)
+    check_topk(m, q.cpu(), w.cpu(), 64, pool_idx)
+    check_attention(m, qa.cpu(), pool_idx.cpu(), 1 / math.sqrt(D), o, lse)
+
+
+def test_large_cache_offsets_past_32_bits():
+    """Pages beyond 2^32 bytes (and 2^31 elements) of a buffer are reached."""
+    page, pages = 1024, 20000  # k: 5.2 GB, 2.6e9 elements
+    cache = dsa.PagedCache.empty(pages, page)
+    n = 3 * page + 5
+    table = i32([pages - 1, 0, pages - 2, 1]).view(1, 4)
+    cu = i32([0, n])
+    batch = dsa.PagedBatch(table, i32([n]), cu)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn(n, D, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    ki = torch.randint(-3, 4, (n, DI), generator=g, device=DEV).to(torch.bfloat16)
+    dsa.dsa_cache_append(cache, batch, k, v, ki)
+    assert same_bits(cache.k[pages - 1], k[:page]) and same_bits(cache.v[pages - 2], v[2 * page:3 * page])
+    qi = torch.randint(-3, 4, (n, 4, DI), generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randint(0, 4, (n, 4), generator=g, device=DEV).float()
+    got = dsa.dsa_paged_index_topk(cache, batch, qi, w, 64)
+    want = dsa.dsa_index_topk(qi, ki, w, chunk=256, topk=64)
+    assert torch.equal(got, want)
+    q = torch.randn(n, HQ, D, generator=g, device=DEV).to(torch.bfloat16)
+    o, lse = dsa.dsa_paged_sparse_attn_fwd(cache, batch, q, got)
+    wo, wl = dsa.dsa_sparse_attn_fwd(q, k, v, want)
+    dsa.dsa_sync_status()
+    torch.testing.assert_close(o.float(), wo.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+    torch.testing.assert_close(lse, wl, rtol=1e-5, atol=1e-5)
+    dsa.dsa_cache_copy_pages(cache, i32([pages - 1]), i32([pages - 3]))
+    dsa.dsa_sync_status()
+    assert same_bits(cache.k[pages - 3], k[:page])
+
+
+def test_calls_record_what_they_ran():
+    m = Model([1], [100], 16, seed=67)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 4)
+    dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 8)
+    c = dsa.last_kernel_config()
+    assert c["entry"] == "dsa_paged_index_topk" and [k for k, _ in c["kernels"]] == ["paged_scores", "paged_select"]
+    dsa.dsa_paged_index_topk(cache, batch, torch.empty(0, 4, DI, dtype=torch.bfloat16, device=DEV),
+                             torch.empty(0, 4, device=DEV), 8)
+    assert dsa.last_kernel_config()["kernels"] == []
+
+
+def test_refusals_of_the_binding():
+    m = Model([2], [30], 16, seed=71)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 4)
+    q, w = q.to(DEV), w.to(DEV)
+    with pytest.raises(TypeError):
+        dsa.dsa_paged_index_topk(cache, batch, q.float(), w, 8)
+    with pytest.raises(ValueError):
+        dsa.dsa_paged_index_topk(cache, batch, q, w[:1], 8)
+    with pytest.raises(ValueError):
+        dsa.dsa_paged_index_topk(cache, batch, q.cpu(), w, 8)
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_paged_index_topk(cache, batch, q, w, 4096)
+    assert e.value.status == dsa.DSA_ERR_UNSUPPORTED
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_paged_index_topk(cache, batch, q, w, 8, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    assert e.value.status == dsa.DSA_ERR_WORKSPACE
+    with pytest.raises(ValueError):
+        dsa.PagedCache(cache.k, cache.v[:, :8], cache.k_idx, cache.khat)
+    with pytest.raises(ValueError):
+        dsa.PagedCache(cache.k.transpose(0, 1), cache.v, cache.k_idx, cache.khat)
+    with pytest.raises(ValueError):
+        dsa.PagedBatch(batch.block_table, batch.seq_lens, i32([0]))
+    with pytest.raises(ValueError):
+        dsa.dsa_cache_append(cache, batch, *[torch.zeros(n, d, dtype=torch.bfloat16, device=DEV)
+                                             for n, d in ((2, D), (3, D), (2, DI))])
+    with pytest.raises(dsa.DsaError) as e:  # rows 260 elements apart: not a multiple of 8
+        x = torch.zeros(2, 260, dtype=torch.bfloat16, device=DEV)
+        dsa.dsa_cache_append(cache, batch, x[:, :D], x[:, :D], x[:, :DI])
+    assert e.value.status == dsa.DSA_ERR_INVALID_ARG
+    with pytest.raises(dsa.DsaError) as e:  # 12 tokens a page
+        z = [torch.zeros(4, n, d, dtype=torch.bfloat16, device=DEV) for n, d in ((12, D), (12, D), (12, DI), (3, D))]
+        dsa.dsa_cache_copy_pages(dsa.PagedCache(*z), i32([0]), i32([1]))
+    assert e.value.status == dsa.DSA_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):
+        dsa.dsa_cache_compact(cache, dsa.PageTable(batch.block_table, batch.seq_lens, i32([1] * (cache.num_pages + 1))))
