@@ -34,6 +34,19 @@ class _TableStruct(ctypes.Structure):
                 ("num_pages", _i64), ("max_pages", _i32), ("max_seqs", _i32), ("page_size", _i32)]
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
+def _full(t, name: str, dtype, ndim: int, device: int):
+    """_need for a call whose current device is known: the checks that pass
+    cost a decoding step less than a microsecond, one that fails is repeated
+    there for its message."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.get_device() == device
+            and t.is_contiguous()):
+        _need(t, name, dtype, ndim)
+
+
 def _on_device(t, name: str, dtype, ndim: int):
     """_need without contiguity: a CUDA tensor on the current device."""
     if not isinstance(t, torch.Tensor):
@@ -49,16 +62,16 @@ def _on_device(t, name: str, dtype, ndim: int):
         raise ValueError(f"{name} must have {ndim} dimensions (got shape {tuple(t.shape)})")
 
 
-def _rows_strided(t, name: str, dtype, row: int):
-    """[rows, row] whose rows are contiguous; the distance between rows is free."""
-    _on_device(t, name, dtype, 2)
-    if t.shape[1] != row or (t.shape[0] > 0 and t.stride(1) != 1):
+def _rows_strided(t, name: str, dtype, row: int, device: int) -> int:
+    """[rows, row] whose rows are contiguous; returns the distance between rows, which is free."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.get_device() == device):
+        _on_device(t, name, dtype, 2)
+    n, d = t.shape
+    apart, step = t.stride()
+    if d != row or (n > 0 and step != 1):
         raise ValueError(f"{name} must have contiguous rows of {row} elements (got shape {tuple(t.shape)}, "
                          f"strides {t.stride()})")
-
-
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return apart if n > 1 else row
 
 
 def _table(t, name: str):
@@ -68,10 +81,14 @@ def _table(t, name: str):
                          f"strides {t.stride()})")
 
 
-def _same_device(owner, what: str):
-    if owner.device_index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on cuda:{owner.device_index}, but the kernels run on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+def _device_of(*owners) -> int:
+    """The current device, which every handle must be on."""
+    now = _current_device()
+    for x in owners:
+        if x.device_index != now:
+            raise ValueError(f"the {type(x).__name__} is on cuda:{x.device_index}, but the kernels run on the current "
+                             f"device cuda:{now}")
+    return now
 
 
 class PagedCache:
@@ -129,10 +146,15 @@ class PagedBatch:
         self.device_index = block_table.device.index
         self._fields = (block_table.data_ptr(), block_table.stride(0) if block_table.shape[0] > 1 else self.max_pages,
                         seq_lens.data_ptr(), cu_q.data_ptr())
+        self._last = (-1, None)
 
     def _with_rows(self, rows: int):
-        # a struct of its own for every call: threads may share a batch
-        return ctypes.byref(_BatchStruct(*self._fields, rows, self.max_pages, self.batch))
+        # the struct of the last number of rows is kept; it is never written
+        # again, so threads may share a batch
+        last = self._last
+        if last[0] != rows:
+            last = self._last = (rows, ctypes.byref(_BatchStruct(*self._fields, rows, self.max_pages, self.batch)))
+        return last[1]
 
 
 class PageTable:
@@ -154,6 +176,7 @@ class PageTable:
         self.device, self.device_index = block_table.device, block_table.device.index
         self._fields = (block_table.data_ptr(), block_table.stride(0) if self.max_seqs > 1 else self.max_pages,
                         seq_lens.data_ptr(), page_count.data_ptr(), self.num_pages, self.max_pages, self.max_seqs)
+        self._last = (-1, None)
 
     @classmethod
     def empty(cls, cache: PagedCache, max_seqs: int, max_pages: int):
@@ -164,7 +187,10 @@ class PageTable:
                    torch.zeros(cache.num_pages, dtype=torch.int32, device=dev))
 
     def _with_page(self, page_size: int):
-        return ctypes.byref(_TableStruct(*self._fields, page_size))
+        last = self._last
+        if last[0] != page_size:
+            last = self._last = (page_size, ctypes.byref(_TableStruct(*self._fields, page_size)))
+        return last[1]
 
 
 def _configure_paged(lib):
@@ -186,59 +212,56 @@ def _configure_paged(lib):
         f.restype = ctypes.c_int
 
 
-class _On:
-    """The call's stream, and allocations that belong to it."""
-
-    def __init__(self, stream, device):
-        self.stream, self.device = stream, device
-        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-    def new(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def out(self, given, name, shape, dtype):
-        return self.new(shape, dtype) if given is None else _out(given, name, shape, dtype, self.device)
-
-    def workspace(self, nbytes, given):
-        if given is None:
-            given = self.new(max(nbytes, 256), torch.uint8)
-        else:
-            _need(given, "workspace", given.dtype, given.dim())
-        return given, given.data_ptr(), given.numel() * given.element_size()
+def _handle(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _ids(t, name: str):
-    _need(t, name, torch.int32, 1)
+def _new(shape, dtype, device: int, stream):
+    """An allocation that belongs to the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(given, name, shape, dtype, device: int, stream):
+    return _new(shape, dtype, device, stream) if given is None else _out(given, name, shape, dtype, device)
+
+
+def _scratch(nbytes: int, given, device: int, stream):
+    if given is None:
+        return _new(max(nbytes, 256), torch.uint8, device, stream)
+    _need(given, "workspace", given.dtype, given.dim())
+    return given
+
+
+def _ids(t, name: str, device: int) -> int:
+    _full(t, name, torch.int32, 1, device)
+    return t.shape[0]
 
 
 def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=None):
     """Writes the new tokens' k, v [rows, 128] and k_idx [rows, 64] (bf16, rows
-    any distance apart) into their pages, and the pooled key of every pool that
-    they complete."""
-    _same_device(cache, "cache")
-    _same_device(batch, "batch")
-    _rows_strided(k, "k", torch.bfloat16, 128)
-    _rows_strided(v, "v", torch.bfloat16, 128)
-    _rows_strided(k_idx, "k_idx", torch.bfloat16, 64)
+    any multiple of 8 elements apart) into their pages, and the pooled key of
+    every pool that they complete."""
+    dev = _device_of(cache, batch)
+    ks = _rows_strided(k, "k", torch.bfloat16, 128, dev)
+    vs = _rows_strided(v, "v", torch.bfloat16, 128, dev)
+    kis = _rows_strided(k_idx, "k_idx", torch.bfloat16, 64, dev)
     rows = k.shape[0]
-    _shape(v, "v", (rows, 128))
-    _shape(k_idx, "k_idx", (rows, 64))
-    _check(load().dsa_cache_append(cache._ref, batch._with_rows(rows), k.data_ptr(), _row_stride(k), v.data_ptr(),
-                                   _row_stride(v), k_idx.data_ptr(), _row_stride(k_idx),
-                                   _On(stream, cache.device).handle))
+    if v.shape[0] != rows or k_idx.shape[0] != rows:
+        raise ValueError(f"k, v and k_idx must have the same rows (got {rows}, {v.shape[0]} and {k_idx.shape[0]})")
+    _check(load().dsa_cache_append(cache._ref, batch._with_rows(rows), k.data_ptr(), ks, v.data_ptr(), vs,
+                                   k_idx.data_ptr(), kis, _handle(stream, dev)))
 
 
 def dsa_cache_copy_pages(cache: PagedCache, src, dst, stream=None):
     """Copies page src[j] onto page dst[j] (int32 tensors), all four buffers."""
-    _same_device(cache, "cache")
-    _ids(src, "src")
-    _ids(dst, "dst")
-    _shape(dst, "dst", tuple(src.shape))
-    _check(load().dsa_cache_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(), src.shape[0],
-                                       _On(stream, cache.device).handle))
+    dev = _device_of(cache)
+    n = _ids(src, "src", dev)
+    _ids(dst, "dst", dev)
+    _shape(dst, "dst", (n,))
+    _check(load().dsa_cache_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(), n, _handle(stream, dev)))
 
 
 def cache_workspace_size(num_pages: int, max_seqs: int, n: int = 0) -> int:
@@ -246,25 +269,24 @@ def cache_workspace_size(num_pages: int, max_seqs: int, n: int = 0) -> int:
     return int(load().dsa_cache_workspace(num_pages, max_seqs, n))
 
 
-def _of_cache(cache: PagedCache, pages: PageTable):
-    _same_device(cache, "cache")
-    if pages.device_index != cache.device_index or pages.num_pages != cache.num_pages:
-        raise ValueError(f"the page table counts {pages.num_pages} pages on cuda:{pages.device_index}, the cache has "
-                         f"{cache.num_pages} on cuda:{cache.device_index}")
+def _of_cache(cache: PagedCache, pages: PageTable) -> int:
+    dev = _device_of(cache, pages)
+    if pages.num_pages != cache.num_pages:
+        raise ValueError(f"the page table counts {pages.num_pages} pages, the cache has {cache.num_pages}")
+    return dev
 
 
 def dsa_cache_reserve(cache: PagedCache, pages: PageTable, add, result=None, workspace=None, stream=None):
     """Grows every sequence s by add[s] tokens (int32 [max_seqs]), taking the
     lowest free pages; returns a device word: pages taken, or minus the number
     lacking (then nothing changed)."""
-    _of_cache(cache, pages)
-    _ids(add, "add")
+    dev, lib = _of_cache(cache, pages), load()
+    _ids(add, "add", dev)
     _shape(add, "add", (pages.max_seqs,))
-    on, lib = _On(stream, cache.device), load()
-    result = on.out(result, "result", (1,), torch.int32)
-    ws, ptr, size = on.workspace(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace)
-    _check(lib.dsa_cache_reserve(pages._with_page(cache.page_size), add.data_ptr(), result.data_ptr(), ptr, size,
-                                 on.handle))
+    result = _result(result, "result", (1,), torch.int32, dev, stream)
+    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, dev, stream)
+    _check(lib.dsa_cache_reserve(pages._with_page(cache.page_size), add.data_ptr(), result.data_ptr(), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
 
 
@@ -272,36 +294,32 @@ def dsa_cache_fork(cache: PagedCache, pages: PageTable, src, dst, result=None, w
     """Row dst[j] becomes a copy of sequence src[j] (int32 tensors): full pages
     shared, a partly filled last page copied; returns a device word: pages
     taken, or minus the number lacking (then nothing changed)."""
-    _of_cache(cache, pages)
-    _ids(src, "src")
-    _ids(dst, "dst")
-    n = src.shape[0]
+    dev, lib = _of_cache(cache, pages), load()
+    n = _ids(src, "src", dev)
+    _ids(dst, "dst", dev)
     _shape(dst, "dst", (n,))
-    on, lib = _On(stream, cache.device), load()
-    result = on.out(result, "result", (1,), torch.int32)
-    ws, ptr, size = on.workspace(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, n), workspace)
+    result = _result(result, "result", (1,), torch.int32, dev, stream)
+    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, n), workspace, dev, stream)
     _check(lib.dsa_cache_fork(cache._ref, pages._with_page(cache.page_size), src.data_ptr(), dst.data_ptr(), n,
-                              result.data_ptr(), ptr, size, on.handle))
+                              result.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
 
 
 def dsa_cache_free(cache: PagedCache, pages: PageTable, seqs, stream=None):
     """Frees the sequences named in seqs (int32 tensor)."""
-    _of_cache(cache, pages)
-    _ids(seqs, "seqs")
-    _check(load().dsa_cache_free(pages._with_page(cache.page_size), seqs.data_ptr(), seqs.shape[0],
-                                 _On(stream, cache.device).handle))
+    dev = _of_cache(cache, pages)
+    n = _ids(seqs, "seqs", dev)
+    _check(load().dsa_cache_free(pages._with_page(cache.page_size), seqs.data_ptr(), n, _handle(stream, dev)))
 
 
 def dsa_cache_compact(cache: PagedCache, pages: PageTable, result=None, workspace=None, stream=None):
     """Moves the used pages down over the free ones; returns device words
     [pages in use, pages moved]."""
-    _of_cache(cache, pages)
-    on, lib = _On(stream, cache.device), load()
-    result = on.out(result, "result", (2,), torch.int32)
-    ws, ptr, size = on.workspace(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace)
-    _check(lib.dsa_cache_compact(cache._ref, pages._with_page(cache.page_size), result.data_ptr(), ptr, size,
-                                 on.handle))
+    dev, lib = _of_cache(cache, pages), load()
+    result = _result(result, "result", (2,), torch.int32, dev, stream)
+    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, dev, stream)
+    _check(lib.dsa_cache_compact(cache._ref, pages._with_page(cache.page_size), result.data_ptr(), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
 
 
@@ -313,17 +331,17 @@ def dsa_paged_index_topk(cache: PagedCache, batch: PagedBatch, q_idx, w, topk: i
                          stream=None):
     """pool_idx [rows, topk] int32 of the new tokens' selected pools (ascending,
     -1 padded), for q_idx [rows, Hi, 64] bf16 and w [rows, Hi] fp32."""
-    _same_device(cache, "cache")
-    _same_device(batch, "batch")
-    _need(q_idx, "q_idx", torch.bfloat16, 3)
-    _need(w, "w", torch.float32, 2)
+    dev, lib = _device_of(cache, batch), load()
+    _full(q_idx, "q_idx", torch.bfloat16, 3, dev)
+    _full(w, "w", torch.float32, 2, dev)
     rows, Hi, Di = q_idx.shape
-    _shape(w, "w", (rows, Hi))
-    on, lib = _On(stream, cache.device), load()
-    pool_idx = on.out(pool_idx, "pool_idx", (rows, max(topk, 0)), torch.int32)
-    ws, ptr, size = on.workspace(lib.dsa_paged_index_topk_workspace(rows, batch.max_pages, cache.page_size), workspace)
+    if w.shape[0] != rows or w.shape[1] != Hi:
+        _shape(w, "w", (rows, Hi))
+    pool_idx = _result(pool_idx, "pool_idx", (rows, max(topk, 0)), torch.int32, dev, stream)
+    ws = _scratch(lib.dsa_paged_index_topk_workspace(rows, batch.max_pages, cache.page_size), workspace, dev, stream)
     _check(lib.dsa_paged_index_topk(cache._ref, batch._with_rows(rows), q_idx.data_ptr(), w.data_ptr(), Hi, Di, topk,
-                                    pool_idx.data_ptr(), ptr, size, on.handle))
+                                    pool_idx.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    _handle(stream, dev)))
     return pool_idx
 
 
@@ -331,17 +349,15 @@ def dsa_paged_sparse_attn_fwd(cache: PagedCache, batch: PagedBatch, q, pool_idx,
                               stream=None):
     """(o [rows, 16, 128] bf16, lse [rows, 16] fp32) of the new tokens' attention
     over their selected pools and their own partial pool."""
-    _same_device(cache, "cache")
-    _same_device(batch, "batch")
-    _need(q, "q", torch.bfloat16, 3)
-    _need(pool_idx, "pool_idx", torch.int32, 2)
+    dev = _device_of(cache, batch)
+    _full(q, "q", torch.bfloat16, 3, dev)
+    _full(pool_idx, "pool_idx", torch.int32, 2, dev)
     rows, Hq, D = q.shape
-    if pool_idx.shape[0] != rows:
-        raise ValueError(f"pool_idx must have {rows} rows (got {pool_idx.shape[0]})")
-    on = _On(stream, cache.device)
-    o = on.out(o, "o", (rows, Hq, D), torch.bfloat16)
-    lse = on.out(lse, "lse", (rows, Hq), torch.float32)
+    sel_rows, topk = pool_idx.shape
+    if sel_rows != rows:
+        raise ValueError(f"pool_idx must have {rows} rows (got {sel_rows})")
+    o = _result(o, "o", (rows, Hq, D), torch.bfloat16, dev, stream)
+    lse = _result(lse, "lse", (rows, Hq), torch.float32, dev, stream)
     _check(load().dsa_paged_sparse_attn_fwd(cache._ref, batch._with_rows(rows), q.data_ptr(), pool_idx.data_ptr(), Hq,
-                                            D, pool_idx.shape[1], float(scale), o.data_ptr(), lse.data_ptr(),
-                                            on.handle))
+                                            D, topk, scale, o.data_ptr(), lse.data_ptr(), _handle(stream, dev)))
     return o, lse

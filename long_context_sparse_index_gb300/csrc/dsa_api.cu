@@ -1204,6 +1204,7 @@ constexpr int64_t kIntMax = 0x7FFFFFFFLL;
 constexpr int64_t kPagedScratch = int64_t{1} << 28;  // scores of a pass in the recommended workspace (1 GiB)
 constexpr int64_t kPagedPassMax = int64_t{1} << 31;  // scores of a pass however large the workspace
 constexpr int kPagedMinRows = 8;
+constexpr int kPagedTcRows = 32;  // rows per sequence from which the tcgen05 scores are taken
 
 bool page_size_ok(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 int log2_of(int x) {
@@ -1287,6 +1288,34 @@ dsa_status_t check_ws(const char* fn, const void* workspace, size_t ws_bytes, si
                 workspace ? ws_bytes : (size_t)0);
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(DSA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+  return DSA_OK;
+}
+
+// Tensor maps of the chunk scores: the queries [rows][Hi][64] and the pooled
+// keys [pages][pools per page][128].
+dsa_status_t paged_score_maps(const char* fn, const dsa::CacheView& c, const void* q_idx, int64_t rows, int Hi,
+                              CUtensorMap* q_map, CUtensorMap* k_map) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return fail(DSA_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable from the driver", fn);
+  const cuuint32_t per_page = 1u << (c.shift - 2);
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kDi), static_cast<cuuint64_t>(Hi),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kDi) * 2, static_cast<cuuint64_t>(Hi) * kDi * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kDi), 1u, 128u};
+    const CUresult r = enc(q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q_idx), dims, strides, box,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "%s: q_idx tensor map (CUresult %d)", fn, (int)r);
+  }
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(2 * kDi), per_page, static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * kDi) * 2, static_cast<cuuint64_t>(c.khat_stride) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kDi), per_page, 1u};
+  const CUresult r = enc(k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.khat, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "%s: pooled-key tensor map (CUresult %d)", fn, (int)r);
   return DSA_OK;
 }
 
@@ -1519,12 +1548,20 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
   dsa::call_param("Hi", Hi);
   dsa::call_param("topk", topk);
   dsa::call_param("rows_per_pass", pass);
-  dsa::call_variant("scores from the pages, then a row's top-k per cluster");
+  const bool tc = b.rows >= kPagedTcRows * b.batch && dsa::paged_scores_tc_fits(b);
+  dsa::call_variant(tc ? "tcgen05 scores of 128-row tiles, then a row's top-k per CTA"
+                       : "mma.sync scores of a few rows a sequence, then a row's top-k per CTA");
+  CUtensorMap q_map, k_map;
+  if (tc) {
+    st = paged_score_maps(fn, c, q_idx, b.rows, Hi, &q_map, &k_map);
+    if (st != DSA_OK) return st;
+  }
   float* scores = static_cast<float*>(workspace);
   for (int64_t r = 0; r < b.rows; r += pass) {
     const int64_t n = b.rows - r < pass ? b.rows - r : pass;
-    cudaError_t e = timed_launch("paged_scores", ctx.stream, [&] {
-      return dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, scores, ld, ctx);
+    cudaError_t e = timed_launch(tc ? "paged_scores_tc" : "paged_scores", ctx.stream, [&] {
+      return tc ? dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, scores, ld, ctx)
+                : dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, scores, ld, ctx);
     });
     if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: scores launch");
     e = timed_launch("paged_select", ctx.stream, [&] {

@@ -206,22 +206,28 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 2 : 1)
 }
 
 // ================================================================= selection
-// One row per cluster of kC CTAs (1, 2, 4 or 8).  Each CTA holds its stretch
-// of the row's scores in shared memory (the part past its room is read again
-// from global memory).  The topk-th largest score T:
-//   1. minimum and maximum; histogram of kBins equal steps between them
-//      (monotone in the score, whatever the rounding), summed over the
-//      cluster: the bin that holds T;
-//   2. while that bin holds more than kFew scores: their minimum and maximum,
-//      and a histogram of equal steps of their 32-bit keys;
-//   3. the few left are ranked against each other.
-// Then every score above T is kept and, of those equal to T, the first ones in
-// pool order; one pass counts per warp, one writes, so the output ascends.
+// One CTA per row of n > topk scores in global memory (L2 as a rule):
+//   1. n > kCap: a strided sample gives a score t that more than topk scores
+//      reach and far fewer than kCap (five standard deviations of the sampling
+//      to either side), and one pass over the row lists the scores >= t.  The
+//      row is read once.  Shorter rows are listed whole.
+//   2. The topk-th largest score T of the list: a histogram of equal steps
+//      between its extrema (monotone in the score, whatever the rounding) finds
+//      the bin that holds T; while that bin has more than kFew scores, a
+//      histogram of equal steps of their 32-bit keys narrows it; the few left
+//      are ranked against each other.
+//   3. Scores above T set a bit each, those equal to T one in a second map; the
+//      set bits in order are the row, ascending, the first ties with them.
+// Should the list come out too short or too long (correlated or non-finite
+// scores), step 2 and 3 run over the row itself: the same result, more passes.
+// Lists and not sorted keys: a row of 32768 costs one read of 128 KB and work
+// on about 1200 candidates; several rows share an SM and hide each other's
+// barriers.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kFew = 512;
-constexpr int kSelRoom = 49152;  // scores of a CTA that stay in shared memory (192 KB)
+constexpr int kFew = kSelThreads;
+constexpr int kSegment = 1 << 18;  // pools whose bits are held at once (2 x 32 KB of bits)
 
 // The order-preserving 32-bit image of a score (-0 and +0 are one), and the
 // score of a key.
@@ -238,30 +244,15 @@ struct alignas(16) SelSmem {
   uint32_t hist[kBins];
   uint32_t few[kFew];
   uint32_t wred[2][kSelWarps];
-  uint32_t wscan[kSelWarps];
-  uint32_t lo, hi;        // this CTA's extrema
-  uint32_t nfew;
-  uint32_t gt, eq;        // this CTA's kept counts
+  uint32_t lo, hi;
+  uint32_t nfew, nlist;
   uint32_t bin, above, inbin;
   uint32_t T, take;
   int seq;
 };
+static_assert(sizeof(SelSmem) % 16 == 0, "what lies after it is read 16 bytes at a time");
 
-static_assert(sizeof(SelSmem) % 16 == 0, "the scores after it are read 16 bytes at a time");
-
-template <int kC>
-__device__ __forceinline__ void sel_cluster_sync() {
-  if (kC > 1) cluster_sync();
-  else __syncthreads();
-}
-// value of a shared word in CTA u of the cluster
-template <int kC>
-__device__ __forceinline__ uint32_t sel_peer(const uint32_t* p, int u) {
-  return kC > 1 ? cluster_ld_u32(cluster_map(smem_u32(p), u)) : *p;
-}
-
-// extrema of (lo, hi) over the cluster; every thread gets them
-template <int kC>
+// extrema over the block; every thread gets them
 __device__ __forceinline__ void sel_minmax(SelSmem& sm, uint32_t& lo, uint32_t& hi) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   lo = __reduce_min_sync(0xffffffffu, lo);
@@ -271,50 +262,41 @@ __device__ __forceinline__ void sel_minmax(SelSmem& sm, uint32_t& lo, uint32_t& 
     sm.wred[1][warp] = hi;
   }
   __syncthreads();
-  if (warp == 0) {
-    const uint32_t a = __reduce_min_sync(0xffffffffu, lane < kSelWarps ? sm.wred[0][lane] : 0xFFFFFFFFu);
-    const uint32_t z = __reduce_max_sync(0xffffffffu, lane < kSelWarps ? sm.wred[1][lane] : 0u);
-    if (lane == 0) {
-      sm.lo = a;
-      sm.hi = z;
-    }
-  }
-  sel_cluster_sync<kC>();
-  lo = 0xFFFFFFFFu;
-  hi = 0u;
-#pragma unroll
-  for (int u = 0; u < kC; ++u) {
-    lo = min(lo, sel_peer<kC>(&sm.lo, u));
-    hi = max(hi, sel_peer<kC>(&sm.hi, u));
-  }
+  lo = __reduce_min_sync(0xffffffffu, lane < kSelWarps ? sm.wred[0][lane] : 0xFFFFFFFFu);
+  hi = __reduce_max_sync(0xffffffffu, lane < kSelWarps ? sm.wred[1][lane] : 0u);
+  __syncthreads();  // read: wred may be written again
 }
 
-// Sums the CTAs' histograms and finds the bin holding the need-th largest:
-// sm.bin, sm.above (scores in higher bins), sm.inbin, the same in every CTA.
-template <int kC>
-__device__ __forceinline__ void sel_find(SelSmem& sm, uint32_t need) {
+// Exclusive prefix of v over the block in thread order, and the total.
+__device__ __forceinline__ uint32_t sel_scan(SelSmem& sm, uint32_t v, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kPer = kBins / kSelThreads;
-  sel_cluster_sync<kC>();  // every CTA's histogram is complete
-  uint32_t cnt[kPer], sum = 0;  // bins in descending order: thread 0 has the highest
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) cnt[j] = 0;
-#pragma unroll
-  for (int u = 0; u < kC; ++u)
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) cnt[j] += sel_peer<kC>(&sm.hist[kBins - 1 - (kPer * threadIdx.x + j)], u);
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) sum += cnt[j];
-  uint32_t x = sum;
+  uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) sm.wscan[warp] = x;
+  if (lane == 31) sm.wred[0][warp] = x;
   __syncthreads();
-  uint32_t before = x - sum;
-  for (int k = 0; k < warp; ++k) before += sm.wscan[k];
+  const uint32_t w = lane < kSelWarps ? sm.wred[0][lane] : 0u;
+  *total = __reduce_add_sync(0xffffffffu, w);
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
+  __syncthreads();
+  return before + x - v;
+}
+
+// The bin of the complete histogram (a barrier precedes) that holds the need-th
+// largest: sm.bin, sm.above (scores in higher bins), sm.inbin.
+__device__ __forceinline__ void sel_find(SelSmem& sm, uint32_t need) {
+  constexpr int kPer = kBins / kSelThreads;
+  uint32_t cnt[kPer], sum = 0;  // bins in descending order: thread 0 has the highest
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    cnt[j] = sm.hist[kBins - 1 - (kPer * threadIdx.x + j)];
+    sum += cnt[j];
+  }
+  uint32_t all;
+  uint32_t before = sel_scan(sm, sum, &all);
   if (before < need && need <= before + sum) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -326,152 +308,107 @@ __device__ __forceinline__ void sel_find(SelSmem& sm, uint32_t need) {
       before += cnt[j];
     }
   }
-  sel_cluster_sync<kC>();  // found, and no histogram is read any more
+  __syncthreads();
 }
 
-template <int kC>
-__global__ void __launch_bounds__(kSelThreads)
-    paged_select_kernel(const BatchView b, int shift, int64_t row0, const float* __restrict__ scores, int64_t ld,
-                        int topk, int room, int32_t* __restrict__ pool_idx, unsigned* status) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
-  float* kept = reinterpret_cast<float*>(smem_raw + sizeof(SelSmem));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = kC > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int64_t lrow = blockIdx.x / kC, row = row0 + lrow;
-  if (warp == 0) {
-    const int n = warp_locate(b, row, lane);
-    if (lane == 0) sm.seq = n;
+// Equal steps of the score between two keys: bin(f) is monotone in f.  inv = 0
+// where the range is not finite or empty.
+struct Steps {
+  float lo, inv;
+  __device__ __forceinline__ static Steps of(uint32_t klo, uint32_t khi) {
+    Steps s;
+    s.lo = key_score(klo);
+    const float range = key_score(khi) - s.lo;
+    s.inv = range > 0.f && range < INFINITY ? fminf(static_cast<float>(kBins) / range, 3.0e38f) : 0.f;
+    return s;
   }
-  __syncthreads();
-  const int seq = sm.seq;
-  if (seq >= b.batch) return;  // padding behind the last sequence (the whole cluster)
-  const int64_t i = row_position(b, shift, seq, row, status);
-  int32_t* orow = pool_idx + row * topk;
-  const int64_t n = i < 0 ? 0 : i >> 2;
-  if (n <= topk) {  // every pool (or, for a row without a position, nothing)
-    for (int j = rank * kSelThreads + tid; j < topk; j += kC * kSelThreads) orow[j] = j < n ? j : -1;
-    return;
+  __device__ __forceinline__ float at(float f) const { return (f - lo) * inv; }
+  __device__ __forceinline__ int bin(float f) const {
+    const float x = at(f);
+    return x >= static_cast<float>(kBins - 1) ? kBins - 1 : static_cast<int>(x);
   }
-  // this CTA's stretch, a multiple of 4 long but for the last
-  const int per = static_cast<int>(((n + kC - 1) / kC + 3) & ~int64_t{3});
-  const int64_t base = static_cast<int64_t>(rank) * per;
-  const int cnt = static_cast<int>(base >= n ? 0 : min(static_cast<int64_t>(per), n - base));
-  const float* srow = scores + lrow * ld + base;
+};
 
-  // ---- load; extrema
-  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-  for (int j = 4 * tid; j < cnt; j += 4 * kSelThreads) {
-    float4 f;
-    if (j + 3 < cnt) {
-      f = *reinterpret_cast<const float4*>(srow + j);
-    } else {
-      f.x = srow[j];
-      f.y = j + 1 < cnt ? srow[j + 1] : f.x;
-      f.z = j + 2 < cnt ? srow[j + 2] : f.x;
-      f.w = f.x;
-    }
-    const uint32_t k0 = score_key(f.x), k1 = score_key(f.y), k2 = score_key(f.z),
-                   k3 = score_key(f.w);
-    lo = min(min(lo, min(k0, k1)), min(k2, k3));
-    hi = max(max(hi, max(k0, k1)), max(k2, k3));
-    if (j < room) *reinterpret_cast<float4*>(kept + j) = f;  // room is a multiple of 4
-  }
-  auto get = [&](int j) { return j < room ? kept[j] : srow[j]; };
+// The need-th largest of the cnt > need scores that `each(f)` walks (f(score),
+// every thread its share): key T, and how many scores equal to it are among
+// the need largest.
+template <typename Each>
+__device__ __forceinline__ void sel_kth(SelSmem& sm, uint32_t need, uint32_t cnt, Each&& each, uint32_t* T,
+                                        uint32_t* take) {
+  const int tid = threadIdx.x;
   for (int j = tid; j < kBins; j += kSelThreads) sm.hist[j] = 0u;
-  sel_minmax<kC>(sm, lo, hi);
-
-  // ---- first round: equal steps of the score
-  uint32_t need = static_cast<uint32_t>(topk), T = lo, take = need;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+  each([&](float f) {
+    const uint32_t k = score_key(f);
+    lo = min(lo, k);
+    hi = max(hi, k);
+  });
+  sel_minmax(sm, lo, hi);
   if (lo != hi) {
-    const float flo = key_score(lo), fhi = key_score(hi);
-    const float step = fhi - flo;
-    const float inv = step > 0.f && step < INFINITY ? fminf(static_cast<float>(kBins) / step, 3.0e38f) : 0.f;
-    auto bin_of = [&](float f) {
-      const float x = (f - flo) * inv;  // non-finite scores make inv 0 or x a NaN: bin 0 or the last
-      return x >= static_cast<float>(kBins - 1) ? kBins - 1 : static_cast<int>(x);
-    };
-    const bool linear = inv > 0.f;  // (the same in every CTA of the cluster)
-    if (!linear) sel_cluster_sync<kC>();  // the extrema have been read: the next round may write its own
-    if (linear) {
-      for (int j = tid; j < cnt; j += kSelThreads) atomicAdd(&sm.hist[bin_of(get(j))], 1u);
-      sel_find<kC>(sm, need);
+    const Steps st = Steps::of(lo, hi);
+    uint32_t members = cnt;
+    int bin0 = -1;  // -1: every score
+    if (st.inv > 0.f) {
+      each([&](float f) { atomicAdd(&sm.hist[st.bin(f)], 1u); });
+      __syncthreads();
+      sel_find(sm, need);
+      members = sm.inbin;
+      need -= sm.above;
+      bin0 = static_cast<int>(sm.bin);
     }
-    uint32_t members = linear ? sm.inbin : static_cast<uint32_t>(min(n, int64_t{0xFFFFFFFF}));
-    if (linear) need -= sm.above;
-    const int bin0 = linear ? static_cast<int>(sm.bin) : -1;
-    // ---- the bin's scores by their keys; window [lo, hi] once it is known
-    bool windowed = false;
-    auto inside = [&](float f, uint32_t k) { return windowed ? k >= lo && k <= hi : bin0 < 0 || bin_of(f) == bin0; };
+    bool windowed = false;  // the members are the scores with keys in [lo, hi]
+    auto inside = [&](float f, uint32_t k) {
+      return windowed ? k >= lo && k <= hi : bin0 < 0 || st.bin(f) == bin0;
+    };
     while (members > static_cast<uint32_t>(kFew)) {
       uint32_t a = 0xFFFFFFFFu, z = 0u;
-      for (int j = tid; j < cnt; j += kSelThreads) {
-        const float f = get(j);
+      each([&](float f) {
         const uint32_t k = score_key(f);
         if (inside(f, k)) {
           a = min(a, k);
           z = max(z, k);
         }
-      }
+      });
       for (int j = tid; j < kBins; j += kSelThreads) sm.hist[j] = 0u;
-      sel_minmax<kC>(sm, a, z);
+      sel_minmax(sm, a, z);
       lo = a;
       hi = z;
       windowed = true;
       if (lo == hi) break;
       const int bits = 32 - __clz(hi - lo);
       const int sh = bits > 11 ? bits - 11 : 0;
-      for (int j = tid; j < cnt; j += kSelThreads) {
-        const uint32_t k = score_key(get(j));
+      each([&](float f) {
+        const uint32_t k = score_key(f);
         if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> sh], 1u);
-      }
-      sel_find<kC>(sm, need);
-      need -= sm.above;
+      });
+      __syncthreads();
+      sel_find(sm, need);
       members = sm.inbin;
+      need -= sm.above;
       const uint32_t nlo = lo + (sm.bin << sh);
       const uint64_t nhi = static_cast<uint64_t>(nlo) + ((1ull << sh) - 1ull);
       lo = nlo;
       hi = nhi < hi ? static_cast<uint32_t>(nhi) : hi;
       if (sh == 0) break;
     }
-    if (windowed && lo == hi) {
-      T = lo;
-      take = need;
-    } else {
-      // ---- at most kFew in the cluster: every CTA lists its own
+    if (!(windowed && lo == hi)) {
       if (tid == 0) sm.nfew = 0u;
       __syncthreads();
-      for (int j = tid; j < cnt; j += kSelThreads) {
-        const float f = get(j);
+      each([&](float f) {
         const uint32_t k = score_key(f);
         if (inside(f, k)) {
           const uint32_t at = atomicAdd(&sm.nfew, 1u);
           if (at < static_cast<uint32_t>(kFew)) sm.few[at] = k;
         }
-      }
-      sel_cluster_sync<kC>();
-      // every CTA ranks every listed key: one key a thread
-      uint32_t mine = 0u, at = static_cast<uint32_t>(tid);
-      bool has = false;
-#pragma unroll
-      for (int u = 0; u < kC; ++u) {
-        const uint32_t m = min(sel_peer<kC>(&sm.nfew, u), static_cast<uint32_t>(kFew));
-        if (!has && at < m) {
-          mine = sel_peer<kC>(&sm.few[at], u);
-          has = true;
-        } else if (!has) {
-          at -= m;
-        }
-      }
-      uint32_t gt = 0u, eq = 0u;
-      if (has) {
-        for (int u = 0; u < kC; ++u) {
-          const uint32_t m = min(sel_peer<kC>(&sm.nfew, u), static_cast<uint32_t>(kFew));
-          for (uint32_t e = 0; e < m; ++e) {
-            const uint32_t k = sel_peer<kC>(&sm.few[e], u);
-            gt += k > mine;
-            eq += k == mine;
-          }
+      });
+      __syncthreads();
+      const uint32_t m = min(sm.nfew, static_cast<uint32_t>(kFew));
+      if (tid < static_cast<int>(m)) {
+        const uint32_t mine = sm.few[tid];
+        uint32_t gt = 0u, eq = 0u;
+        for (uint32_t e = 0; e < m; ++e) {
+          gt += sm.few[e] > mine;
+          eq += sm.few[e] == mine;
         }
         if (gt < need && need <= gt + eq) {  // every thread with T writes the same
           sm.T = mine;
@@ -479,59 +416,205 @@ __global__ void __launch_bounds__(kSelThreads)
         }
       }
       __syncthreads();
-      T = sm.T;
-      take = sm.take;
+      *T = sm.T;
+      *take = sm.take;
+      return;
     }
   }
+  *T = lo;
+  *take = need;
+}
 
-  // ---- keep: counts per warp (each warp a contiguous stretch), prefix over the cluster, then the indices
-  const int wper = ((cnt + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int w0 = min(warp * wper, cnt), w1 = min(w0 + wper, cnt);
-  uint32_t ngt = 0u, neq = 0u;
-  for (int j = w0; j < w1; j += 32) {
-    const uint32_t k = j + lane < w1 ? score_key(get(j + lane)) : 0u;
-    ngt += j + lane < w1 && k > T;
-    neq += j + lane < w1 && k == T;
-  }
-  ngt = __reduce_add_sync(0xffffffffu, ngt);
-  neq = __reduce_add_sync(0xffffffffu, neq);
-  if (lane == 0) {
-    sm.wred[0][warp] = ngt;
-    sm.wred[1][warp] = neq;
+template <int kCap>
+__global__ void __launch_bounds__(kSelThreads, kCap <= 4096 ? 3 : 2)
+    paged_select_kernel(const BatchView b, int shift, int64_t row0, const float* __restrict__ scores, int64_t ld,
+                        int topk, int words_room, int32_t* __restrict__ pool_idx, unsigned* status) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
+  float* cval = reinterpret_cast<float*>(smem_raw + sizeof(SelSmem));    // [kCap] candidates
+  int32_t* cidx = reinterpret_cast<int32_t*>(cval + kCap);                // [kCap] their pools
+  uint32_t* above = reinterpret_cast<uint32_t*>(cidx + kCap);             // [words_room] bits: scores above T
+  uint32_t* equal = above + words_room;                                   // [words_room] bits: scores equal to T
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t lrow = blockIdx.x, row = row0 + lrow;
+  if (warp == 0) {
+    const int n = warp_locate(b, row, lane);
+    if (lane == 0) {
+      sm.seq = n;
+      sm.nlist = 0u;
+    }
   }
   __syncthreads();
-  uint32_t gt = 0u, eq = 0u;
-  for (int k = 0; k < kSelWarps; ++k) {
-    gt += k < warp ? sm.wred[0][k] : 0u;
-    eq += k < warp ? sm.wred[1][k] : 0u;
+  const int seq = sm.seq;
+  if (seq >= b.batch) return;  // padding behind the last sequence
+  const int64_t i = row_position(b, shift, seq, row, status);
+  int32_t* orow = pool_idx + row * topk;
+  const int n = i < 0 ? 0 : static_cast<int>(i >> 2);
+  if (n <= topk) {  // every pool (or, for a row without a position, nothing)
+    for (int j = tid; j < topk; j += kSelThreads) orow[j] = j < n ? j : -1;
+    return;
   }
-  if (kC > 1) {
-    if (tid == kSelThreads - 1) {  // the last warp's prefix and its own
-      sm.gt = gt + ngt;
-      sm.eq = eq + neq;
+  const float* srow = scores + lrow * ld;
+
+  // ---- candidates
+  bool listed = n <= kCap;
+  if (listed) {
+    for (int j = tid; j < n; j += kSelThreads) {
+      cval[j] = srow[j];
+      cidx[j] = j;
     }
-    cluster_sync();
+    if (tid == 0) sm.nlist = static_cast<uint32_t>(n);
+  } else {
+    // quads (4 consecutive scores) of the sample: 2 a thread, 8 beyond 2^16 pools
+    const int nq = n >> 2, per = n > 65536 ? 8 : 2;
+    float4 q[8];
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
 #pragma unroll
-    for (int u = 0; u < kC; ++u)
-      if (u < rank) {
-        gt += sel_peer<kC>(&sm.gt, u);
-        eq += sel_peer<kC>(&sm.eq, u);
-      }
-  }
-  const unsigned below = (1u << lane) - 1u;
-  for (int j = w0; j < w1; j += 32) {
-    const bool in = j + lane < w1;
-    const uint32_t k = in ? score_key(get(j + lane)) : 0u;
-    const unsigned mg = __ballot_sync(0xffffffffu, in && k > T), me = __ballot_sync(0xffffffffu, in && k == T);
-    const uint32_t pe = eq + __popc(me & below);
-    if (in && (k > T || (k == T && pe < take))) {
-      const uint32_t pos = gt + __popc(mg & below) + min(pe, take);
-      if (pos < static_cast<uint32_t>(topk)) orow[pos] = static_cast<int32_t>(base + j + lane);
+    for (int u = 0; u < 8; ++u) {
+      if (u >= per) break;
+      const int64_t k = static_cast<int64_t>(u * kSelThreads + tid) * nq / (per * kSelThreads);
+      q[u] = *reinterpret_cast<const float4*>(srow + 4 * k);
     }
-    gt += __popc(mg);
-    eq += __popc(me);
+    for (int j = tid; j < kBins; j += kSelThreads) sm.hist[j] = 0u;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (u >= per) break;
+      const uint32_t k0 = score_key(q[u].x), k1 = score_key(q[u].y), k2 = score_key(q[u].z), k3 = score_key(q[u].w);
+      lo = min(min(lo, min(k0, k1)), min(k2, k3));
+      hi = max(max(hi, max(k0, k1)), max(k2, k3));
+    }
+    sel_minmax(sm, lo, hi);
+    const Steps st = Steps::of(lo, hi);
+    if (st.inv > 0.f) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (u >= per) break;
+        atomicAdd(&sm.hist[st.bin(q[u].x)], 1u);
+        atomicAdd(&sm.hist[st.bin(q[u].y)], 1u);
+        atomicAdd(&sm.hist[st.bin(q[u].z)], 1u);
+        atomicAdd(&sm.hist[st.bin(q[u].w)], 1u);
+      }
+      __syncthreads();
+      // c candidates with c - 5 sqrt(c sigma) = topk, sigma scores a sample
+      const float sigma = static_cast<float>(n) / static_cast<float>(4 * per * kSelThreads);
+      const float rc = 0.5f * (5.f * sqrtf(sigma) + sqrtf(25.f * sigma + 4.f * static_cast<float>(topk)));
+      const int want = min(static_cast<int>(rc * rc / sigma) + 1, 4 * per * kSelThreads);
+      sel_find(sm, static_cast<uint32_t>(want));
+      const float edge = static_cast<float>(sm.bin);
+      // one pass over the row; four 16-byte loads in flight a thread
+      constexpr int kU = 4;
+      for (int j0 = 0; j0 < n; j0 += 4 * kU * kSelThreads) {
+        float4 x[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int j = j0 + 4 * (u * kSelThreads + tid);
+          if (j + 3 < n) x[u] = *reinterpret_cast<const float4*>(srow + j);
+          else {
+            x[u].x = j < n ? srow[j] : -INFINITY;
+            x[u].y = j + 1 < n ? srow[j + 1] : -INFINITY;
+            x[u].z = j + 2 < n ? srow[j + 2] : -INFINITY;
+            x[u].w = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int j = j0 + 4 * (u * kSelThreads + tid);
+          const float f[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          bool hit[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hit[e] = st.at(f[e]) >= edge && j + e < n;
+          if (!__any_sync(0xffffffffu, hit[0] || hit[1] || hit[2] || hit[3])) continue;
+          uint32_t m[4], all = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            m[e] = __ballot_sync(0xffffffffu, hit[e]);
+            all += __popc(m[e]);
+          }
+          uint32_t at = 0u;
+          if (lane == 0) at = atomicAdd(&sm.nlist, all);
+          at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t to = at + __popc(m[e] & ((1u << lane) - 1u));
+            if (hit[e] && to < static_cast<uint32_t>(kCap)) {
+              cval[to] = f[e];
+              cidx[to] = j + e;
+            }
+            at += __popc(m[e]);
+          }
+        }
+      }
+      __syncthreads();
+      listed = sm.nlist >= static_cast<uint32_t>(topk) && sm.nlist <= static_cast<uint32_t>(kCap);
+    }
   }
-  if (kC > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
+  __syncthreads();
+  const int m = static_cast<int>(sm.nlist);
+
+  // ---- T
+  uint32_t T = 0u, take = 0u;
+  if (listed && m > topk) {
+    sel_kth(sm, static_cast<uint32_t>(topk), static_cast<uint32_t>(m), [&](auto&& f) {
+      for (int j = tid; j < m; j += kSelThreads) f(cval[j]);
+    }, &T, &take);
+  } else if (!listed) {
+    sel_kth(sm, static_cast<uint32_t>(topk), static_cast<uint32_t>(n), [&](auto&& f) {
+      for (int j = tid; j < n; j += kSelThreads) f(srow[j]);
+    }, &T, &take);
+  }  // a list of exactly topk scores is kept whole: every key is above T = 0 (no score's), or equal to it
+
+  // ---- the row, segment by segment
+  uint32_t done = 0u, ties = 0u;  // written so far; ties met so far
+  if (listed && m == topk) take = static_cast<uint32_t>(topk);
+  for (int s0 = 0; s0 < n; s0 += kSegment) {
+    const int len = min(kSegment, n - s0), words = (len + 31) >> 5;
+    if (listed) {
+      for (int k = tid; k < words; k += kSelThreads) above[k] = equal[k] = 0u;
+      __syncthreads();
+      for (int j = tid; j < m; j += kSelThreads) {
+        const int p = cidx[j] - s0;
+        const uint32_t k = score_key(cval[j]);
+        if (p >= 0 && p < len && k >= T) atomicOr((k > T ? above : equal) + (p >> 5), 1u << (p & 31));
+      }
+    } else {
+      for (int k = warp; k < words; k += kSelWarps) {
+        const int j = s0 + 32 * k + lane;
+        const uint32_t key = j < n ? score_key(srow[j]) : 0u;
+        const uint32_t g = __ballot_sync(0xffffffffu, j < n && key > T), e = __ballot_sync(0xffffffffu, j < n && key == T);
+        if (lane == 0) {
+          above[k] = g;
+          equal[k] = e;
+        }
+      }
+    }
+    __syncthreads();
+    const int wpt = (words + kSelThreads - 1) / kSelThreads;
+    const int k0 = min(tid * wpt, words), k1 = min(k0 + wpt, words);
+    uint32_t g = 0u, e = 0u;
+    for (int k = k0; k < k1; ++k) {
+      g += __popc(above[k]);
+      e += __popc(equal[k]);
+    }
+    uint32_t g_all, e_all;
+    uint32_t pe = ties + sel_scan(sm, e, &e_all);
+    const uint32_t pg = sel_scan(sm, g, &g_all);
+    uint32_t pos = done + pg + (min(pe, take) - min(ties, take));
+    for (int k = k0; k < k1; ++k) {
+      const uint32_t ek = equal[k];
+      uint32_t bits = above[k] | ek;
+      while (bits) {
+        const int z = __ffs(bits) - 1;
+        bits &= bits - 1u;
+        const bool tie = (ek >> z) & 1u;
+        if (tie && pe++ >= take) continue;
+        if (pos < static_cast<uint32_t>(topk)) orow[pos] = s0 + 32 * k + z;
+        ++pos;
+      }
+    }
+    done += g_all + (min(ties + e_all, take) - min(ties, take));
+    ties += e_all;
+    __syncthreads();  // the bits are read: the next segment may set its own
+  }
 }
 
 template <int kMt>
@@ -544,30 +627,20 @@ cudaError_t launch_scores(const CacheView& c, const BatchView& b, const void* q_
   return cudaGetLastError();
 }
 
-template <int kC>
+template <int kCap>
 cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores, int64_t ld,
-                          int64_t pools, int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
-  const int64_t per = ((pools + kC - 1) / kC + 3) & ~int64_t{3};
-  const int room = static_cast<int>(per < kSelRoom ? per : kSelRoom);
-  constexpr int kMost = static_cast<int>(sizeof(SelSmem)) + kSelRoom * 4;
+                          int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
+  const int64_t pools = static_cast<int64_t>(b.max_pages) << (shift - 2);
+  const int words = static_cast<int>((pools < kSegment ? pools : kSegment) + 31) / 32;
+  constexpr size_t kFixed = sizeof(SelSmem) + static_cast<size_t>(kCap) * 8;
+  constexpr size_t kMost = kFixed + 2 * (kSegment / 32) * 4;
   static_assert(kMost <= 232448 - 1024, "shared memory per CTA");
   static std::atomic<bool> attr_done[kAttrDevices];
-  cudaError_t e = set_smem_limit_once(paged_select_kernel<kC>, kMost, attr_done);
+  const cudaError_t e = set_smem_limit_once(paged_select_kernel<kCap>, static_cast<int>(kMost), attr_done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(nrows * kC));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = sizeof(SelSmem) + static_cast<size_t>(room) * 4;
-  cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kC;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kC > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_select_kernel<kC>, b, shift, row0, scores, ld, topk, room, pool_idx,
-                            ctx.status);
+  paged_select_kernel<kCap><<<static_cast<unsigned>(nrows), kSelThreads, kFixed + static_cast<size_t>(words) * 8,
+                              ctx.stream>>>(b, shift, row0, scores, ld, topk, words, pool_idx, ctx.status);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -581,13 +654,9 @@ cudaError_t launch_paged_scores(const CacheView& c, const BatchView& b, const vo
 
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,
                                 int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
-  const int64_t pools = static_cast<int64_t>(b.max_pages) << (shift - 2);
-  if (nrows * 8 <= 2 * ctx.num_sms || pools > 4 * kSelRoom)
-    return launch_select<8>(b, shift, row0, nrows, scores, ld, pools, topk, pool_idx, ctx);
-  if (nrows * 4 <= 4 * ctx.num_sms || pools > 2 * kSelRoom)
-    return launch_select<4>(b, shift, row0, nrows, scores, ld, pools, topk, pool_idx, ctx);
-  if (pools > kSelRoom) return launch_select<2>(b, shift, row0, nrows, scores, ld, pools, topk, pool_idx, ctx);
-  return launch_select<1>(b, shift, row0, nrows, scores, ld, pools, topk, pool_idx, ctx);
+  // the list must hold topk and the spread of the sampling
+  if (topk <= 512) return launch_select<4096>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
+  return launch_select<8192>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
 }
 
 }  // namespace dsa
