@@ -147,6 +147,14 @@ class PagedBatch:
         self._fields = (block_table.data_ptr(), block_table.stride(0) if block_table.shape[0] > 1 else self.max_pages,
                         seq_lens.data_ptr(), cu_q.data_ptr())
         self._last = (-1, None)
+        self._index_ws = (None, 0)
+
+    def _index_workspace(self, rows: int, page_size: int) -> int:
+        last = self._index_ws
+        if last[0] != (rows, page_size):
+            last = self._index_ws = ((rows, page_size),
+                                     load().dsa_paged_index_topk_workspace(rows, self.max_pages, page_size))
+        return last[1]
 
     def _with_rows(self, rows: int):
         # the struct of the last number of rows is kept; it is never written
@@ -216,19 +224,20 @@ def _handle(stream, device: int) -> int:
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _new(shape, dtype, device: int, stream):
-    """An allocation that belongs to the call's stream."""
+def _new(shape, dtype, device, stream):
+    """An allocation that belongs to the call's stream.  (`device` is a
+    torch.device: an ordinal costs torch.empty three microseconds more.)"""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _result(given, name, shape, dtype, device: int, stream):
+def _result(given, name, shape, dtype, device, stream):
     return _new(shape, dtype, device, stream) if given is None else _out(given, name, shape, dtype, device)
 
 
-def _scratch(nbytes: int, given, device: int, stream):
+def _scratch(nbytes: int, given, device, stream):
     if given is None:
         return _new(max(nbytes, 256), torch.uint8, device, stream)
     _need(given, "workspace", given.dtype, given.dim())
@@ -283,8 +292,8 @@ def dsa_cache_reserve(cache: PagedCache, pages: PageTable, add, result=None, wor
     dev, lib = _of_cache(cache, pages), load()
     _ids(add, "add", dev)
     _shape(add, "add", (pages.max_seqs,))
-    result = _result(result, "result", (1,), torch.int32, dev, stream)
-    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, dev, stream)
+    result = _result(result, "result", (1,), torch.int32, cache.device, stream)
+    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, cache.device, stream)
     _check(lib.dsa_cache_reserve(pages._with_page(cache.page_size), add.data_ptr(), result.data_ptr(), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
@@ -298,8 +307,8 @@ def dsa_cache_fork(cache: PagedCache, pages: PageTable, src, dst, result=None, w
     n = _ids(src, "src", dev)
     _ids(dst, "dst", dev)
     _shape(dst, "dst", (n,))
-    result = _result(result, "result", (1,), torch.int32, dev, stream)
-    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, n), workspace, dev, stream)
+    result = _result(result, "result", (1,), torch.int32, cache.device, stream)
+    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, n), workspace, cache.device, stream)
     _check(lib.dsa_cache_fork(cache._ref, pages._with_page(cache.page_size), src.data_ptr(), dst.data_ptr(), n,
                               result.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
@@ -316,8 +325,8 @@ def dsa_cache_compact(cache: PagedCache, pages: PageTable, result=None, workspac
     """Moves the used pages down over the free ones; returns device words
     [pages in use, pages moved]."""
     dev, lib = _of_cache(cache, pages), load()
-    result = _result(result, "result", (2,), torch.int32, dev, stream)
-    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, dev, stream)
+    result = _result(result, "result", (2,), torch.int32, cache.device, stream)
+    ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, cache.device, stream)
     _check(lib.dsa_cache_compact(cache._ref, pages._with_page(cache.page_size), result.data_ptr(), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
@@ -337,8 +346,8 @@ def dsa_paged_index_topk(cache: PagedCache, batch: PagedBatch, q_idx, w, topk: i
     rows, Hi, Di = q_idx.shape
     if w.shape[0] != rows or w.shape[1] != Hi:
         _shape(w, "w", (rows, Hi))
-    pool_idx = _result(pool_idx, "pool_idx", (rows, max(topk, 0)), torch.int32, dev, stream)
-    ws = _scratch(lib.dsa_paged_index_topk_workspace(rows, batch.max_pages, cache.page_size), workspace, dev, stream)
+    pool_idx = _result(pool_idx, "pool_idx", (rows, max(topk, 0)), torch.int32, cache.device, stream)
+    ws = _scratch(batch._index_workspace(rows, cache.page_size), workspace, cache.device, stream)
     _check(lib.dsa_paged_index_topk(cache._ref, batch._with_rows(rows), q_idx.data_ptr(), w.data_ptr(), Hi, Di, topk,
                                     pool_idx.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
                                     _handle(stream, dev)))
@@ -356,8 +365,8 @@ def dsa_paged_sparse_attn_fwd(cache: PagedCache, batch: PagedBatch, q, pool_idx,
     sel_rows, topk = pool_idx.shape
     if sel_rows != rows:
         raise ValueError(f"pool_idx must have {rows} rows (got {sel_rows})")
-    o = _result(o, "o", (rows, Hq, D), torch.bfloat16, dev, stream)
-    lse = _result(lse, "lse", (rows, Hq), torch.float32, dev, stream)
+    o = _result(o, "o", (rows, Hq, D), torch.bfloat16, cache.device, stream)
+    lse = _result(lse, "lse", (rows, Hq), torch.float32, cache.device, stream)
     _check(load().dsa_paged_sparse_attn_fwd(cache._ref, batch._with_rows(rows), q.data_ptr(), pool_idx.data_ptr(), Hq,
                                             D, topk, scale, o.data_ptr(), lse.data_ptr(), _handle(stream, dev)))
     return o, lse

@@ -12,26 +12,48 @@
 
 namespace dsa {
 
-// Sequence of `row` (all lanes of a warp call it together with the same row):
-// the number of sequences that end at or before it.  batch: past the last.
-__device__ __forceinline__ int warp_locate(const BatchView& b, int64_t row, int lane) {
-  int n = 0;
-  for (int j = lane; j < b.batch; j += 32) n += __ldg(b.cu + j + 1) <= row;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
+// Sequence and position of a row; seq < 0: padding behind the last sequence;
+// pos < 0: offsets and lengths that contradict each other (recorded).
+struct RowAt {
+  int seq;
+  int64_t pos;
+};
 
-// Position of `row` in its sequence s (< batch), or -1 (recorded) when the
-// offsets and lengths contradict each other or the block table is too short.
-__device__ __forceinline__ int64_t row_position(const BatchView& b, int shift, int s, int64_t row, unsigned* status) {
-  const int c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1), len = __ldg(b.lens + s);
-  const int64_t i = static_cast<int64_t>(len) - c1 + row;
-  if (row < c0 || row >= c1 || i < row - c0 || len > (static_cast<int64_t>(b.max_pages) << shift)) {
-    record_status(status, kStatusInternal);
-    return -1;
+// All lanes of a warp call it together with the same row.  Offsets and lengths
+// of 128 sequences are looked at at once, so that a call of up to 128
+// sequences waits for memory once.
+__device__ __forceinline__ RowAt warp_locate(const BatchView& b, int shift, int64_t row, int lane, unsigned* status) {
+  constexpr int kU = 4;
+  RowAt x{-1, -1};
+  for (int j0 = 0; j0 < b.batch && x.seq < 0; j0 += 32 * kU) {
+    int c0[kU], c1[kU], len[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int j = j0 + 32 * u + lane;
+      c0[u] = c1[u] = len[u] = 0;  // (an empty stretch: no row lies in it)
+      if (j < b.batch) {
+        c0[u] = __ldg(b.cu + j);
+        c1[u] = __ldg(b.cu + j + 1);
+        len[u] = __ldg(b.lens + j);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const unsigned hit = __ballot_sync(0xffffffffu, c0[u] <= row && row < c1[u]);
+      if (hit == 0u || x.seq >= 0) continue;
+      const int src = __ffs(hit) - 1;
+      const int64_t first = __shfl_sync(0xffffffffu, c0[u], src), last = __shfl_sync(0xffffffffu, c1[u], src);
+      const int64_t n = __shfl_sync(0xffffffffu, len[u], src);
+      x.seq = j0 + 32 * u + src;
+      x.pos = n - last + row;
+      // the sequence must be as long as its new tokens, and its table as long as it
+      if (x.pos < row - first || n > (static_cast<int64_t>(b.max_pages) << shift)) {
+        x.pos = -1;
+        if (lane == 0) record_status(status, kStatusInternal);
+      }
+    }
   }
-  return i;
+  return x;
 }
 
 // Page x of sequence s (x < max_pages), or -1 (recorded) for a number that is

@@ -9,8 +9,7 @@
 // (relative 2^-9 of each weight, averaged over the keys; the normaliser sums
 // the unrounded weights), and o once more at the end.
 //
-// Layout of the work: a cluster of C CTAs (1, 2, 4 or 8) of four warps per
-// row.  CTA c takes the row's 64-key blocks c, c + C, ...; each warp gathers
+// Layout of the work: a cluster of C CTAs (1 to 8) of four warps per row.  CTA c takes the row's 64-key blocks c, c + C, ...; each warp gathers
 // the K and V rows of its own 16 keys of a block with 16-byte cp.async copies
 // into its quarter of a ring of kStages blocks (rows XOR-swizzled in 16-B
 // chunks so that ldmatrix reads are conflict-free) and waits only for its own
@@ -33,6 +32,7 @@ constexpr int kWarpKeys = kBlkKeys / kWarps;           // 16 keys of each block 
 constexpr uint32_t kWarpTile = kWarpKeys * kD * 2;     // 4 KB: K (or V) rows of a warp's keys
 constexpr uint32_t kWarpStage = 2 * kWarpTile;         // K then V
 constexpr uint32_t kStageBytes = kWarps * kWarpStage;  // 32 KB: one block
+constexpr int kMaxSplit = 8;                           // CTAs of a row's cluster
 constexpr int kRedLd = kD + 4;                         // padded rows of the merge slabs
 constexpr uint32_t kSlabBytes = kHq * kRedLd * 4;      // one warp's partial O
 constexpr float kLog2e = 1.4426950408889634f;
@@ -46,7 +46,6 @@ constexpr float kLag = 8.f;
 // fill slots 16w..16w+15, its even keys first, so that the lane that gathers keys
 // p, p + 2, ..., p + 14 of the warp reads their rows with two 16-byte loads.
 __device__ __forceinline__ int row_slot(int kr) { return (kr & ~15) + (kr & 1) * 8 + ((kr & 15) >> 1); }
-__device__ __forceinline__ int slot_row(int pos) { return (pos & ~15) + 2 * (pos & 7) + ((pos >> 3) & 1); }
 
 // byte offset of 16-B chunk ch (0..15) of row r in a swizzled [rows][256 B] tile
 __device__ __forceinline__ uint32_t swz(int r, int ch) {
@@ -55,7 +54,9 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
 
 // Gathers the K and V rows of warp w's 16 keys of a block into `st`.  `rows`
 // holds the block's 64 rows as page * page_size + offset (-1: nothing there,
-// zero-filled and masked).
+// zero-filled and masked).  kFlat: pages follow one another without a gap in
+// both buffers, so the row number is the address.
+template <bool kFlat>
 __device__ __forceinline__ void gather_warp(uint32_t st, const CacheView& c, const int32_t* rows, int w, int lane) {
   const int p = lane >> 4, ch = lane & 15;
   const int4 ra = *reinterpret_cast<const int4*>(rows + w * kWarpKeys + p * 8);
@@ -66,18 +67,25 @@ __device__ __forceinline__ void gather_warp(uint32_t st, const CacheView& c, con
   for (int u = 0; u < 8; ++u) {
     const int kl = p + 2 * u;
     const bool ok = r8[u] >= 0;
-    const int64_t page = ok ? r8[u] >> c.shift : 0;
-    const int off = (ok ? r8[u] & mask : 0) * kD + ch * 8;
-    cp_async16(st + swz(kl, ch), c.k + page * c.k_stride + off, ok);
-    cp_async16(st + kWarpTile + swz(kl, ch), c.v + page * c.v_stride + off, ok);
+    const int r = ok ? r8[u] : 0;
+    if (kFlat) {
+      const int64_t src = static_cast<int64_t>(r) * kD + ch * 8;
+      cp_async16(st + swz(kl, ch), c.k + src, ok);
+      cp_async16(st + kWarpTile + swz(kl, ch), c.v + src, ok);
+    } else {
+      const int64_t page = r >> c.shift;
+      const int off = (r & mask) * kD + ch * 8;
+      cp_async16(st + swz(kl, ch), c.k + page * c.k_stride + off, ok);
+      cp_async16(st + kWarpTile + swz(kl, ch), c.v + page * c.v_stride + off, ok);
+    }
   }
 }
 
-template <int kStages, int kC>
+template <int kStages, bool kSplit, bool kFlat>
 __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
     paged_attn_kernel(const CacheView c, const BatchView b, const __nv_bfloat16* __restrict__ q,
                       const int32_t* __restrict__ pool_idx, int topk, float scale_log2, __nv_bfloat16* __restrict__ o,
-                      float* __restrict__ lse, unsigned* status) {
+                      float* __restrict__ lse, int split, unsigned* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 127u) & ~127u;
@@ -86,74 +94,18 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
   // Q is read into registers before the last stage of the ring is first filled
   const uint32_t sQ = base + (kStages - 1) * kStageBytes;
   int32_t* rows = reinterpret_cast<int32_t*>(gbase + kStages * kStageBytes);
-  __shared__ int s_nsel, s_seq;
+  __shared__ int s_nsel;
   __shared__ float s_m[kWarps][kHq], s_l[kWarps][kHq];
   __shared__ float s_cm[kHq], s_cl[kHq];  // this CTA's merged reference and normaliser
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const uint32_t rank = kC > 1 ? cluster_rank() : 0u;
-  const int64_t r = blockIdx.x / kC;
+  const int kC = kSplit ? split : 1;  // CTAs of the row's cluster
+  const int rank = kSplit ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t r = kSplit ? blockIdx.x / static_cast<unsigned>(split) : blockIdx.x;
 
-  // ---- the row's sequence and position; its selected pools (leading non-negative entries)
-  const int32_t* prow = pool_idx + r * topk;
-  if (tid == 0) s_nsel = topk;
-  if (warp == 0) {
-    const int n = warp_locate(b, r, lane);
-    if (lane == 0) s_seq = n;
-  }
-  __syncthreads();
-  {
-    int first = topk;
-    for (int j = tid; j < topk; j += kThreads)
-      if (__ldg(prow + j) < 0) {
-        first = j;
-        break;
-      }
-    first = __reduce_min_sync(0xffffffffu, first);
-    if (lane == 0 && first < topk) atomicMin(&s_nsel, first);
-  }
-  const int seq = s_seq;
-  if (seq >= b.batch) return;  // padding behind the last sequence: every CTA of the cluster leaves here
-  const int64_t i = row_position(b, c.shift, seq, r, status);
-  if (i < 0) return;
-  const int64_t n_elig = i >> 2;
-  __syncthreads();
-  const int nsel = s_nsel;
-  const int nblk_all = (nsel + 1 + kBlkPools - 1) / kBlkPools;
-  const int nblk = nblk_all > static_cast<int>(rank) ? (nblk_all - static_cast<int>(rank) + kC - 1) / kC : 0;
-
-  // Row table of this CTA's blocks.  Slot s < nsel holds pool prow[s]; slot
-  // nsel is the row's own pool; slots beyond are empty.  An entry that is no
-  // eligible pool or breaks ascending order, and a page that is none, are
-  // recorded; nothing is read for them.
-  bool bad = false;
-  const int pshift = c.shift - 2;  // log2(pools per page)
-  for (int e = tid; e < nblk * kBlkKeys; e += kThreads) {
-    const int blk = static_cast<int>(rank) + (e / kBlkKeys) * kC;
-    const int kr = slot_row(e % kBlkKeys);
-    const int slot = blk * kBlkPools + (kr >> 2);
-    int64_t pool = -1;
-    if (slot < nsel) {
-      const int p = __ldg(prow + slot);
-      if (p < n_elig) pool = p;
-      else bad = true;
-      if ((kr & 3) == 0 && slot > 0 && p <= __ldg(prow + slot - 1)) bad = true;
-    } else if (slot == nsel && 4 * n_elig + (kr & 3) <= i) {
-      pool = n_elig;
-    }
-    int32_t row = -1;
-    if (pool >= 0) {
-      const int page = __ldg(b.table + seq * b.table_stride + (pool >> pshift));
-      if (static_cast<unsigned>(page) < static_cast<unsigned>(c.num_pages))
-        row = (page << c.shift) + static_cast<int>(((pool & ((1 << pshift) - 1)) << 2) + (kr & 3));
-      else bad = true;
-    }
-    rows[e] = row;
-  }
-  if (bad) record_status(status, kStatusInternal);
-
-  // ---- Q tile (swizzled) and the gather pipeline prologue
+  // ---- everything that depends on the row's number alone is asked for at
+  // once: Q (swizzled), the selection, the offsets and lengths
   {
     const __nv_bfloat16* qrow = q + r * (kHq * kD);
 #pragma unroll
@@ -163,12 +115,77 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
     }
     cp_async_commit();
   }
+  const int32_t* prow = pool_idx + r * topk;
+  constexpr int kAhead = 4;
+  int sel[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) sel[u] = tid + u * kThreads < topk ? __ldg(prow + tid + u * kThreads) : 0;
+  if (tid == 0) s_nsel = topk;
+  // the row's sequence and position, every warp for itself
+  const RowAt at = warp_locate(b, c.shift, r, lane, warp == 0 ? status : nullptr);
+  if (at.seq < 0 || at.pos < 0) {  // padding behind the last sequence, or a row without a position:
+    cp_async_wait<0>();            // every CTA of the cluster leaves here
+    return;
+  }
+  const int64_t i = at.pos;
+  const int64_t n_elig = i >> 2;
+  // selected pools: the leading non-negative entries
+  int first = topk;
+#pragma unroll
+  for (int u = kAhead - 1; u >= 0; --u)
+    if (sel[u] < 0) first = tid + u * kThreads;
+  for (int j = tid + kAhead * kThreads; j < topk; j += kThreads)
+    if (__ldg(prow + j) < 0) first = min(first, j);
+  __syncthreads();
+  first = __reduce_min_sync(0xffffffffu, first);
+  if (lane == 0 && first < topk) atomicMin(&s_nsel, first);
+  __syncthreads();
+  const int nsel = s_nsel;
+  const int nblk_all = (nsel + 1 + kBlkPools - 1) / kBlkPools;
+  const int nblk = nblk_all > rank ? (nblk_all - rank + kC - 1) / kC : 0;
+
+  // Row table of this CTA's blocks, a pool a thread.  Slot s < nsel holds pool
+  // prow[s]; slot nsel is the row's own pool; slots beyond are empty.  An entry
+  // that is no eligible pool or breaks ascending order, and a page that is
+  // none, are recorded; nothing is read for them.
+  bool bad = false;
+  const int pshift = c.shift - 2;  // log2(pools per page)
+  for (int e = tid; e < nblk * kBlkPools; e += kThreads) {
+    const int lb = e / kBlkPools, in = e % kBlkPools;
+    const int slot = (rank + lb * kC) * kBlkPools + in;
+    int64_t pool = -1;
+    int have = 4;  // tokens of the pool
+    if (slot < nsel) {
+      const int p = __ldg(prow + slot);
+      if (p < n_elig) pool = p;
+      else bad = true;
+      if (slot > 0 && p <= __ldg(prow + slot - 1)) bad = true;
+    } else if (slot == nsel) {
+      pool = n_elig;
+      have = static_cast<int>(i & 3) + 1;
+    }
+    int32_t row = -1;
+    if (pool >= 0) {
+      const int page = __ldg(b.table + at.seq * b.table_stride + (pool >> pshift));
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(c.num_pages))
+        row = (page << c.shift) + static_cast<int>((pool & ((1 << pshift) - 1)) << 2);
+      else bad = true;
+    }
+    // keys 0 and 2 of the pool lie side by side, and so do keys 1 and 3
+    int32_t* to = rows + lb * kBlkKeys + row_slot(4 * in);
+    *reinterpret_cast<int2*>(to) = make_int2(row, row >= 0 && have > 2 ? row + 2 : -1);
+    *reinterpret_cast<int2*>(to + 8) =
+        make_int2(row >= 0 && have > 1 ? row + 1 : -1, row >= 0 && have > 3 ? row + 3 : -1);
+  }
+  if (bad) record_status(status, kStatusInternal);
+
+  // ---- the gather pipeline's prologue
   // the row table is visible; without holes only the row's last block (its
   // own pool and the empty slots after it) needs a mask
   const bool any_hole = __syncthreads_or(bad) != 0;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    if (s < nblk) gather_warp(sKV + s * kStageBytes + warp * kWarpStage, c, rows + s * kBlkKeys, warp, lane);
+    if (s < nblk) gather_warp<kFlat>(sKV + s * kStageBytes + warp * kWarpStage, c, rows + s * kBlkKeys, warp, lane);
     cp_async_commit();
   }
 
@@ -193,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
     {
       const int ahead = lb + kStages - 1;
       const int st = stage == 0 ? kStages - 1 : stage - 1;
-      if (ahead < nblk) gather_warp(sKV + st * kStageBytes + warp * kWarpStage, c, rows + ahead * kBlkKeys, warp, lane);
+      if (ahead < nblk) gather_warp<kFlat>(sKV + st * kStageBytes + warp * kWarpStage, c, rows + ahead * kBlkKeys, warp, lane);
       cp_async_commit();
     }
     const uint32_t sK = sKV + stage * kStageBytes + warp * kWarpStage;
@@ -211,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
       mma_bf16_16816(s1, qa[kk], b2, b3);
     }
     float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-    if (static_cast<int>(rank) + lb * kC + 1 == nblk_all || any_hole) {
+    if (rank + lb * kC + 1 == nblk_all || any_hole) {
       const int key0 = warp * kWarpKeys + 2 * t4;
       const int kc[4] = {key0, key0 + 1, key0 + 8, key0 + 9};
       bool valid[4];
@@ -297,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) L += s_l[w][h] * exp2f(s_m[w][h] - Mu);
     fac[hh] = exp2f(m_run[hh] - Mu);
-    if (kC == 1) fac[hh] /= L;
+    if (!kSplit) fac[hh] /= L;
     if (warp == 0 && t4 == 0) {
-      if (kC == 1) {
+      if (!kSplit) {
         lse[r * kHq + h] = (M + log2f(L)) * kLn2;
       } else {
         s_cm[h] = M;
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
   }
   __syncthreads();
   __nv_bfloat16* orow = o + r * (kHq * kD);
-  if (kC == 1) {
+  if (!kSplit) {
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
       const int e = 2 * (tid + kThreads * m);
@@ -351,30 +368,34 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
       *reinterpret_cast<float4*>(red + at) = y;
     }
     cluster_sync();
-    constexpr int kMine = kHq * kD / kC;  // outputs of this CTA
-    for (int e0 = 4 * tid; e0 < kMine; e0 += 4 * kThreads) {
-      const int e = static_cast<int>(rank) * kMine + e0;
-      const int h = e / kD, col = e % kD;
-      float cm[kC], cl[kC];
+    for (int u4 = rank * kThreads + tid; u4 < kHq * kD / 4; u4 += kC * kThreads) {
+      const int e = 4 * u4, h = e / kD, col = e % kD;
+      float cm[kMaxSplit], cl[kMaxSplit];
+      float4 y[kMaxSplit];
 #pragma unroll
-      for (int u = 0; u < kC; ++u) {
-        cm[u] = cluster_ld_f32(cluster_map(smem_u32(&s_cm[h]), u));
-        cl[u] = cluster_ld_f32(cluster_map(smem_u32(&s_cl[h]), u));
+      for (int u = 0; u < kMaxSplit; ++u) {
+        cm[u] = -INFINITY;
+        cl[u] = 0.f;
+        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (u < kC) {
+          cm[u] = cluster_ld_f32(cluster_map(smem_u32(&s_cm[h]), u));
+          cl[u] = cluster_ld_f32(cluster_map(smem_u32(&s_cl[h]), u));
+          y[u] = cluster_ld_f32x4(cluster_map(smem_u32(red + h * kRedLd + col), u));
+        }
       }
       float M = cm[0];
 #pragma unroll
-      for (int u = 1; u < kC; ++u) M = fmaxf(M, cm[u]);
+      for (int u = 1; u < kMaxSplit; ++u) M = fmaxf(M, cm[u]);
       float L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < kC; ++u) {
+      for (int u = 0; u < kMaxSplit; ++u) {
         const float f = exp2f(cm[u] - M);  // every row has a key of its own: M is finite
-        const float4 y = cluster_ld_f32x4(cluster_map(smem_u32(red + h * kRedLd + col), u));
         L += cl[u] * f;
-        acc.x += y.x * f;
-        acc.y += y.y * f;
-        acc.z += y.z * f;
-        acc.w += y.w * f;
+        acc.x += y[u].x * f;
+        acc.y += y[u].y * f;
+        acc.z += y[u].z * f;
+        acc.w += y[u].w * f;
       }
       const float inv = 1.f / L;
       *reinterpret_cast<uint2*>(orow + e) =
@@ -385,43 +406,61 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
   }
 }
 
-template <int kStages, int kC>
+template <int kStages, bool kSplit, bool kFlat>
 cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
-                           float scale, void* o, float* lse, const LaunchCtx& ctx) {
+                           float scale, void* o, float* lse, int split, const LaunchCtx& ctx) {
   const int blocks = (topk + 1 + kBlkPools - 1) / kBlkPools;
-  const size_t smem = 128 + static_cast<size_t>(kStages) * kStageBytes +
-                      static_cast<size_t>((blocks + kC - 1) / kC) * kBlkKeys * sizeof(int32_t);
+  const size_t fixed = 128 + static_cast<size_t>(kStages) * kStageBytes;
+  const size_t smem = fixed + static_cast<size_t>((blocks + split - 1) / split) * kBlkKeys * sizeof(int32_t);
   constexpr int kMaxBlocks = (2048 + 1 + kBlkPools - 1) / kBlkPools;
+  // (a split of one never has the long ring)
   constexpr size_t kMost = 128 + static_cast<size_t>(kStages) * kStageBytes +
-                           static_cast<size_t>((kMaxBlocks + kC - 1) / kC) * kBlkKeys * sizeof(int32_t);
+                           static_cast<size_t>(kStages == 2 ? kMaxBlocks : (kMaxBlocks + 1) / 2) * kBlkKeys *
+                               sizeof(int32_t);
   static_assert(kMost <= 232448 - 1024, "shared memory per CTA");
   static_assert(kWarps * kSlabBytes <= kStages * kStageBytes, "the merge slabs fit in the ring");
   static std::atomic<bool> attr_done[kAttrDevices];
-  cudaError_t e = set_smem_limit_once(paged_attn_kernel<kStages, kC>, static_cast<int>(kMost), attr_done);
+  cudaError_t e = set_smem_limit_once(paged_attn_kernel<kStages, kSplit, kFlat>, static_cast<int>(kMost), attr_done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(b.rows * kC));
+  cfg.gridDim = dim3(static_cast<unsigned>(b.rows * split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = ctx.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kC;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kC > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<kStages, kC>, c, b, static_cast<const __nv_bfloat16*>(q), pool_idx,
-                            topk, scale * kLog2e, static_cast<__nv_bfloat16*>(o), lse, ctx.status);
+  cfg.numAttrs = kSplit ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<kStages, kSplit, kFlat>, c, b,
+                            static_cast<const __nv_bfloat16*>(q), pool_idx, topk, scale * kLog2e,
+                            static_cast<__nv_bfloat16*>(o), lse, split, ctx.status);
+}
+
+template <int kStages, bool kSplit>
+cudaError_t launch_layout(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
+                          float scale, void* o, float* lse, int split, const LaunchCtx& ctx) {
+  const int64_t page = static_cast<int64_t>(kD) << c.shift;
+  if (c.k_stride == page && c.v_stride == page)
+    return launch_variant<kStages, kSplit, true>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
+  return launch_variant<kStages, kSplit, false>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
                               float scale, void* o, float* lse, const LaunchCtx& ctx) {
-  if (b.rows * 8 <= 2 * ctx.num_sms) return launch_variant<4, 8>(c, b, q, pool_idx, topk, scale, o, lse, ctx);
-  if (b.rows * 4 <= 4 * ctx.num_sms) return launch_variant<2, 4>(c, b, q, pool_idx, topk, scale, o, lse, ctx);
-  return launch_variant<2, 1>(c, b, q, pool_idx, topk, scale, o, lse, ctx);
+  // as many CTAs per row as give every SM two; with one CTA an SM or fewer, a
+  // ring that takes all of a CTA's blocks at once
+  const int64_t fit = 2 * static_cast<int64_t>(ctx.num_sms) / b.rows;
+  const int blocks = (topk + 1 + kBlkPools - 1) / kBlkPools;
+  int split = static_cast<int>(fit < 1 ? 1 : fit < kMaxSplit ? fit : kMaxSplit);
+  split = split < blocks ? split : blocks;
+  if (split == 1) return launch_layout<2, false>(c, b, q, pool_idx, topk, scale, o, lse, 1, ctx);
+  if (b.rows * split <= ctx.num_sms) return launch_layout<6, true>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
+  return launch_layout<2, true>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
 }
 
 }  // namespace dsa

@@ -33,30 +33,36 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int lane = threadIdx.x & 31;
   const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5)) * 4;
   if (r0 >= b.rows) return;
-  // sequences of the four rows: one walk over the offsets
-  int n[4] = {0, 0, 0, 0};
-  for (int j = lane; j < b.batch; j += 32) {
-    const int e = __ldg(b.cu + j + 1);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) n[u] += e <= r0 + u;
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n[u] += __shfl_xor_sync(0xffffffffu, n[u], o);
-
-  // lanes 8u .. 8u+7 work out row r0 + u
+  // the four rows' sequences: one walk over the offsets; lanes 8u .. 8u+7 work out row r0 + u
   const int mine = lane >> 3;
-  const int s = mine == 0 ? n[0] : mine == 1 ? n[1] : mine == 2 ? n[2] : n[3];
   const int64_t row = r0 + mine;
   int page = -1, off = 0, older = 0;  // older: how many of the pool's tokens come before the call's rows
-  if (row < b.rows && s < b.batch) {
-    const int64_t i = row_position(b, c.shift, s, row, status);
-    if (i >= 0) {
-      page = page_of(b, c.num_pages, s, static_cast<int>(i >> c.shift), status);
-      off = static_cast<int>(i & ((1 << c.shift) - 1));
-      const int64_t before = row - __ldg(b.cu + s);  // the call's rows before this one
-      older = static_cast<int>(before < 3 ? 3 - before : 0);
+  for (int j0 = 0; j0 < b.batch; j0 += 32) {
+    const int j = j0 + lane;
+    int c0 = 0, c1 = 0, len = 0;
+    if (j < b.batch) {
+      c0 = __ldg(b.cu + j);
+      c1 = __ldg(b.cu + j + 1);
+      len = __ldg(b.lens + j);
+    }
+    int src = -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const unsigned hit =
+          __ballot_sync(0xffffffffu, j < b.batch && c0 <= r0 + u && r0 + u < c1 && r0 + u < b.rows);
+      if (mine == u && hit != 0u) src = __ffs(hit) - 1;
+    }
+    const int64_t first = __shfl_sync(0xffffffffu, c0, src & 31), last = __shfl_sync(0xffffffffu, c1, src & 31);
+    const int64_t n = __shfl_sync(0xffffffffu, len, src & 31);
+    if (src >= 0) {
+      const int64_t before = row - first, i = n - last + row;  // before: the call's rows of the sequence before this one
+      if (i < before || n > (static_cast<int64_t>(b.max_pages) << c.shift)) {
+        record_status(status, kStatusInternal);
+      } else {
+        page = page_of(b, c.num_pages, j0 + src, static_cast<int>(i >> c.shift), status);
+        off = static_cast<int>(i & ((1 << c.shift) - 1));
+        older = static_cast<int>(before < 3 ? 3 - before : 0);
+      }
     }
   }
   // keys and values: lanes 0..15 the key, 16..31 the value

@@ -24,9 +24,9 @@ constexpr int kDi = 64;
 // head g's (and g + 8's) query as A fragments.  No shared memory, no
 // transposes, 64 bytes of a row per quad of lanes and load.
 //
-// Work items are (sequence, group of kRows rows, 256 pools); every CTA walks
+// Work items are (sequence, group of kRows rows, 128 pools); every CTA walks
 // an equal, contiguous range of them.
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32 * kWarps;  // pools of an item
 constexpr int kRows = 8;            // rows of an item
@@ -85,12 +85,56 @@ __device__ __forceinline__ void item_prefix(int* off, int batch, F&& items_of) {
   __syncthreads();
 }
 
+// A stretch of a CTA's walk: pools [p0, p1) of one sequence, a tile of 128 at a
+// time, against up to kRows of its rows.
+struct Run {
+  int64_t ra;            // first row
+  const int32_t* table;  // the sequence's pages
+  int nr;                // rows; 0: the walk has ended
+  int pools;             // pools that the last row may see
+  int p0, p1;            // multiples of 128 (p1 may lie past `pools`)
+};
+
+// The run that begins at item `*it` (or at the first one behind it that has
+// anything to score) and ends with its rows, or with the walk at it1; moves
+// *it past it.  *s is a cursor that only moves forward.
+__device__ __noinline__ Run next_run(const BatchView& b, int shift, const int* off, int64_t row0, int64_t row1,
+                                     int it1, int* it, int* s) {
+  Run x;
+  x.nr = 0;
+  while (*it < it1) {
+    while (*s + 1 < b.batch && *it >= off[*s + 1]) ++*s;
+    int64_t first;
+    const int n = seq_rows(b, *s, row0, row1, &first);
+    const int tiles = static_cast<int>((seq_pools(b, shift, *s, first, n) + kTile - 1) / kTile);
+    if (tiles == 0) {
+      ++*it;
+      continue;
+    }
+    const int rg = (*it - off[*s]) / tiles, tile = (*it - off[*s]) % tiles;
+    const int many = min(tiles - tile, it1 - *it);
+    *it += many;
+    x.ra = first + static_cast<int64_t>(rg) * kRows;
+    x.nr = static_cast<int>(min(static_cast<int64_t>(kRows), first + n - x.ra));
+    if (x.nr > 0) {
+      x.pools = static_cast<int>(seq_pools(b, shift, *s, x.ra, x.nr));
+      x.p0 = tile * kTile;
+      x.p1 = min((tile + many) * kTile, (x.pools + kTile - 1) / kTile * kTile);
+      x.table = b.table + *s * b.table_stride;
+      if (x.p0 < x.p1) return x;
+    }
+    x.nr = 0;
+  }
+  return x;
+}
+
 template <int kMt>
-__global__ void __launch_bounds__(kThreads, kMt <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
     paged_score_kernel(const CacheView c, const BatchView b, const __nv_bfloat16* __restrict__ q,
                        const float* __restrict__ w, int Hi, int64_t row0, int64_t row1, float* __restrict__ scores,
                        int64_t ld, unsigned* status) {
   extern __shared__ int off[];
+
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   item_prefix(off, b.batch, [&](int s) {
@@ -102,53 +146,61 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 2 : 1)
     return static_cast<int>(items < kMaxItems ? items : kMaxItems);
   });
   const int total = off[b.batch];
-  const int it0 = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
+  int it = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
   const int it1 = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
-  if (it0 >= it1) return;
+  if (it >= it1) return;
   int s = 0;
   {
-    int lo = 0, hi = b.batch - 1;  // the last sequence whose first item is at or before it0
+    int lo = 0, hi = b.batch - 1;  // the last sequence whose first item is at or before `it`
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (off[mid] <= it0) lo = mid;
+      if (off[mid] <= it) lo = mid;
       else hi = mid - 1;
     }
     s = lo;
   }
+  const int pshift = c.shift - 2, pmask = (1 << pshift) - 1;
+  // this lane's piece of pool p + 8 * nt + g of a run (p: the warp's first pool of a tile); null past the row's
+  // pools or without a page
+  auto source = [&](const Run& x, int p, int nt) -> const uint4* {
+    p += nt * 8 + g;
+    if (p >= x.pools) return nullptr;
+    const int page = __ldg(x.table + (p >> pshift));
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) {
+      record_status(status, kStatusInternal);
+      return nullptr;
+    }
+    return reinterpret_cast<const uint4*>(c.khat + page * c.khat_stride + (p & pmask) * (2 * kDi)) + t;
+  };
+  uint4 kf[4][4];
+  auto fetch = [&](uint4 (&k)[4], const uint4* src) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = src ? __ldcs(src + 4 * e) : make_uint4(0u, 0u, 0u, 0u);
+  };
   uint4 qa[kMt][2][2];  // [m-tile][head g / g + 8][half of the 64 dims]
   float wv[kMt][2];
   int64_t in_regs = -1;  // the row whose query they hold
-  const int pshift = c.shift - 2;
-  for (int it = it0; it < it1; ++it) {
-    while (s + 1 < b.batch && it >= off[s + 1]) ++s;
-    int64_t first;
-    const int n = seq_rows(b, s, row0, row1, &first);
-    const int tiles = static_cast<int>((seq_pools(b, c.shift, s, first, n) + kTile - 1) / kTile);
-    if (tiles == 0) continue;
-    const int rg = (it - off[s]) / tiles, tile = (it - off[s]) % tiles;
-    const int64_t ra = first + rg * kRows;
-    const int nr = static_cast<int>(min(static_cast<int64_t>(kRows), first + n - ra));
-    if (nr <= 0) continue;
-    const int64_t pools = seq_pools(b, c.shift, s, ra, nr);  // of this group's last row
-    const int64_t p0 = static_cast<int64_t>(tile) * kTile + warp * 32;
-    if (p0 >= pools) continue;
-    // pooled keys of the warp's 32 pools
-    uint4 kf[4][4];
+
+  // The pooled keys of the next tile are fetched n-tile by n-tile into the
+  // registers that the last row of this one has just used, so that the loads
+  // of three n-tiles are always in flight behind the products of the fourth.
+  Run cur = next_run(b, c.shift, off, row0, row1, it1, &it, &s);
+  if (cur.nr == 0) return;
+  int p = cur.p0 + warp * 32;  // the warp's first pool
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const int64_t p = p0 + nt * 8 + g;
-      const uint4* src = nullptr;
-      if (p < pools) {
-        const int page = page_of(b, c.num_pages, s, static_cast<int>(p >> pshift), status);
-        if (page >= 0)
-          src = reinterpret_cast<const uint4*>(c.khat + page * c.khat_stride +
-                                               (p & ((1 << pshift) - 1)) * (2 * kDi));
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) kf[nt][e] = src ? __ldg(src + t + 4 * e) : make_uint4(0u, 0u, 0u, 0u);
+  for (int nt = 0; nt < 4; ++nt) fetch(kf[nt], source(cur, p, nt));
+  while (true) {
+    Run nxt = cur;
+    int pn = p + kTile;
+    if (pn >= cur.p1) {
+      nxt = next_run(b, c.shift, off, row0, row1, it1, &it, &s);
+      pn = nxt.p0 + warp * 32;
     }
-    for (int rr = 0; rr < nr; ++rr) {
-      const int64_t row = ra + rr;
+    const uint4* ahead[4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) ahead[nt] = nxt.nr > 0 ? source(nxt, pn, nt) : nullptr;
+    for (int rr = 0; rr < cur.nr; ++rr) {
+      const int64_t row = cur.ra + rr;
       if (in_regs != row) {
         in_regs = row;
 #pragma unroll
@@ -162,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 2 : 1)
             wv[m][u] = h < Hi ? __ldg(w + row * Hi + h) : 0.f;
           }
       }
+      const bool last = rr + 1 == cur.nr;
       float v[4][2];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
@@ -181,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 2 : 1)
           v[nt][0] = fmaf(wv[m][1], fmaxf(acc[2], 0.f), v[nt][0]);
           v[nt][1] = fmaf(wv[m][1], fmaxf(acc[3], 0.f), v[nt][1]);
         }
+        if (last) fetch(kf[nt], ahead[nt]);
       }
       // sum over the 8 head lanes, scattering the 8 values over them
       const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
@@ -199,9 +253,12 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 2 : 1)
         x1[z] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
       }
       const float sum = (b2 ? x1[1] : x1[0]) + __shfl_xor_sync(0xffffffffu, b2 ? x1[0] : x1[1], 4);
-      const int64_t p = p0 + (b4 ? 16 : 0) + (b3 ? 8 : 0) + 2 * t + (b2 ? 1 : 0);
-      if (p < pools) scores[(row - row0) * ld + p] = sum;
+      const int at = p + (b4 ? 16 : 0) + (b3 ? 8 : 0) + 2 * t + (b2 ? 1 : 0);
+      if (at < cur.pools) scores[(row - row0) * ld + at] = sum;
     }
+    if (nxt.nr == 0) return;
+    cur = nxt;
+    p = pn;
   }
 }
 
@@ -223,10 +280,9 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 2 : 1)
 // Lists and not sorted keys: a row of 32768 costs one read of 128 KB and work
 // on about 1200 candidates; several rows share an SM and hide each other's
 // barriers.
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kFew = kSelThreads;
+constexpr int kFew = 512;
+constexpr int kSelMaxWarps = 32;
 constexpr int kSegment = 1 << 18;  // pools whose bits are held at once (2 x 32 KB of bits)
 
 // The order-preserving 32-bit image of a score (-0 and +0 are one), and the
@@ -243,60 +299,70 @@ __device__ __forceinline__ float key_score(uint32_t k) {
 struct alignas(16) SelSmem {
   uint32_t hist[kBins];
   uint32_t few[kFew];
-  uint32_t wred[2][kSelWarps];
+  uint32_t wred[2][2][kSelMaxWarps];  // two buffers, used in turn: one barrier a reduction
   uint32_t lo, hi;
-  uint32_t nfew, nlist;
+  uint32_t nfew;
   uint32_t bin, above, inbin;
   uint32_t T, take;
-  int seq;
 };
 static_assert(sizeof(SelSmem) % 16 == 0, "what lies after it is read 16 bytes at a time");
 
 // extrema over the block; every thread gets them
-__device__ __forceinline__ void sel_minmax(SelSmem& sm, uint32_t& lo, uint32_t& hi) {
+template <int kThr>
+__device__ __forceinline__ void sel_minmax(SelSmem& sm, uint32_t& lo, uint32_t& hi, int& turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
-    sm.wred[0][warp] = lo;
-    sm.wred[1][warp] = hi;
+    sm.wred[turn][0][warp] = lo;
+    sm.wred[turn][1][warp] = hi;
   }
   __syncthreads();
-  lo = __reduce_min_sync(0xffffffffu, lane < kSelWarps ? sm.wred[0][lane] : 0xFFFFFFFFu);
-  hi = __reduce_max_sync(0xffffffffu, lane < kSelWarps ? sm.wred[1][lane] : 0u);
-  __syncthreads();  // read: wred may be written again
+  lo = __reduce_min_sync(0xffffffffu, lane < kThr / 32 ? sm.wred[turn][0][lane] : 0xFFFFFFFFu);
+  hi = __reduce_max_sync(0xffffffffu, lane < kThr / 32 ? sm.wred[turn][1][lane] : 0u);
+  turn ^= 1;
 }
 
-// Exclusive prefix of v over the block in thread order, and the total.
-__device__ __forceinline__ uint32_t sel_scan(SelSmem& sm, uint32_t v, uint32_t* total) {
+// Exclusive prefixes of v and u over the block in thread order, and their totals.
+template <int kThr>
+__device__ __forceinline__ void sel_scan2(SelSmem& sm, uint32_t& v, uint32_t& u, uint32_t* v_all, uint32_t* u_all,
+                                          int& turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+  uint32_t x = v, y = u;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const uint32_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+    }
   }
-  if (lane == 31) sm.wred[0][warp] = x;
+  if (lane == 31) {
+    sm.wred[turn][0][warp] = x;
+    sm.wred[turn][1][warp] = y;
+  }
   __syncthreads();
-  const uint32_t w = lane < kSelWarps ? sm.wred[0][lane] : 0u;
-  *total = __reduce_add_sync(0xffffffffu, w);
-  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
-  __syncthreads();
-  return before + x - v;
+  const uint32_t wx = lane < kThr / 32 ? sm.wred[turn][0][lane] : 0u, wy = lane < kThr / 32 ? sm.wred[turn][1][lane] : 0u;
+  *v_all = __reduce_add_sync(0xffffffffu, wx);
+  *u_all = __reduce_add_sync(0xffffffffu, wy);
+  v = __reduce_add_sync(0xffffffffu, lane < warp ? wx : 0u) + x - v;
+  u = __reduce_add_sync(0xffffffffu, lane < warp ? wy : 0u) + y - u;
+  turn ^= 1;
 }
 
 // The bin of the complete histogram (a barrier precedes) that holds the need-th
 // largest: sm.bin, sm.above (scores in higher bins), sm.inbin.
-__device__ __forceinline__ void sel_find(SelSmem& sm, uint32_t need) {
-  constexpr int kPer = kBins / kSelThreads;
+template <int kThr>
+__device__ __forceinline__ void sel_find(SelSmem& sm, uint32_t need, int& turn) {
+  constexpr int kPer = kBins / kThr;
   uint32_t cnt[kPer], sum = 0;  // bins in descending order: thread 0 has the highest
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     cnt[j] = sm.hist[kBins - 1 - (kPer * threadIdx.x + j)];
     sum += cnt[j];
   }
-  uint32_t all;
-  uint32_t before = sel_scan(sm, sum, &all);
+  uint32_t before = sum, none = 0u, all, zero;
+  sel_scan2<kThr>(sm, before, none, &all, &zero, turn);
   if (before < need && need <= before + sum) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -311,8 +377,9 @@ __device__ __forceinline__ void sel_find(SelSmem& sm, uint32_t need) {
   __syncthreads();
 }
 
-// Equal steps of the score between two keys: bin(f) is monotone in f.  inv = 0
-// where the range is not finite or empty.
+// Equal steps of the score between two keys: bin(f) is monotone in f (scores
+// outside fall into the first and the last).  inv = 0 where the range is not
+// finite or empty.
 struct Steps {
   float lo, inv;
   __device__ __forceinline__ static Steps of(uint32_t klo, uint32_t khi) {
@@ -322,111 +389,97 @@ struct Steps {
     s.inv = range > 0.f && range < INFINITY ? fminf(static_cast<float>(kBins) / range, 3.0e38f) : 0.f;
     return s;
   }
-  __device__ __forceinline__ float at(float f) const { return (f - lo) * inv; }
   __device__ __forceinline__ int bin(float f) const {
-    const float x = at(f);
-    return x >= static_cast<float>(kBins - 1) ? kBins - 1 : static_cast<int>(x);
+    return static_cast<int>(fminf(fmaxf((f - lo) * inv, 0.f), static_cast<float>(kBins - 1)));
   }
 };
 
-// The need-th largest of the cnt > need scores that `each(f)` walks (f(score),
-// every thread its share): key T, and how many scores equal to it are among
-// the need largest.
-template <typename Each>
-__device__ __forceinline__ void sel_kth(SelSmem& sm, uint32_t need, uint32_t cnt, Each&& each, uint32_t* T,
-                                        uint32_t* take) {
+// The need-th largest of the cnt > need scores at v (shared or global memory):
+// key T, and how many scores equal to it are among the need largest.  sm.hist
+// is their complete histogram by st (a barrier has passed since), or st.inv is
+// 0; sm.nfew is zero.
+template <int kThr>
+__device__ __forceinline__ void sel_kth(SelSmem& sm, uint32_t need, int cnt, const float* v, const Steps& st,
+                                        uint32_t* T, uint32_t* take, int& turn) {
   const int tid = threadIdx.x;
-  for (int j = tid; j < kBins; j += kSelThreads) sm.hist[j] = 0u;
-  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-  each([&](float f) {
-    const uint32_t k = score_key(f);
-    lo = min(lo, k);
-    hi = max(hi, k);
-  });
-  sel_minmax(sm, lo, hi);
-  if (lo != hi) {
-    const Steps st = Steps::of(lo, hi);
-    uint32_t members = cnt;
-    int bin0 = -1;  // -1: every score
-    if (st.inv > 0.f) {
-      each([&](float f) { atomicAdd(&sm.hist[st.bin(f)], 1u); });
-      __syncthreads();
-      sel_find(sm, need);
-      members = sm.inbin;
-      need -= sm.above;
-      bin0 = static_cast<int>(sm.bin);
-    }
-    bool windowed = false;  // the members are the scores with keys in [lo, hi]
-    auto inside = [&](float f, uint32_t k) {
-      return windowed ? k >= lo && k <= hi : bin0 < 0 || st.bin(f) == bin0;
-    };
-    while (members > static_cast<uint32_t>(kFew)) {
-      uint32_t a = 0xFFFFFFFFu, z = 0u;
-      each([&](float f) {
-        const uint32_t k = score_key(f);
-        if (inside(f, k)) {
-          a = min(a, k);
-          z = max(z, k);
-        }
-      });
-      for (int j = tid; j < kBins; j += kSelThreads) sm.hist[j] = 0u;
-      sel_minmax(sm, a, z);
-      lo = a;
-      hi = z;
-      windowed = true;
-      if (lo == hi) break;
-      const int bits = 32 - __clz(hi - lo);
-      const int sh = bits > 11 ? bits - 11 : 0;
-      each([&](float f) {
-        const uint32_t k = score_key(f);
-        if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> sh], 1u);
-      });
-      __syncthreads();
-      sel_find(sm, need);
-      members = sm.inbin;
-      need -= sm.above;
-      const uint32_t nlo = lo + (sm.bin << sh);
-      const uint64_t nhi = static_cast<uint64_t>(nlo) + ((1ull << sh) - 1ull);
-      lo = nlo;
-      hi = nhi < hi ? static_cast<uint32_t>(nhi) : hi;
-      if (sh == 0) break;
-    }
-    if (!(windowed && lo == hi)) {
-      if (tid == 0) sm.nfew = 0u;
-      __syncthreads();
-      each([&](float f) {
-        const uint32_t k = score_key(f);
-        if (inside(f, k)) {
-          const uint32_t at = atomicAdd(&sm.nfew, 1u);
-          if (at < static_cast<uint32_t>(kFew)) sm.few[at] = k;
-        }
-      });
-      __syncthreads();
-      const uint32_t m = min(sm.nfew, static_cast<uint32_t>(kFew));
-      if (tid < static_cast<int>(m)) {
-        const uint32_t mine = sm.few[tid];
-        uint32_t gt = 0u, eq = 0u;
-        for (uint32_t e = 0; e < m; ++e) {
-          gt += sm.few[e] > mine;
-          eq += sm.few[e] == mine;
-        }
-        if (gt < need && need <= gt + eq) {  // every thread with T writes the same
-          sm.T = mine;
-          sm.take = need - gt;
-        }
+  uint32_t lo = 0u, hi = 0u, members = static_cast<uint32_t>(cnt);
+  int bin0 = -1;  // -1: every score
+  if (st.inv > 0.f) {
+    sel_find<kThr>(sm, need, turn);
+    members = sm.inbin;
+    need -= sm.above;
+    bin0 = static_cast<int>(sm.bin);
+  }
+  bool windowed = false;  // the members are the scores with keys in [lo, hi]
+  auto inside = [&](float f, uint32_t k) {
+    return windowed ? k >= lo && k <= hi : bin0 < 0 || st.bin(f) == bin0;
+  };
+  while (members > static_cast<uint32_t>(kFew)) {
+    uint32_t a = 0xFFFFFFFFu, z = 0u;
+    for (int j = tid; j < cnt; j += kThr) {
+      const float f = v[j];
+      const uint32_t k = score_key(f);
+      if (inside(f, k)) {
+        a = min(a, k);
+        z = max(z, k);
       }
-      __syncthreads();
-      *T = sm.T;
-      *take = sm.take;
-      return;
+    }
+    for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
+    sel_minmax<kThr>(sm, a, z, turn);
+    lo = a;
+    hi = z;
+    windowed = true;
+    if (lo == hi) break;
+    const int bits = 32 - __clz(hi - lo);
+    const int sh = bits > 11 ? bits - 11 : 0;
+    for (int j = tid; j < cnt; j += kThr) {
+      const uint32_t k = score_key(v[j]);
+      if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> sh], 1u);
+    }
+    __syncthreads();
+    sel_find<kThr>(sm, need, turn);
+    members = sm.inbin;
+    need -= sm.above;
+    const uint32_t nlo = lo + (sm.bin << sh);
+    const uint64_t nhi = static_cast<uint64_t>(nlo) + ((1ull << sh) - 1ull);
+    lo = nlo;
+    hi = nhi < hi ? static_cast<uint32_t>(nhi) : hi;
+    if (sh == 0) break;
+  }
+  if (windowed && lo == hi) {
+    *T = lo;
+    *take = need;
+    return;
+  }
+  for (int j = tid; j < cnt; j += kThr) {
+    const float f = v[j];
+    const uint32_t k = score_key(f);
+    if (inside(f, k)) {
+      const uint32_t at = atomicAdd(&sm.nfew, 1u);
+      if (at < static_cast<uint32_t>(kFew)) sm.few[at] = k;
     }
   }
-  *T = lo;
-  *take = need;
+  __syncthreads();
+  const uint32_t m = min(sm.nfew, static_cast<uint32_t>(kFew));
+  if (tid < static_cast<int>(m)) {
+    const uint32_t mine = sm.few[tid];
+    uint32_t gt = 0u, eq = 0u;
+    for (uint32_t e = 0; e < m; ++e) {
+      gt += sm.few[e] > mine;
+      eq += sm.few[e] == mine;
+    }
+    if (gt < need && need <= gt + eq) {  // every thread with T writes the same
+      sm.T = mine;
+      sm.take = need - gt;
+    }
+  }
+  __syncthreads();
+  *T = sm.T;
+  *take = sm.take;
 }
 
-template <int kCap>
-__global__ void __launch_bounds__(kSelThreads, kCap <= 4096 ? 3 : 2)
+template <int kCap, int kThr>
+__global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kCap <= 4096 ? 3 : 2)
     paged_select_kernel(const BatchView b, int shift, int64_t row0, const float* __restrict__ scores, int64_t ld,
                         int topk, int words_room, int32_t* __restrict__ pool_idx, unsigned* status) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -437,147 +490,150 @@ __global__ void __launch_bounds__(kSelThreads, kCap <= 4096 ? 3 : 2)
   uint32_t* equal = above + words_room;                                   // [words_room] bits: scores equal to T
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t lrow = blockIdx.x, row = row0 + lrow;
-  if (warp == 0) {
-    const int n = warp_locate(b, row, lane);
-    if (lane == 0) {
-      sm.seq = n;
-      sm.nlist = 0u;
-    }
-  }
-  __syncthreads();
-  const int seq = sm.seq;
-  if (seq >= b.batch) return;  // padding behind the last sequence
-  const int64_t i = row_position(b, shift, seq, row, status);
+  int turn = 0;
+  if (tid == 0) sm.nfew = 0u;
+  for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
+  const RowAt at = warp_locate(b, shift, row, lane, status);
+  pdl_wait();  // the scores are written (what was read above is older than their launch)
+  if (at.seq < 0) return;  // padding behind the last sequence
   int32_t* orow = pool_idx + row * topk;
-  const int n = i < 0 ? 0 : static_cast<int>(i >> 2);
+  const int n = at.pos < 0 ? 0 : static_cast<int>(at.pos >> 2);
   if (n <= topk) {  // every pool (or, for a row without a position, nothing)
-    for (int j = tid; j < topk; j += kSelThreads) orow[j] = j < n ? j : -1;
+    for (int j = tid; j < topk; j += kThr) orow[j] = j < n ? j : -1;
     return;
   }
   const float* srow = scores + lrow * ld;
+  for (int k = tid; k < min(kSegment, n + 31) >> 5; k += kThr) above[k] = equal[k] = 0u;
 
   // ---- candidates
   bool listed = n <= kCap;
+  int m = n;  // scores that T is looked for in: the list's, or the row's
+  Steps st{0.f, 0.f};
   if (listed) {
-    for (int j = tid; j < n; j += kSelThreads) {
+    for (int j = tid; j < n; j += kThr) {
       cval[j] = srow[j];
       cidx[j] = j;
     }
-    if (tid == 0) sm.nlist = static_cast<uint32_t>(n);
   } else {
-    // quads (4 consecutive scores) of the sample: 2 a thread, 8 beyond 2^16 pools
-    const int nq = n >> 2, per = n > 65536 ? 8 : 2;
-    float4 q[8];
+    // quads (4 consecutive scores) of the sample: 1024 in all, 4096 beyond 2^16 pools
+    constexpr int kQuads = 1024 / kThr;
+    const int nq = n >> 2, per = n > 65536 ? 4 * kQuads : kQuads;
+    auto quad = [&](int u) {
+      return *reinterpret_cast<const float4*>(
+          srow + 4 * (static_cast<int64_t>(u * kThr + tid) * nq / (per * kThr)));
+    };
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (u >= per) break;
-      const int64_t k = static_cast<int64_t>(u * kSelThreads + tid) * nq / (per * kSelThreads);
-      q[u] = *reinterpret_cast<const float4*>(srow + 4 * k);
-    }
-    for (int j = tid; j < kBins; j += kSelThreads) sm.hist[j] = 0u;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (u >= per) break;
-      const uint32_t k0 = score_key(q[u].x), k1 = score_key(q[u].y), k2 = score_key(q[u].z), k3 = score_key(q[u].w);
+#pragma unroll 2
+    for (int u = 0; u < per; ++u) {
+      const float4 q = quad(u);
+      const uint32_t k0 = score_key(q.x), k1 = score_key(q.y), k2 = score_key(q.z), k3 = score_key(q.w);
       lo = min(min(lo, min(k0, k1)), min(k2, k3));
       hi = max(max(hi, max(k0, k1)), max(k2, k3));
     }
-    sel_minmax(sm, lo, hi);
-    const Steps st = Steps::of(lo, hi);
+    sel_minmax<kThr>(sm, lo, hi, turn);
+    st = Steps::of(lo, hi);
     if (st.inv > 0.f) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (u >= per) break;
-        atomicAdd(&sm.hist[st.bin(q[u].x)], 1u);
-        atomicAdd(&sm.hist[st.bin(q[u].y)], 1u);
-        atomicAdd(&sm.hist[st.bin(q[u].z)], 1u);
-        atomicAdd(&sm.hist[st.bin(q[u].w)], 1u);
+#pragma unroll 2
+      for (int u = 0; u < per; ++u) {  // (from L1)
+        const float4 q = quad(u);
+        atomicAdd(&sm.hist[st.bin(q.x)], 1u);
+        atomicAdd(&sm.hist[st.bin(q.y)], 1u);
+        atomicAdd(&sm.hist[st.bin(q.z)], 1u);
+        atomicAdd(&sm.hist[st.bin(q.w)], 1u);
       }
       __syncthreads();
       // c candidates with c - 5 sqrt(c sigma) = topk, sigma scores a sample
-      const float sigma = static_cast<float>(n) / static_cast<float>(4 * per * kSelThreads);
+      const float sigma = static_cast<float>(n) / static_cast<float>(4 * per * kThr);
       const float rc = 0.5f * (5.f * sqrtf(sigma) + sqrtf(25.f * sigma + 4.f * static_cast<float>(topk)));
-      const int want = min(static_cast<int>(rc * rc / sigma) + 1, 4 * per * kSelThreads);
-      sel_find(sm, static_cast<uint32_t>(want));
-      const float edge = static_cast<float>(sm.bin);
-      // one pass over the row; four 16-byte loads in flight a thread
-      constexpr int kU = 4;
-      for (int j0 = 0; j0 < n; j0 += 4 * kU * kSelThreads) {
+      const int want = min(static_cast<int>(rc * rc / sigma) + 1, 4 * per * kThr);
+      sel_find<kThr>(sm, static_cast<uint32_t>(want), turn);
+      // the threshold, near that bin's lower edge; the list's own histogram has its steps between it and the
+      // sample's maximum (the few above fall into the last bin)
+      const float t = st.lo + static_cast<float>(sm.bin) / st.inv;
+      st = Steps::of(score_key(t), hi);
+      for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
+      // one pass over the row: kU 16-byte loads in flight a thread, its hits counted, their places from a scan
+      constexpr int kU = kThr == 1024 ? 8 : 4;
+      uint32_t listed_before = 0u;
+      for (int j0 = 0; j0 < n; j0 += 4 * kU * kThr) {
         float4 x[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int j = j0 + 4 * (u * kSelThreads + tid);
-          if (j + 3 < n) x[u] = *reinterpret_cast<const float4*>(srow + j);
-          else {
-            x[u].x = j < n ? srow[j] : -INFINITY;
-            x[u].y = j + 1 < n ? srow[j + 1] : -INFINITY;
-            x[u].z = j + 2 < n ? srow[j + 2] : -INFINITY;
-            x[u].w = -INFINITY;
+          const int j = j0 + 4 * (u * kThr + tid);
+          x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j < n) x[u] = *reinterpret_cast<const float4*>(srow + j);  // (rows are whole quads)
+        }
+        uint32_t hit = 0u;  // bit 4 u + e
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          hit |= (static_cast<uint32_t>(x[u].x >= t) | (static_cast<uint32_t>(x[u].y >= t) << 1) |
+                  (static_cast<uint32_t>(x[u].z >= t) << 2) | (static_cast<uint32_t>(x[u].w >= t) << 3)) << (4 * u);
+        if (j0 + 4 * kU * kThr > n) {  // the row's end: only what lies before it
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int left = min(max(n - (j0 + 4 * (u * kThr + tid)), 0), 4);
+            hit &= ~((0xFu & ~((1u << left) - 1u)) << (4 * u));
           }
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int j = j0 + 4 * (u * kSelThreads + tid);
-          const float f[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-          bool hit[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) hit[e] = st.at(f[e]) >= edge && j + e < n;
-          if (!__any_sync(0xffffffffu, hit[0] || hit[1] || hit[2] || hit[3])) continue;
-          uint32_t m[4], all = 0u;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            m[e] = __ballot_sync(0xffffffffu, hit[e]);
-            all += __popc(m[e]);
+        uint32_t to = __popc(hit), none = 0u, all, zero;
+        sel_scan2<kThr>(sm, to, none, &all, &zero, turn);  // (its barrier also orders the histogram's zeroes)
+        to += listed_before;
+        listed_before += all;
+        // every lane walks only its own hits (and reads them again, from L1)
+        while (hit) {
+          const int z = __ffs(hit) - 1, j = j0 + 4 * ((z >> 2) * kThr + tid) + (z & 3);
+          hit &= hit - 1u;
+          if (to < static_cast<uint32_t>(kCap)) {
+            const float f = srow[j];
+            cval[to] = f;
+            cidx[to] = j;
+            atomicAdd(&sm.hist[st.bin(f)], 1u);
           }
-          uint32_t at = 0u;
-          if (lane == 0) at = atomicAdd(&sm.nlist, all);
-          at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t to = at + __popc(m[e] & ((1u << lane) - 1u));
-            if (hit[e] && to < static_cast<uint32_t>(kCap)) {
-              cval[to] = f[e];
-              cidx[to] = j + e;
-            }
-            at += __popc(m[e]);
-          }
+          ++to;
         }
       }
-      __syncthreads();
-      listed = sm.nlist >= static_cast<uint32_t>(topk) && sm.nlist <= static_cast<uint32_t>(kCap);
+      m = static_cast<int>(min(listed_before, 0x7FFFFFFFu));
+      listed = m >= topk && m <= kCap;
+      if (!listed) m = n;
     }
   }
+  if (!listed || n <= kCap) {  // no histogram yet: of the short row's list, or of the row itself
+    __syncthreads();
+    for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
+    const float* v = listed ? cval : srow;
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+    for (int j = tid; j < m; j += kThr) {
+      const uint32_t k = score_key(v[j]);
+      lo = min(lo, k);
+      hi = max(hi, k);
+    }
+    sel_minmax<kThr>(sm, lo, hi, turn);
+    st = Steps::of(lo, hi);
+    if (st.inv > 0.f)
+      for (int j = tid; j < m; j += kThr) atomicAdd(&sm.hist[st.bin(v[j])], 1u);
+  }
   __syncthreads();
-  const int m = static_cast<int>(sm.nlist);
 
-  // ---- T
-  uint32_t T = 0u, take = 0u;
-  if (listed && m > topk) {
-    sel_kth(sm, static_cast<uint32_t>(topk), static_cast<uint32_t>(m), [&](auto&& f) {
-      for (int j = tid; j < m; j += kSelThreads) f(cval[j]);
-    }, &T, &take);
-  } else if (!listed) {
-    sel_kth(sm, static_cast<uint32_t>(topk), static_cast<uint32_t>(n), [&](auto&& f) {
-      for (int j = tid; j < n; j += kSelThreads) f(srow[j]);
-    }, &T, &take);
-  }  // a list of exactly topk scores is kept whole: every key is above T = 0 (no score's), or equal to it
+  // ---- T: of the list, or of the row itself
+  uint32_t T = 0u, take = static_cast<uint32_t>(topk);  // a list of topk scores is kept whole: no key is below 0
+  if (m > topk) sel_kth<kThr>(sm, static_cast<uint32_t>(topk), m, listed ? cval : srow, st, &T, &take, turn);
 
   // ---- the row, segment by segment
   uint32_t done = 0u, ties = 0u;  // written so far; ties met so far
-  if (listed && m == topk) take = static_cast<uint32_t>(topk);
   for (int s0 = 0; s0 < n; s0 += kSegment) {
     const int len = min(kSegment, n - s0), words = (len + 31) >> 5;
     if (listed) {
-      for (int k = tid; k < words; k += kSelThreads) above[k] = equal[k] = 0u;
-      __syncthreads();
-      for (int j = tid; j < m; j += kSelThreads) {
+      if (s0 > 0) {
+        for (int k = tid; k < words; k += kThr) above[k] = equal[k] = 0u;
+        __syncthreads();
+      }
+      for (int j = tid; j < m; j += kThr) {
         const int p = cidx[j] - s0;
         const uint32_t k = score_key(cval[j]);
         if (p >= 0 && p < len && k >= T) atomicOr((k > T ? above : equal) + (p >> 5), 1u << (p & 31));
       }
     } else {
-      for (int k = warp; k < words; k += kSelWarps) {
+      for (int k = warp; k < words; k += kThr / 32) {
         const int j = s0 + 32 * k + lane;
         const uint32_t key = j < n ? score_key(srow[j]) : 0u;
         const uint32_t g = __ballot_sync(0xffffffffu, j < n && key > T), e = __ballot_sync(0xffffffffu, j < n && key == T);
@@ -588,17 +644,16 @@ __global__ void __launch_bounds__(kSelThreads, kCap <= 4096 ? 3 : 2)
       }
     }
     __syncthreads();
-    const int wpt = (words + kSelThreads - 1) / kSelThreads;
+    const int wpt = (words + kThr - 1) / kThr;
     const int k0 = min(tid * wpt, words), k1 = min(k0 + wpt, words);
-    uint32_t g = 0u, e = 0u;
+    uint32_t g = 0u, e = 0u, g_all, e_all;
     for (int k = k0; k < k1; ++k) {
       g += __popc(above[k]);
       e += __popc(equal[k]);
     }
-    uint32_t g_all, e_all;
-    uint32_t pe = ties + sel_scan(sm, e, &e_all);
-    const uint32_t pg = sel_scan(sm, g, &g_all);
-    uint32_t pos = done + pg + (min(pe, take) - min(ties, take));
+    sel_scan2<kThr>(sm, g, e, &g_all, &e_all, turn);
+    uint32_t pe = ties + e;
+    uint32_t pos = done + g + (min(pe, take) - min(ties, take));
     for (int k = k0; k < k1; ++k) {
       const uint32_t ek = equal[k];
       uint32_t bits = above[k] | ek;
@@ -613,7 +668,7 @@ __global__ void __launch_bounds__(kSelThreads, kCap <= 4096 ? 3 : 2)
     }
     done += g_all + (min(ties + e_all, take) - min(ties, take));
     ties += e_all;
-    __syncthreads();  // the bits are read: the next segment may set its own
+    if (s0 + kSegment < n) __syncthreads();  // the bits are read: the next segment may set its own
   }
 }
 
@@ -621,13 +676,13 @@ template <int kMt>
 cudaError_t launch_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
                           int64_t row0, int64_t nrows, float* scores, int64_t ld, const LaunchCtx& ctx) {
   const size_t smem = static_cast<size_t>(b.batch + 1) * sizeof(int);
-  const int grid = ctx.num_sms * (kMt <= 2 ? 2 : 1);
+  const int grid = ctx.num_sms * (kMt <= 2 ? 3 : 2);
   paged_score_kernel<kMt><<<grid, kThreads, smem, ctx.stream>>>(c, b, static_cast<const __nv_bfloat16*>(q_idx), w, Hi,
                                                                 row0, row0 + nrows, scores, ld, ctx.status);
   return cudaGetLastError();
 }
 
-template <int kCap>
+template <int kCap, int kThr>
 cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores, int64_t ld,
                           int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
   const int64_t pools = static_cast<int64_t>(b.max_pages) << (shift - 2);
@@ -636,11 +691,13 @@ cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t n
   constexpr size_t kMost = kFixed + 2 * (kSegment / 32) * 4;
   static_assert(kMost <= 232448 - 1024, "shared memory per CTA");
   static std::atomic<bool> attr_done[kAttrDevices];
-  const cudaError_t e = set_smem_limit_once(paged_select_kernel<kCap>, static_cast<int>(kMost), attr_done);
+  const cudaError_t e = set_smem_limit_once(paged_select_kernel<kCap, kThr>, static_cast<int>(kMost), attr_done);
   if (e != cudaSuccess) return e;
-  paged_select_kernel<kCap><<<static_cast<unsigned>(nrows), kSelThreads, kFixed + static_cast<size_t>(words) * 8,
-                              ctx.stream>>>(b, shift, row0, scores, ld, topk, words, pool_idx, ctx.status);
-  return cudaGetLastError();
+  LaunchCtx early = ctx;
+  early.pdl = 1;
+  return launch_ex(early, paged_select_kernel<kCap, kThr>, dim3(static_cast<unsigned>(nrows)), dim3(kThr),
+                   kFixed + static_cast<size_t>(words) * 8, b, shift, row0, scores, ld, topk, words, pool_idx,
+                   ctx.status);
 }
 
 }  // namespace
@@ -654,9 +711,14 @@ cudaError_t launch_paged_scores(const CacheView& c, const BatchView& b, const vo
 
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,
                                 int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
-  // the list must hold topk and the spread of the sampling
-  if (topk <= 512) return launch_select<4096>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
-  return launch_select<8192>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
+  // the list must hold topk and the spread of the sampling.  A row per SM or
+  // fewer: 1024 threads, for the latency of a row; more: 512, so that rows share an SM
+  const bool few = nrows <= ctx.num_sms;
+  if (topk <= 512)
+    return few ? launch_select<4096, 1024>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx)
+               : launch_select<4096, 512>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
+  return few ? launch_select<8192, 1024>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx)
+             : launch_select<8192, 512>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
 }
 
 }  // namespace dsa

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_score_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                           const TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
+
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // 128-B swizzle atoms need 1024-B alignment
   uint8_t* gbase = smem_raw + (base - raw);
