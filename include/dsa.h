@@ -433,8 +433,9 @@ dsa_status_t dsa_cache_free(const dsa_page_table_t* pages, const int32_t* seqs, 
 dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, int32_t* result,
                                void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace dsa_paged_index_topk is best given: 4 B per row and pool
- * of max_pages pages, in passes of rows that together stay under 1 GiB.  It
+/* Bytes of workspace dsa_paged_index_topk is best given: 4.5 B per row and
+ * pool of max_pages pages (rounded up to 32 pools: the scores, and the largest
+ * of each eight), in passes of rows whose scores stay under 1 GiB.  It
  * accepts less, down to the bytes for min(rows, 8) rows, with the same result.
  * Returns 0 for invalid sizes (and for rows = 0, which needs none). */
 size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size);

@@ -1319,9 +1319,11 @@ dsa_status_t paged_score_maps(const char* fn, const dsa::CacheView& c, const voi
   return DSA_OK;
 }
 
+// A row of the scratch: its scores, rounded up to 32 pools, and the largest of each eight of them.
 int64_t paged_score_ld(int max_pages, int page_size) {
-  return static_cast<int64_t>(max_pages) * (page_size / 4);  // a multiple of 4: page_size >= 16
+  return (static_cast<int64_t>(max_pages) * (page_size / 4) + 31) / 32 * 32;
 }
+size_t paged_scratch_bytes(int64_t rows, int64_t ld) { return static_cast<size_t>(rows) * (ld + ld / 8) * 4; }
 
 }  // namespace
 
@@ -1511,7 +1513,7 @@ size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size
   int64_t r = kPagedScratch / ld;
   r = r < kPagedMinRows ? kPagedMinRows : r;
   r = r < rows ? r : rows;
-  return round_up(static_cast<size_t>(r * ld) * 4, 256);
+  return round_up(paged_scratch_bytes(r, ld), 256);
 }
 
 dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
@@ -1535,9 +1537,9 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
     return fail(DSA_ERR_INVALID_ARG, "%s: q_idx must be 16-byte aligned, w and pool_idx 4-byte aligned", fn);
   const int64_t ld = paged_score_ld(b.max_pages, cache->page_size);
   const int64_t least = b.rows < kPagedMinRows ? b.rows : kPagedMinRows;
-  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(least * ld) * 4);
+  st = check_ws(fn, workspace, ws_bytes, paged_scratch_bytes(least, ld));
   if (st != DSA_OK) return st;
-  int64_t pass = static_cast<int64_t>(ws_bytes / 4) / ld;
+  int64_t pass = static_cast<int64_t>(ws_bytes / paged_scratch_bytes(1, ld));
   if (pass > kPagedPassMax / ld) pass = kPagedPassMax / ld < least ? least : kPagedPassMax / ld;
   if (pass > b.rows) pass = b.rows;
   dsa::LaunchCtx ctx;
@@ -1557,15 +1559,16 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
     if (st != DSA_OK) return st;
   }
   float* scores = static_cast<float*>(workspace);
+  float* tops = scores + pass * ld;
   for (int64_t r = 0; r < b.rows; r += pass) {
     const int64_t n = b.rows - r < pass ? b.rows - r : pass;
     cudaError_t e = timed_launch(tc ? "paged_scores_tc" : "paged_scores", ctx.stream, [&] {
-      return tc ? dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, scores, ld, ctx)
-                : dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, scores, ld, ctx);
+      return tc ? dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, scores, tops, ld, ctx)
+                : dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, scores, tops, ld, ctx);
     });
     if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: scores launch");
     e = timed_launch("paged_select", ctx.stream, [&] {
-      return dsa::launch_paged_select(b, c.shift, r, n, scores, ld, topk, pool_idx, ctx);
+      return dsa::launch_paged_select(b, c.shift, r, n, scores, tops, ld, topk, pool_idx, ctx);
     });
     if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: selection launch");
   }

@@ -132,7 +132,7 @@ template <int kMt>
 __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
     paged_score_kernel(const CacheView c, const BatchView b, const __nv_bfloat16* __restrict__ q,
                        const float* __restrict__ w, int Hi, int64_t row0, int64_t row1, float* __restrict__ scores,
-                       int64_t ld, unsigned* status) {
+                       float* __restrict__ tops, int64_t ld, unsigned* status) {
   extern __shared__ int off[];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -254,7 +254,15 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
       }
       const float sum = (b2 ? x1[1] : x1[0]) + __shfl_xor_sync(0xffffffffu, b2 ? x1[0] : x1[1], 4);
       const int at = p + (b4 ? 16 : 0) + (b3 ? 8 : 0) + 2 * t + (b2 ? 1 : 0);
-      if (at < cur.pools) scores[(row - row0) * ld + at] = sum;
+      float top = -INFINITY;
+      if (at < cur.pools) {
+        scores[(row - row0) * ld + at] = sum;
+        top = sum;
+      }
+      // the largest of each eight pools (an n-tile: lanes alike in bits 3 and 4)
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if ((lane & 7) == 0 && at < cur.pools) tops[((row - row0) * ld + at) >> 3] = top;
     }
     if (nxt.nr == 0) return;
     cur = nxt;
@@ -263,27 +271,29 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
 }
 
 // ================================================================= selection
-// One CTA per row of n > topk scores in global memory (L2 as a rule):
-//   1. n > kCap: a strided sample gives a score t that more than topk scores
-//      reach and far fewer than kCap (five standard deviations of the sampling
-//      to either side), and one pass over the row lists the scores >= t.  The
-//      row is read once.  Shorter rows are listed whole.
-//   2. The topk-th largest score T of the list: a histogram of equal steps
-//      between its extrema (monotone in the score, whatever the rounding) finds
-//      the bin that holds T; while that bin has more than kFew scores, a
-//      histogram of equal steps of their 32-bit keys narrows it; the few left
-//      are ranked against each other.
+// One CTA per row of n > topk scores in global memory, with the largest score
+// of each eight pools beside them (the score kernels write both):
+//   1. n > 8 * topk: the topk-th largest of the groups' maxima is a lower bound
+//      t of the row's topk-th largest score T, for topk groups hold a score
+//      that reaches it.  Only the groups whose maximum reaches t
+//      can hold a score that does; theirs are listed.  (t is taken from a
+//      histogram, one step low at the most.)  For independent scores that is
+//      little more than topk scores from topk groups: of a row of 32768, 16 KB
+//      of maxima and 16 KB of scores are read instead of 128 KB.  Shorter rows
+//      are not listed: steps 2 and 3 read the row itself, from L1.
+//   2. T: a histogram of equal steps between its extrema (monotone
+//      in the score, whatever the rounding) finds the bin that holds T; while
+//      that bin has more than kFew scores, a histogram of equal steps of their
+//      32-bit keys narrows it; the few left are ranked against each other.
 //   3. Scores above T set a bit each, those equal to T one in a second map; the
 //      set bits in order are the row, ascending, the first ties with them.
-// Should the list come out too short or too long (correlated or non-finite
-// scores), step 2 and 3 run over the row itself: the same result, more passes.
-// Lists and not sorted keys: a row of 32768 costs one read of 128 KB and work
-// on about 1200 candidates; several rows share an SM and hide each other's
-// barriers.
+// Should the list run over (hundreds of ties or of neighbours alike), or the
+// maxima have no finite range, a long row goes the short rows' way: the same
+// result, more passes.
 constexpr int kBins = 2048;
 constexpr int kFew = 512;
 constexpr int kSelMaxWarps = 32;
-constexpr int kSegment = 1 << 18;  // pools whose bits are held at once (2 x 32 KB of bits)
+constexpr int kSegment = 1 << 17;  // pools whose bits are held at once (2 x 16 KB of bits)
 
 // The order-preserving 32-bit image of a score (-0 and +0 are one), and the
 // score of a key.
@@ -461,8 +471,8 @@ __device__ __forceinline__ void sel_kth(SelSmem& sm, uint32_t need, int cnt, con
   }
   __syncthreads();
   const uint32_t m = min(sm.nfew, static_cast<uint32_t>(kFew));
-  if (tid < static_cast<int>(m)) {
-    const uint32_t mine = sm.few[tid];
+  for (uint32_t j = tid; j < m; j += kThr) {
+    const uint32_t mine = sm.few[j];
     uint32_t gt = 0u, eq = 0u;
     for (uint32_t e = 0; e < m; ++e) {
       gt += sm.few[e] > mine;
@@ -479,14 +489,16 @@ __device__ __forceinline__ void sel_kth(SelSmem& sm, uint32_t need, int cnt, con
 }
 
 template <int kCap, int kThr>
-__global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kCap <= 4096 ? 3 : 2)
+__global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kThr == 256 ? 5 : 2)
     paged_select_kernel(const BatchView b, int shift, int64_t row0, const float* __restrict__ scores, int64_t ld,
-                        int topk, int words_room, int32_t* __restrict__ pool_idx, unsigned* status) {
+                        const float* __restrict__ tops, int topk, int words_room, int32_t* __restrict__ pool_idx,
+                        unsigned* status) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
   float* cval = reinterpret_cast<float*>(smem_raw + sizeof(SelSmem));    // [kCap] candidates
   int32_t* cidx = reinterpret_cast<int32_t*>(cval + kCap);                // [kCap] their pools
-  uint32_t* above = reinterpret_cast<uint32_t*>(cidx + kCap);             // [words_room] bits: scores above T
+  int32_t* gidx = cidx + kCap;                                            // [kCap / 2] groups to look into
+  uint32_t* above = reinterpret_cast<uint32_t*>(gidx + kCap / 2);         // [words_room] bits: scores above T
   uint32_t* equal = above + words_room;                                   // [words_room] bits: scores equal to T
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t lrow = blockIdx.x, row = row0 + lrow;
@@ -506,116 +518,124 @@ __global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kCap <= 4096 ? 3 : 2)
   for (int k = tid; k < min(kSegment, n + 31) >> 5; k += kThr) above[k] = equal[k] = 0u;
 
   // ---- candidates
-  bool listed = n <= kCap;
+  bool listed = false;
   int m = n;  // scores that T is looked for in: the list's, or the row's
   Steps st{0.f, 0.f};
-  if (listed) {
-    for (int j = tid; j < n; j += kThr) {
-      cval[j] = srow[j];
-      cidx[j] = j;
-    }
-  } else {
-    // quads (4 consecutive scores) of the sample: 1024 in all, 4096 beyond 2^16 pools
-    constexpr int kQuads = 1024 / kThr;
-    const int nq = n >> 2, per = n > 65536 ? 4 * kQuads : kQuads;
-    auto quad = [&](int u) {
-      return *reinterpret_cast<const float4*>(
-          srow + 4 * (static_cast<int64_t>(u * kThr + tid) * nq / (per * kThr)));
-    };
+  if (n > 8 * topk) {
+    const int groups = n >> 3;  // whole groups of eight; what is left of the row is listed in any case
+    const float* trow = tops + ((lrow * ld) >> 3);
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-#pragma unroll 2
-    for (int u = 0; u < per; ++u) {
-      const float4 q = quad(u);
-      const uint32_t k0 = score_key(q.x), k1 = score_key(q.y), k2 = score_key(q.z), k3 = score_key(q.w);
-      lo = min(min(lo, min(k0, k1)), min(k2, k3));
-      hi = max(max(hi, max(k0, k1)), max(k2, k3));
-    }
-    sel_minmax<kThr>(sm, lo, hi, turn);
-    st = Steps::of(lo, hi);
-    if (st.inv > 0.f) {
-#pragma unroll 2
-      for (int u = 0; u < per; ++u) {  // (from L1)
-        const float4 q = quad(u);
-        atomicAdd(&sm.hist[st.bin(q.x)], 1u);
-        atomicAdd(&sm.hist[st.bin(q.y)], 1u);
-        atomicAdd(&sm.hist[st.bin(q.z)], 1u);
-        atomicAdd(&sm.hist[st.bin(q.w)], 1u);
-      }
-      __syncthreads();
-      // c candidates with c - 5 sqrt(c sigma) = topk, sigma scores a sample
-      const float sigma = static_cast<float>(n) / static_cast<float>(4 * per * kThr);
-      const float rc = 0.5f * (5.f * sqrtf(sigma) + sqrtf(25.f * sigma + 4.f * static_cast<float>(topk)));
-      const int want = min(static_cast<int>(rc * rc / sigma) + 1, 4 * per * kThr);
-      sel_find<kThr>(sm, static_cast<uint32_t>(want), turn);
-      // the threshold, near that bin's lower edge; the list's own histogram has its steps between it and the
-      // sample's maximum (the few above fall into the last bin)
-      const float t = st.lo + static_cast<float>(sm.bin) / st.inv;
-      st = Steps::of(score_key(t), hi);
-      for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
-      // one pass over the row: kU 16-byte loads in flight a thread, its hits counted, their places from a scan
-      constexpr int kU = kThr == 1024 ? 8 : 4;
-      uint32_t listed_before = 0u;
-      for (int j0 = 0; j0 < n; j0 += 4 * kU * kThr) {
-        float4 x[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int j = j0 + 4 * (u * kThr + tid);
-          x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j < n) x[u] = *reinterpret_cast<const float4*>(srow + j);  // (rows are whole quads)
-        }
-        uint32_t hit = 0u;  // bit 4 u + e
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-          hit |= (static_cast<uint32_t>(x[u].x >= t) | (static_cast<uint32_t>(x[u].y >= t) << 1) |
-                  (static_cast<uint32_t>(x[u].z >= t) << 2) | (static_cast<uint32_t>(x[u].w >= t) << 3)) << (4 * u);
-        if (j0 + 4 * kU * kThr > n) {  // the row's end: only what lies before it
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            const int left = min(max(n - (j0 + 4 * (u * kThr + tid)), 0), 4);
-            hit &= ~((0xFu & ~((1u << left) - 1u)) << (4 * u));
-          }
-        }
-        uint32_t to = __popc(hit), none = 0u, all, zero;
-        sel_scan2<kThr>(sm, to, none, &all, &zero, turn);  // (its barrier also orders the histogram's zeroes)
-        to += listed_before;
-        listed_before += all;
-        // every lane walks only its own hits (and reads them again, from L1)
-        while (hit) {
-          const int z = __ffs(hit) - 1, j = j0 + 4 * ((z >> 2) * kThr + tid) + (z & 3);
-          hit &= hit - 1u;
-          if (to < static_cast<uint32_t>(kCap)) {
-            const float f = srow[j];
-            cval[to] = f;
-            cidx[to] = j;
-            atomicAdd(&sm.hist[st.bin(f)], 1u);
-          }
-          ++to;
-        }
-      }
-      m = static_cast<int>(min(listed_before, 0x7FFFFFFFu));
-      listed = m >= topk && m <= kCap;
-      if (!listed) m = n;
-    }
-  }
-  if (!listed || n <= kCap) {  // no histogram yet: of the short row's list, or of the row itself
-    __syncthreads();
-    for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
-    const float* v = listed ? cval : srow;
-    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    for (int j = tid; j < m; j += kThr) {
-      const uint32_t k = score_key(v[j]);
+    for (int j = tid; j < groups; j += kThr) {
+      const uint32_t k = score_key(trow[j]);
       lo = min(lo, k);
       hi = max(hi, k);
     }
     sel_minmax<kThr>(sm, lo, hi, turn);
     st = Steps::of(lo, hi);
-    if (st.inv > 0.f)
-      for (int j = tid; j < m; j += kThr) atomicAdd(&sm.hist[st.bin(v[j])], 1u);
+    if (st.inv > 0.f) {
+      for (int j = tid; j < groups; j += kThr) atomicAdd(&sm.hist[st.bin(trow[j])], 1u);  // (from L1)
+      __syncthreads();
+      sel_find<kThr>(sm, static_cast<uint32_t>(topk), turn);
+      const int bin = static_cast<int>(sm.bin);
+      const Steps by = st;  // a score reaches t when it lies in this bin or a higher one
+      st = Steps::of(score_key(st.lo + static_cast<float>(bin) / st.inv), hi);
+      for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
+      // the groups whose maximum does
+      // (4096 at a time: one scan for a row of 32768)
+      constexpr int kGu = 4096 / kThr;
+      uint32_t found = 0u, none = 0u, all, zero;
+      for (int j0 = 0; j0 < groups; j0 += kGu * kThr) {
+        uint32_t hit = 0u;
+#pragma unroll
+        for (int u = 0; u < kGu; ++u) {
+          const int j = j0 + u * kThr + tid;
+          if (j < groups && by.bin(trow[j]) >= bin) hit |= 1u << u;
+        }
+        uint32_t to = __popc(hit);
+        sel_scan2<kThr>(sm, to, none, &all, &zero, turn);
+        to += found;
+        found += all;
+        while (hit) {
+          const int u = __ffs(hit) - 1;
+          hit &= hit - 1u;
+          if (to < static_cast<uint32_t>(kCap / 2)) gidx[to] = j0 + u * kThr + tid;
+          ++to;
+        }
+      }
+      __syncthreads();
+      listed = found <= static_cast<uint32_t>(kCap / 2);
+      if (listed) {
+        // their scores: kHu halves of a group a thread, all asked for before the first is looked at
+        constexpr int kHu = kThr == 1024 ? 2 : 4;
+        uint32_t before = 0u;
+        const int halves = 2 * static_cast<int>(found) + 2;  // and the row's last n % 8
+        for (int e0 = 0; e0 < halves; e0 += kHu * kThr) {
+          float4 x[kHu];
+          int at[kHu];
+#pragma unroll
+          for (int u = 0; u < kHu; ++u) {
+            const int e = e0 + u * kThr + tid;
+            at[u] = n;
+            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e < halves) {
+              at[u] = 8 * (e < halves - 2 ? gidx[e >> 1] : groups) + 4 * (e & 1);
+              if (at[u] < n) x[u] = *reinterpret_cast<const float4*>(srow + at[u]);  // (rows are whole quads)
+            }
+          }
+          uint32_t hit = 0u;
+#pragma unroll
+          for (int u = 0; u < kHu; ++u) {
+            const float f[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (at[u] + v < n && by.bin(f[v]) >= bin) hit |= 1u << (4 * u + v);
+          }
+          uint32_t to = __popc(hit);
+          sel_scan2<kThr>(sm, to, none, &all, &zero, turn);
+          to += before;
+          before += all;
+#pragma unroll
+          for (int u = 0; u < kHu; ++u) {
+            const float f[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if ((hit >> (4 * u + v)) & 1u) {
+                if (to < static_cast<uint32_t>(kCap)) {
+                  cval[to] = f[v];
+                  cidx[to] = at[u] + v;
+                  atomicAdd(&sm.hist[st.bin(f[v])], 1u);
+                }
+                ++to;
+              }
+          }
+        }
+        m = static_cast<int>(before);
+        listed = m >= topk && m <= kCap;
+      }
+      if (!listed) m = n;
+    }
+  }
+  if (!listed) {
+    __syncthreads();
+    for (int j = tid; j < kBins; j += kThr) sm.hist[j] = 0u;
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll 4
+    for (int j = tid; j < n; j += kThr) {
+      const uint32_t k = score_key(srow[j]);
+      lo = min(lo, k);
+      hi = max(hi, k);
+    }
+    sel_minmax<kThr>(sm, lo, hi, turn);
+    st = Steps::of(lo, hi);
+    if (st.inv > 0.f) {
+#pragma unroll 4
+      for (int j = tid; j < n; j += kThr) atomicAdd(&sm.hist[st.bin(srow[j])], 1u);
+    }
   }
   __syncthreads();
 
   // ---- T: of the list, or of the row itself
-  uint32_t T = 0u, take = static_cast<uint32_t>(topk);  // a list of topk scores is kept whole: no key is below 0
+  uint32_t T = 0u, take = static_cast<uint32_t>(topk);  // (a list of topk scores is kept whole: no key is below 0)
   if (m > topk) sel_kth<kThr>(sm, static_cast<uint32_t>(topk), m, listed ? cval : srow, st, &T, &take, turn);
 
   // ---- the row, segment by segment
@@ -674,20 +694,20 @@ __global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kCap <= 4096 ? 3 : 2)
 
 template <int kMt>
 cudaError_t launch_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                          int64_t row0, int64_t nrows, float* scores, int64_t ld, const LaunchCtx& ctx) {
+                          int64_t row0, int64_t nrows, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx) {
   const size_t smem = static_cast<size_t>(b.batch + 1) * sizeof(int);
   const int grid = ctx.num_sms * (kMt <= 2 ? 3 : 2);
   paged_score_kernel<kMt><<<grid, kThreads, smem, ctx.stream>>>(c, b, static_cast<const __nv_bfloat16*>(q_idx), w, Hi,
-                                                                row0, row0 + nrows, scores, ld, ctx.status);
+                                                                row0, row0 + nrows, scores, tops, ld, ctx.status);
   return cudaGetLastError();
 }
 
 template <int kCap, int kThr>
-cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores, int64_t ld,
-                          int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
+cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,
+                          const float* tops, int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
   const int64_t pools = static_cast<int64_t>(b.max_pages) << (shift - 2);
   const int words = static_cast<int>((pools < kSegment ? pools : kSegment) + 31) / 32;
-  constexpr size_t kFixed = sizeof(SelSmem) + static_cast<size_t>(kCap) * 8;
+  constexpr size_t kFixed = sizeof(SelSmem) + static_cast<size_t>(kCap) * 10;
   constexpr size_t kMost = kFixed + 2 * (kSegment / 32) * 4;
   static_assert(kMost <= 232448 - 1024, "shared memory per CTA");
   static std::atomic<bool> attr_done[kAttrDevices];
@@ -696,29 +716,30 @@ cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t n
   LaunchCtx early = ctx;
   early.pdl = 1;
   return launch_ex(early, paged_select_kernel<kCap, kThr>, dim3(static_cast<unsigned>(nrows)), dim3(kThr),
-                   kFixed + static_cast<size_t>(words) * 8, b, shift, row0, scores, ld, topk, words, pool_idx,
-                   ctx.status);
+                   kFixed + static_cast<size_t>(words) * 8, b, shift, row0, scores, ld, tops, topk, words,
+                   pool_idx, ctx.status);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                                int64_t row0, int64_t nrows, float* scores, int64_t ld, const LaunchCtx& ctx) {
-  if (Hi <= 16) return launch_scores<1>(c, b, q_idx, w, Hi, row0, nrows, scores, ld, ctx);
-  if (Hi <= 32) return launch_scores<2>(c, b, q_idx, w, Hi, row0, nrows, scores, ld, ctx);
-  return launch_scores<4>(c, b, q_idx, w, Hi, row0, nrows, scores, ld, ctx);
+                                int64_t row0, int64_t nrows, float* scores, float* tops, int64_t ld,
+                                const LaunchCtx& ctx) {
+  if (Hi <= 16) return launch_scores<1>(c, b, q_idx, w, Hi, row0, nrows, scores, tops, ld, ctx);
+  if (Hi <= 32) return launch_scores<2>(c, b, q_idx, w, Hi, row0, nrows, scores, tops, ld, ctx);
+  return launch_scores<4>(c, b, q_idx, w, Hi, row0, nrows, scores, tops, ld, ctx);
 }
 
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,
-                                int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
-  // the list must hold topk and the spread of the sampling.  A row per SM or
-  // fewer: 1024 threads, for the latency of a row; more: 512, so that rows share an SM
+                                const float* tops, int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx) {
+  // A list of four times the largest topk of its class.  A row per SM or
+  // fewer: 1024 threads, for the latency of a row; more: rows share an SM.
   const bool few = nrows <= ctx.num_sms;
   if (topk <= 512)
-    return few ? launch_select<4096, 1024>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx)
-               : launch_select<4096, 512>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
-  return few ? launch_select<8192, 1024>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx)
-             : launch_select<8192, 512>(b, shift, row0, nrows, scores, ld, topk, pool_idx, ctx);
+    return few ? launch_select<2048, 1024>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx)
+               : launch_select<2048, 256>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx);
+  return few ? launch_select<8192, 1024>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx)
+             : launch_select<8192, 512>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx);
 }
 
 }  // namespace dsa

@@ -54,6 +54,7 @@ struct TcArgs {
   int Hi;
   int64_t row0, row1;
   float* scores;
+  float* tops;
   int64_t ld;
   unsigned* status;
   uint64_t limit_ns;
@@ -346,6 +347,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t room = x.pools - x.p0;  // columns of this tile that exist (stores of four may end past it, inside ld)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        // the largest of each eight pools of this thread's row (a group past
+        // the pools that exist holds anything: nobody reads it)
+        float top[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 u = acc[16 * half + 4 * k], v = acc[16 * half + 4 * k + 1], y = acc[16 * half + 4 * k + 2],
+                       z = acc[16 * half + 4 * k + 3];
+          top[k] = fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(v.x, v.y)), fmaxf(fmaxf(y.x, y.y), fmaxf(z.x, z.y)));
+        }
+        if (valid && cq * kEpiCols + 32 * half < room)
+          *reinterpret_cast<float4*>(a.tops +
+                                     (((x.ra - a.row0 + r) * a.ld + x.p0 + cq * kEpiCols + 32 * half) >> 3)) =
+              make_float4(top[0], top[1], top[2], top[3]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float2 u = acc[16 * half + 2 * j], v = acc[16 * half + 2 * j + 1];
@@ -378,12 +392,12 @@ bool paged_scores_tc_fits(const BatchView& b) { return b.batch <= kMaxBatchTc; }
 
 cudaError_t launch_paged_scores_tc(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                    const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
-                                   float* scores, int64_t ld, const LaunchCtx& ctx) {
+                                   float* scores, float* tops, int64_t ld, const LaunchCtx& ctx) {
   static std::atomic<bool> attr_done[kAttrDevices];
   const cudaError_t e =
       set_smem_limit_once(paged_score_tc_kernel, static_cast<int>(smem_bytes(kMaxBatchTc)), attr_done);
   if (e != cudaSuccess) return e;
-  const TcArgs a{c, b, w, Hi, row0, row0 + nrows, scores, ld, ctx.status, ctx.wait_limit_ns, ctx.inject_timeout};
+  const TcArgs a{c, b, w, Hi, row0, row0 + nrows, scores, tops, ld, ctx.status, ctx.wait_limit_ns, ctx.inject_timeout};
   paged_score_tc_kernel<<<ctx.num_sms, kThreads, smem_bytes(b.batch), ctx.stream>>>(q_map, k_map, a);
   return cudaGetLastError();
 }

@@ -77,8 +77,8 @@ def test_index_arguments_are_checked(lib):
     for kw in (dict(q=None), dict(w=None), dict(out=None), dict(q=FAKE + 8), dict(w=FAKE + 1), dict(topk=0), dict(Hi=0)):
         assert index(lib, **kw) == INVALID, kw
     assert index(lib, Hi=65) == UNSUPPORTED and index(lib, topk=2049) == UNSUPPORTED
-    # 8 pages of 4 pools, 4 bytes, 4 rows
-    assert index(lib, ws=None) == WORKSPACE and index(lib, size=4 * 32 * 4 - 1) == WORKSPACE
+    # 8 pages of 4 pools, 4 bytes and an eighth, 4 rows
+    assert index(lib, ws=None) == WORKSPACE and index(lib, size=4 * 36 * 4 - 1) == WORKSPACE
     assert index(lib, ws=FAKE + 16) == INVALID
     assert index(lib, rows=0, q=None, w=None, out=None, ws=None, size=0) == OK  # nothing to do
 
@@ -128,11 +128,11 @@ def test_workspace_sizes(lib):
     assert lib.dsa_cache_workspace(1000, 8, 0) == r((4 + 3 * 1000) * 4)
     assert lib.dsa_cache_workspace(10, 500, 400) == r((4 + 1200 + 500) * 4)
     assert lib.dsa_cache_workspace(0, 8, 0) == 0 and lib.dsa_cache_workspace(10, 0, 0) == 0
-    assert lib.dsa_paged_index_topk_workspace(64, 2050, 64) == 64 * 2050 * 16 * 4
-    assert lib.dsa_paged_index_topk_workspace(3, 5, 16) == r(3 * 20 * 4)
+    assert lib.dsa_paged_index_topk_workspace(64, 2050, 64) == 64 * 2050 * 18 * 4
+    assert lib.dsa_paged_index_topk_workspace(3, 5, 16) == r(3 * 36 * 4)
     # a pass stays under 1 GiB, and takes at least 8 rows
-    assert lib.dsa_paged_index_topk_workspace(100000, 2050, 64) <= 1 << 30
-    assert lib.dsa_paged_index_topk_workspace(100, 1 << 20, 1024) == 8 * (1 << 28) * 4
+    assert lib.dsa_paged_index_topk_workspace(100000, 2050, 64) <= (1 << 30) * 9 // 8
+    assert lib.dsa_paged_index_topk_workspace(100, 1 << 20, 1024) == 8 * (1 << 28) * 9 // 2
     assert lib.dsa_paged_index_topk_workspace(0, 5, 16) == 0 and lib.dsa_paged_index_topk_workspace(3, 5, 24) == 0
 
 

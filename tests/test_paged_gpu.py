@@ -409,7 +409,8 @@ def test_index_small_bit_exact(layout, page, Hi, topk):
 @pytest.mark.parametrize("new,old,page,Hi,topk", [
     ([1], [40000], 64, 8, 512), ([1, 1], [9001, 30003], 16, 32, 100), ([1] * 90, [2000 + 13 * j for j in range(90)], 64, 4, 64),
     ([3, 9, 1], [20000, 16383, 5000], 256, 16, 2048), ([130], [8191], 64, 8, 512), ([300, 20], [1000, 0], 32, 32, 77),
-    ([1] * 20, [12000 + j for j in range(20)], 1024, 8, 511)])
+    ([1] * 20, [12000 + j for j in range(20)], 1024, 8, 511), ([420, 3], [9000, 30000], 64, 2, 512),
+    ([310], [70000], 256, 1, 40)])
 def test_index_long_bit_exact(new, old, page, Hi, topk):
     m = Model(new, old, page, seed=13, ints=True)
     cache, batch = m.to_gpu(dsa)
@@ -473,8 +474,37 @@ def check_selected(m, q, w, topk, got):
         assert ((s + slack)[kept].min() >= (s - slack)[~kept].max()), (r, b, i)
 
 
+@pytest.mark.parametrize("case", ["zeros", "two_values", "one_high", "negative", "few_values"])
+@pytest.mark.parametrize("topk", [1, 300, 512])
+def test_index_ties_of_many_rows(case, topk):
+    """Rows by the hundred go a warp each; rows whose list of candidates cannot hold the ties, or comes out too short,
+    are left to the other kernel."""
+    m = Model([330], [12001], 64, seed=18, ints=True)
+    q, w = index_inputs(m, 1, seed=19)
+    w = torch.ones_like(w)
+    ki = m.k_idx.view(-1, 4, DI)
+    if case == "zeros":
+        w[::2] = 0  # every other row
+    elif case == "two_values":
+        q.zero_()
+        q[:, 0, 0] = 1
+        m.k_idx.fill_(0)
+        ki[::3, :, 0] = 2
+    elif case == "one_high":
+        ki[m.slot(0, 4000) // 4] *= 2 ** 20
+    elif case == "negative":
+        w *= -1
+    else:
+        q[:, :, 4:] = 0  # scores of few values: the k-th ties with hundreds
+    m.khat = split_hi_lo(pool_mean(ki)).view(m.khat.shape)
+    cache, batch = m.to_gpu(dsa)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+    dsa.dsa_sync_status()
+    check_topk(m, q, w, topk, got)
+
+
 @pytest.mark.parametrize("Hi,topk", [(32, 512), (5, 100)])
-@pytest.mark.parametrize("new,old", [([1, 1, 1], [33000, 4097, 12003]), ([140], [10000])])
+@pytest.mark.parametrize("new,old", [([1, 1, 1], [33000, 4097, 12003]), ([140], [10000]), ([350], [10000])])
 def test_index_real_values(new, old, Hi, topk):
     m = Model(new, old, 64, seed=19)
     cache, batch = m.to_gpu(dsa)
@@ -494,7 +524,7 @@ def test_index_does_not_depend_on_the_workspace_and_leaves_padding():
     q, w = q.to(DEV), w.to(DEV)
     out = torch.full((m.T + 6, 50), 77, dtype=torch.int32, device=DEV)
     full = dsa.dsa_paged_index_topk(cache, batch, q, w, 50, pool_idx=out.clone())
-    least = torch.empty(8 * m.width * 16 * 4, dtype=torch.uint8, device=DEV)
+    least = torch.empty(8 * (m.width * 16 + 31) // 32 * 36 * 4 + 8 * 36 * 4, dtype=torch.uint8, device=DEV)
     small = dsa.dsa_paged_index_topk(cache, batch, q, w, 50, pool_idx=out.clone(), workspace=least)
     dsa.dsa_sync_status()
     assert torch.equal(full, small)
