@@ -1373,7 +1373,7 @@ dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* cache, const int32_t*
   st = make_ctx(stream, &ctx);
   if (st != DSA_OK) return st;
   dsa::call_param("n", n);
-  dsa::call_variant("a block per 32 KB of a page");
+  dsa::call_variant("a block per slice of a page");
   cudaError_t e = timed_launch("copy_pages", ctx.stream, [&] { return dsa::launch_copy_pages(c, src, dst, n, ctx); });
   if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_copy_pages: launch");
   return DSA_OK;
@@ -1409,7 +1409,7 @@ dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add
   if (st != DSA_OK) return st;
   dsa::call_param("max_seqs", t.max_seqs);
   dsa::call_param("num_pages", np);
-  dsa::call_variant("one cluster: plan and take");
+  dsa::call_variant("plan and take in one launch");
   cudaError_t e = timed_launch("cache_reserve", ctx.stream, [&] {
     return dsa::launch_cache_reserve(t, log2_of(pages->page_size), np, add, result, static_cast<int32_t*>(workspace),
                                      ctx);
@@ -1444,7 +1444,7 @@ dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* cache, const dsa_page_table
   if (st != DSA_OK) return st;
   dsa::call_param("n", n);
   dsa::call_param("max_seqs", t.max_seqs);
-  dsa::call_variant("one cluster plans, then a block per 32 KB of a last page");
+  dsa::call_variant("plan, then a block per slice of a last page");
   cudaError_t e = timed_launch("cache_fork", ctx.stream, [&] {
     return dsa::launch_cache_fork(c, t, src, dst, static_cast<int>(n), result, static_cast<int32_t*>(workspace), ctx);
   }, n > 0 ? 2 : 1);
@@ -1497,7 +1497,7 @@ dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* cache, const dsa_page_ta
   if (st != DSA_OK) return st;
   dsa::call_param("num_pages", c.num_pages);
   dsa::call_param("max_seqs", t.max_seqs);
-  dsa::call_variant("one cluster plans, then copies in 32 KB slices");
+  dsa::call_variant("plan, then copies in slices of a page");
   cudaError_t e = timed_launch("cache_compact", ctx.stream, [&] {
     return dsa::launch_cache_compact(c, t, result, static_cast<int32_t*>(workspace), ctx);
   }, 2);

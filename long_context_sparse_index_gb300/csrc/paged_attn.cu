@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
   const int rank = kSplit ? static_cast<int>(cluster_rank()) : 0;
   const int64_t r = kSplit ? blockIdx.x / static_cast<unsigned>(split) : blockIdx.x;
 
+  pdl_wait();  // launched early: what stands before in the stream has ended
   // ---- everything that depends on the row's number alone is asked for at
   // once: Q (swizzled), the selection, the offsets and lengths
   {
@@ -427,13 +428,15 @@ cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kSplit ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = kSplit ? attr : attr + 1;
+  cfg.numAttrs = kSplit ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, paged_attn_kernel<kStages, kSplit, kFlat>, c, b,
                             static_cast<const __nv_bfloat16*>(q), pool_idx, topk, scale * kLog2e,
                             static_cast<__nv_bfloat16*>(o), lse, split, ctx.status);

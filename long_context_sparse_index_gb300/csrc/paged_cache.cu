@@ -125,8 +125,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 
 // ================================================================= page copies
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 8;
-constexpr int kCopyVecs = kCopyThreads * kCopyUnroll;  // 16-byte vectors a block copies at a time (32 KB)
+// 16-byte vectors a block copies at a time: a page of 64 tokens, or half of one
+// of 128, and so on (704 B a token), so that no block has a remainder to copy
+// from pages of 64 tokens on.  Blocks of 32 KB left a third of every second one
+// idle: a compaction of 165 MB took 28 us.
+constexpr int kCopyUnroll = 11;
+constexpr int kCopyVecs = kCopyThreads * kCopyUnroll;
 
 __device__ __forceinline__ int page_vecs(const CacheView& c) { return 44 << c.shift; }  // 704 B a token
 __device__ __forceinline__ int page_slices(const CacheView& c) { return (page_vecs(c) + kCopyVecs - 1) / kCopyVecs; }
@@ -171,8 +175,10 @@ __global__ void __launch_bounds__(kCopyThreads)
 // page is free when its count is 0).  One cluster of 8 CTAs does it in a
 // single launch: each of its 256 warps owns a contiguous stretch of pages,
 // counts it, the counts are scanned in shared memory and across the cluster,
-// and the warps walk their stretches again (from L2) with their offsets.
+// and the warps walk their stretches again (from L2) with their offsets.  A
+// cache of few pages is planned by one CTA, which needs no cluster barriers.
 constexpr int kPlanCtas = 8;
+constexpr int kPlanAlone = 16384;  // pages up to which one CTA plans
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
@@ -184,6 +190,17 @@ struct PlanSmem {
   int bad;
   int carry;
 };
+
+template <int kC>
+__device__ __forceinline__ void plan_sync() {
+  if (kC > 1) cluster_sync();
+  else __syncthreads();
+}
+// a word of CTA u's shared memory
+template <int kC>
+__device__ __forceinline__ uint32_t plan_peer(const int* p, uint32_t u) {
+  return kC > 1 ? cluster_ld_u32(cluster_map(smem_u32(p), u)) : static_cast<uint32_t>(*reinterpret_cast<const volatile int*>(p));
+}
 
 // Exclusive prefix of v over the block's threads; *total: the sum.  sm.scan is free again on return.
 __device__ __forceinline__ int block_excl(PlanSmem& sm, int v, int* total) {
@@ -208,18 +225,20 @@ __device__ __forceinline__ int block_excl(PlanSmem& sm, int v, int* total) {
 }
 
 // The stretch [p0, p1) of warp `gw` of the cluster's 256.
+template <int kC>
 __device__ __forceinline__ void plan_stretch(int num_pages, int gw, int* p0, int* p1) {
-  const int per = ((num_pages + kPlanCtas * kPlanWarps * 32 - 1) / (kPlanCtas * kPlanWarps * 32)) * 32;
+  const int per = ((num_pages + kC * kPlanWarps * 32 - 1) / (kC * kPlanWarps * 32)) * 32;
   *p0 = min(static_cast<int64_t>(gw) * per, static_cast<int64_t>(num_pages));
   *p1 = min(*p0 + per, num_pages);
 }
 
 // Counts the pages of this warp's stretch that are used, scans the counts over the cluster: used pages before the stretch;
 // *all: used pages in the whole cache.
+template <int kC>
 __device__ __forceinline__ int plan_scan(PlanSmem& sm, const int32_t* count, int num_pages, uint32_t rank, int* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int p0, p1;
-  plan_stretch(num_pages, static_cast<int>(rank) * kPlanWarps + warp, &p0, &p1);
+  plan_stretch<kC>(num_pages, static_cast<int>(rank) * kPlanWarps + warp, &p0, &p1);
   int n = 0;
 #pragma unroll 8
   for (int p = p0; p < p1; p += 32) n += p + lane < p1 && count[p + lane] != 0;
@@ -238,10 +257,10 @@ __device__ __forceinline__ int plan_scan(PlanSmem& sm, const int32_t* count, int
     sm.warp[lane] = x - v;
     if (lane == 31) sm.total = x;
   }
-  cluster_sync();
+  plan_sync<kC>();
   int before = 0, sum = 0;
-  for (uint32_t r = 0; r < kPlanCtas; ++r) {
-    const int t = static_cast<int>(cluster_ld_u32(cluster_map(smem_u32(&sm.total), r)));
+  for (uint32_t r = 0; r < kC; ++r) {
+    const int t = static_cast<int>(plan_peer<kC>(&sm.total, r));
     before += r < rank ? t : 0;
     sum += t;
   }
@@ -250,11 +269,12 @@ __device__ __forceinline__ int plan_scan(PlanSmem& sm, const int32_t* count, int
 }
 
 // Writes the k-th lowest free page to list[k] for k < need.
+template <int kC>
 __device__ __forceinline__ void plan_free_list(const int32_t* count, int num_pages, uint32_t rank, int used_before,
                                                int need, int32_t* list) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int p0, p1;
-  plan_stretch(num_pages, static_cast<int>(rank) * kPlanWarps + warp, &p0, &p1);
+  plan_stretch<kC>(num_pages, static_cast<int>(rank) * kPlanWarps + warp, &p0, &p1);
   int at = p0 - used_before;  // free pages before the stretch
   for (int p = p0; p < p1 && at < need; p += 32) {
     const bool free = p + lane < p1 && count[p + lane] == 0;
@@ -268,11 +288,12 @@ __device__ __forceinline__ void plan_free_list(const int32_t* count, int num_pag
 // ----------------------------------------------------------------- reserve
 // ws: off [max_seqs], list [num_pages].  One launch: the plan, then a warp per
 // sequence takes its pages.
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kC>
+__global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
     cache_reserve_kernel(const PageTableView t, int shift, int num_pages, const int32_t* __restrict__ add,
                          int32_t* result, int32_t* ws, unsigned* status) {
   __shared__ PlanSmem sm;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = kC > 1 ? cluster_rank() : 0u;
   int32_t* off = ws;
   int32_t* list = ws + t.max_seqs;
   const int64_t cap = static_cast<int64_t>(t.max_pages) << shift;
@@ -297,7 +318,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   __syncthreads();
   const bool bad = sm.bad != 0;
   int used;
-  const int before = plan_scan(sm, t.count, num_pages, rank, &used);
+  const int before = plan_scan<kC>(sm, t.count, num_pages, rank, &used);
   const int64_t room = num_pages - used;
   const bool go = !bad && need <= room;
   if (rank == 0 && threadIdx.x == 0) {
@@ -305,12 +326,12 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                                    : static_cast<int32_t>(-min(need - room, static_cast<int64_t>(INT32_MAX)));
     if (bad) record_status(status, kStatusInternal);
   }
-  if (go) plan_free_list(t.count, num_pages, rank, before, static_cast<int>(need), list);
-  cluster_sync();  // the list and the prefix are written; every count has been read
+  if (go) plan_free_list<kC>(t.count, num_pages, rank, before, static_cast<int>(need), list);
+  plan_sync<kC>();  // the list and the prefix are written; every count has been read
   if (!go) return;
   const int lane = threadIdx.x & 31;
   const int gw = static_cast<int>(rank) * kPlanWarps + (threadIdx.x >> 5);
-  for (int s = gw; s < t.max_seqs; s += kPlanCtas * kPlanWarps) {
+  for (int s = gw; s < t.max_seqs; s += kC * kPlanWarps) {
     const int64_t len = t.lens[s], more = add[s];
     const int have = static_cast<int>((len + (1 << shift) - 1) >> shift);
     const int want = static_cast<int>((len + more + (1 << shift) - 1) >> shift);
@@ -335,20 +356,21 @@ __host__ __device__ inline ForkWs fork_ws(int32_t* ws, int64_t n) {
   return ForkWs{ws, ws + 4, ws + 4 + n, ws + 4 + 2 * n, ws + 4 + 3 * n};
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kC>
+__global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
     fork_plan_kernel(const PageTableView t, int shift, int num_pages, const int32_t* __restrict__ src,
                      const int32_t* __restrict__ dst, int n, int32_t* result, int32_t* ws_, unsigned* status) {
   __shared__ PlanSmem sm;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = kC > 1 ? cluster_rank() : 0u;
   const ForkWs ws = fork_ws(ws_, n);
   const int64_t cap = static_cast<int64_t>(t.max_pages) << shift;
   const unsigned seqs = static_cast<unsigned>(t.max_seqs);
   if (threadIdx.x == 0) sm.bad = 0;
-  for (int j = rank * kPlanThreads + threadIdx.x; j < n; j += kPlanCtas * kPlanThreads)
+  for (int j = rank * kPlanThreads + threadIdx.x; j < n; j += kC * kPlanThreads)
     if (static_cast<unsigned>(dst[j]) < seqs) ws.claim[dst[j]] = 0;
-  cluster_sync();
+  plan_sync<kC>();
   // every CTA checks its part of the request; the same child twice shows in its claim
-  for (int j = rank * kPlanThreads + threadIdx.x; j < n; j += kPlanCtas * kPlanThreads) {
+  for (int j = rank * kPlanThreads + threadIdx.x; j < n; j += kC * kPlanThreads) {
     const int s = src[j], d = dst[j];
     bool ok = static_cast<unsigned>(s) < seqs && static_cast<unsigned>(d) < seqs;
     if (ok) {
@@ -372,9 +394,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     need += tile;
   }
   int used;
-  const int before = plan_scan(sm, t.count, num_pages, rank, &used);
+  const int before = plan_scan<kC>(sm, t.count, num_pages, rank, &used);
   bool bad = false;
-  for (uint32_t r = 0; r < kPlanCtas; ++r) bad |= cluster_ld_u32(cluster_map(smem_u32(&sm.bad), r)) != 0;
+  for (uint32_t r = 0; r < kC; ++r) bad |= plan_peer<kC>(&sm.bad, r) != 0;
   const int room = num_pages - used;
   const bool go = !bad && need <= room;
   if (rank == 0 && threadIdx.x == 0) {
@@ -382,8 +404,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     *ws.go = go;
     if (bad) record_status(status, kStatusInternal);
   }
-  if (go) plan_free_list(t.count, num_pages, rank, before, need, ws.list);
-  cluster_sync();  // no CTA leaves while another reads its shared memory
+  if (go) plan_free_list<kC>(t.count, num_pages, rank, before, need, ws.list);
+  plan_sync<kC>();  // no CTA leaves while another reads its shared memory
 }
 
 // Block (j, y): child j's part y.  Parts 0 .. slices-1 also copy a slice of
@@ -392,6 +414,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(const CacheView c, const PageTableView t, const int32_t* __restrict__ src,
                       const int32_t* __restrict__ dst, int n, int32_t* ws_, unsigned* status) {
   const ForkWs ws = fork_ws(ws_, n);
+  pdl_wait();  // the plan is written
   if (*ws.go == 0) return;
   const int j = blockIdx.x;
   const int s = src[j], d = dst[j], len = ws.len[j];
@@ -465,27 +488,28 @@ __host__ __device__ inline CompactWs compact_ws(int32_t* ws, int64_t num_pages) 
   return CompactWs{ws, ws + 4, ws + 4 + num_pages, ws + 4 + 2 * num_pages};
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+template <int kC>
+__global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
     compact_plan_kernel(const PageTableView t, int num_pages, int32_t* result, int32_t* ws_) {
   __shared__ PlanSmem sm;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = kC > 1 ? cluster_rank() : 0u;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const CompactWs ws = compact_ws(ws_, num_pages);
   if (threadIdx.x == 0) sm.below = -1;
   int used;
-  const int before = plan_scan(sm, t.count, num_pages, rank, &used);  // (its barriers order sm.below)
+  const int before = plan_scan<kC>(sm, t.count, num_pages, rank, &used);  // (its barriers order sm.below)
   int p0, p1;
-  plan_stretch(num_pages, static_cast<int>(rank) * kPlanWarps + warp, &p0, &p1);
+  plan_stretch<kC>(num_pages, static_cast<int>(rank) * kPlanWarps + warp, &p0, &p1);
   // used pages below page number `used`, found by the warp whose stretch holds that page
   if (used >= p0 && used < p1) {
     int n = 0;
     for (int p = p0; p < used; p += 32) n += __popc(__ballot_sync(0xffffffffu, p + lane < used && t.count[p + lane] != 0));
     if (lane == 0) sm.below = before + n;
   }
-  cluster_sync();
+  plan_sync<kC>();
   int below = used;  // a full cache: no page is at or above `used`
-  for (uint32_t r = 0; r < kPlanCtas; ++r) {
-    const int x = static_cast<int>(cluster_ld_u32(cluster_map(smem_u32(&sm.below), r)));
+  for (uint32_t r = 0; r < kC; ++r) {
+    const int x = static_cast<int>(plan_peer<kC>(&sm.below, r));
     if (x >= 0) below = x;
   }
   if (rank == 0 && threadIdx.x == 0) {
@@ -506,12 +530,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
     at += __popc(m);
   }
-  cluster_sync();  // no CTA leaves while another reads its shared memory
+  plan_sync<kC>();  // no CTA leaves while another reads its shared memory
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
     compact_apply_kernel(const CacheView c, const PageTableView t, int32_t* ws_) {
   const CompactWs ws = compact_ws(ws_, c.num_pages);
+  pdl_wait();  // the plan is written
   const int used = ws.head[0], moved = ws.head[1];
   if (moved == 0) return;
   const int slices = page_slices(c);
@@ -561,22 +586,31 @@ int64_t compact_ws_words(int num_pages) { return 4 + 3 * static_cast<int64_t>(nu
 
 cudaError_t launch_cache_reserve(const PageTableView& t, int shift, int num_pages, const int32_t* add, int32_t* result,
                                  int32_t* ws, const LaunchCtx& ctx) {
-  cache_reserve_kernel<<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, shift, num_pages, add, result, ws, ctx.status);
+  if (num_pages <= kPlanAlone)
+    cache_reserve_kernel<1><<<1, kPlanThreads, 0, ctx.stream>>>(t, shift, num_pages, add, result, ws, ctx.status);
+  else
+    cache_reserve_kernel<kPlanCtas>
+        <<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, shift, num_pages, add, result, ws, ctx.status);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_fork(const CacheView& c, const PageTableView& t, const int32_t* src, const int32_t* dst,
                               int n, int32_t* result, int32_t* ws, const LaunchCtx& ctx) {
-  fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, c.shift, c.num_pages, src, dst, n, result, ws,
-                                                               ctx.status);
+  if (c.num_pages <= kPlanAlone)
+    fork_plan_kernel<1>
+        <<<1, kPlanThreads, 0, ctx.stream>>>(t, c.shift, c.num_pages, src, dst, n, result, ws, ctx.status);
+  else
+    fork_plan_kernel<kPlanCtas>
+        <<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, c.shift, c.num_pages, src, dst, n, result, ws, ctx.status);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || n == 0) return e;
   // parts of a child: one per slice of its last page, and enough that a thread
   // copies at most 4 entries of the row (8 parts at the most for long rows)
   const int by_row = (t.max_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
   const int parts = host_slices(c.shift) > by_row ? host_slices(c.shift) : by_row < 8 ? by_row : 8;
-  fork_apply_kernel<<<dim3(n, parts), kCopyThreads, 0, ctx.stream>>>(c, t, src, dst, n, ws, ctx.status);
-  return cudaGetLastError();
+  LaunchCtx early = ctx;
+  early.pdl = 1;
+  return launch_ex(early, fork_apply_kernel, dim3(n, parts), dim3(kCopyThreads), 0, c, t, src, dst, n, ws, ctx.status);
 }
 
 cudaError_t launch_cache_free(const PageTableView& t, int shift, int num_pages, const int32_t* seqs, int n,
@@ -587,11 +621,15 @@ cudaError_t launch_cache_free(const PageTableView& t, int shift, int num_pages, 
 
 cudaError_t launch_cache_compact(const CacheView& c, const PageTableView& t, int32_t* result, int32_t* ws,
                                  const LaunchCtx& ctx) {
-  compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, c.num_pages, result, ws);
+  if (c.num_pages <= kPlanAlone)
+    compact_plan_kernel<1><<<1, kPlanThreads, 0, ctx.stream>>>(t, c.num_pages, result, ws);
+  else
+    compact_plan_kernel<kPlanCtas><<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, c.num_pages, result, ws);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  compact_apply_kernel<<<ctx.num_sms * 8, kCopyThreads, 0, ctx.stream>>>(c, t, ws);
-  return cudaGetLastError();
+  LaunchCtx early = ctx;
+  early.pdl = 1;
+  return launch_ex(early, compact_apply_kernel, dim3(ctx.num_sms * 16), dim3(kCopyThreads), 0, c, t, ws);
 }
 
 }  // namespace dsa
