@@ -395,12 +395,14 @@ dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* cache, const int32_t*
 size_t dsa_cache_workspace(int64_t num_pages, int max_seqs, int64_t n);
 
 /*
- * Grows every sequence s by add[s] >= 0 tokens (device int32 [max_seqs]):
- * seq_lens[s] += add[s], and the pages it then needs are taken, the lowest
- * free ones in the order of sequences and of positions.  *result (device
- * int32) is the number of pages taken.  When too few are free, nothing
- * changes and *result is minus the number lacking; for a length that max_pages
- * cannot hold, or a negative one, nothing changes, *result is INT32_MIN and
+ * Changes the length of every sequence s by add[s] (device int32 [max_seqs]):
+ * seq_lens[s] += add[s].  The pages that longer sequences then need are taken,
+ * the lowest free ones in the order of sequences and of positions; shorter
+ * sequences (a rejected draft) give theirs back, for later calls.  *result
+ * (device int32) is the number of pages taken.  When too few are free, nothing
+ * changes and *result is minus the number lacking.  For a length below 0 or
+ * above what max_pages holds, or a shorter one that would end inside a page
+ * that another sequence holds too, nothing changes, *result is INT32_MIN and
  * the status reports DSA_ERR_INTERNAL.
  */
 dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add, int32_t* result, void* workspace,

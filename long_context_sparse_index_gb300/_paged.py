@@ -286,8 +286,9 @@ def _of_cache(cache: PagedCache, pages: PageTable) -> int:
 
 
 def dsa_cache_reserve(cache: PagedCache, pages: PageTable, add, result=None, workspace=None, stream=None):
-    """Grows every sequence s by add[s] tokens (int32 [max_seqs]), taking the
-    lowest free pages; returns a device word: pages taken, or minus the number
+    """Changes the length of every sequence s by add[s] tokens (int32
+    [max_seqs]): longer ones take the lowest free pages, shorter ones give
+    theirs back; returns a device word: pages taken, or minus the number
     lacking (then nothing changed)."""
     dev, lib = _of_cache(cache, pages), load()
     _ids(add, "add", dev)

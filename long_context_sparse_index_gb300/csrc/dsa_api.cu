@@ -1204,7 +1204,12 @@ constexpr int64_t kIntMax = 0x7FFFFFFFLL;
 constexpr int64_t kPagedScratch = int64_t{1} << 28;  // scores of a pass in the recommended workspace (1 GiB)
 constexpr int64_t kPagedPassMax = int64_t{1} << 31;  // scores of a pass however large the workspace
 constexpr int kPagedMinRows = 8;
-constexpr int kPagedTcRows = 32;  // rows per sequence from which the tcgen05 scores are taken
+// Rows per sequence (on average) from which the tcgen05 scores are taken: their
+// 128-row tiles cost the same however few rows they hold, the mma.sync kernel
+// grows with every 8.  Measured at 32 heads, mma.sync / tcgen05: one sequence of
+// 131072 tokens 31 / 33 us at 16 rows and 36 / 33 at 24; 16 sequences of 32768
+// tokens 76 / 102 and 105 / 102; 64 of 8192 76 / 104 and 107 / 105.
+constexpr int kPagedTcRows = 24;
 
 bool page_size_ok(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 int log2_of(int x) {

@@ -305,9 +305,16 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
     const int s = s0 + static_cast<int>(threadIdx.x);
     int v = 0;
     if (s < t.max_seqs) {
-      const int64_t len = t.lens[s], more = add[s];
-      if (len < 0 || more < 0 || len + more > cap) sm.bad = 1;
-      else v = static_cast<int>(((len + more + (1 << shift) - 1) >> shift) - ((len + (1 << shift) - 1) >> shift));
+      const int64_t len = t.lens[s], more = add[s], to = len + more;
+      if (len < 0 || to < 0 || len > cap || to > cap) {
+        sm.bad = 1;
+      } else {
+        v = static_cast<int>(max(((to + (1 << shift) - 1) >> shift) - ((len + (1 << shift) - 1) >> shift), int64_t{0}));
+        if (more < 0 && (to & ((1 << shift) - 1)) != 0) {  // the page that becomes the last is written next: it must be its own
+          const int p = t.table[s * t.table_stride + (to >> shift)];
+          if (static_cast<unsigned>(p) >= static_cast<unsigned>(num_pages) || t.count[p] > 1) sm.bad = 1;
+        }
+      }
     }
     int tile;
     const int before = block_excl(sm, v, &tile);
@@ -339,6 +346,15 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
       const int p = list[off[s] + x - have];
       t.table[s * t.table_stride + x] = p;
       t.count[p] = 1;
+    }
+    for (int x = want + lane; x < have; x += 32) {  // a shorter sequence gives pages back
+      const int p = t.table[s * t.table_stride + x];
+      t.table[s * t.table_stride + x] = -1;
+      if (static_cast<unsigned>(p) >= static_cast<unsigned>(num_pages)) record_status(status, kStatusInternal);
+      else if (atomicSub(t.count + p, 1) <= 0) {
+        atomicAdd(t.count + p, 1);  // the page was free already
+        record_status(status, kStatusInternal);
+      }
     }
     __syncwarp();
     if (lane == 0) t.lens[s] = static_cast<int32_t>(len + more);

@@ -118,16 +118,20 @@ class Pages:
         free, need = self.free_pages(), []
         for s, a in enumerate(add):
             need.append(-(-(self.lens[s] + a) // self.page) - -(-self.lens[s] // self.page))
-        if sum(need) > len(free):
-            return len(free) - sum(need)
+        taken = sum(max(n, 0) for n in need)
+        if taken > len(free):
+            return len(free) - taken
         for s, a in enumerate(add):
             have = -(-self.lens[s] // self.page)
             for x in range(need[s]):
                 p = free.pop(0)
                 self.table[s, have + x] = p
                 self.count[p] = 1
+            for x in range(have + min(need[s], 0), have):
+                self.count[self.table[s, x]] -= 1
+                self.table[s, x] = -1
             self.lens[s] += a
-        return sum(need)
+        return taken
 
     def fork(self, src, dst):
         """(pages taken, [(from, to)])"""
@@ -246,13 +250,41 @@ def test_reserve_without_room_changes_nothing():
     t, cache = p.to_gpu(), random_cache(8, 16)
     assert dsa.dsa_cache_reserve(cache, t, i32([3, 33])).item() == p.reserve([3, 33]) == -2
     p.check(t)
-    # a length the table cannot hold, and a negative one
-    for add in ([320, 0], [0, -1]):
+    # a length the table cannot hold, and one below zero
+    for add in ([320, 0], [0, -65]):
         assert dsa.dsa_cache_reserve(cache, t, i32(add)).item() == -2 ** 31
         with pytest.raises(dsa.DsaError):
             dsa.dsa_sync_status()
         dsa.dsa_clear_status()
         p.check(t)
+
+
+def test_reserve_gives_pages_back():
+    """Rejected drafts: sequences shrink, some to a page's end, some to nothing, while others grow in the same call."""
+    p = Pages([50, 33, 16, 7, 0, 80], 16, 60, 8, seed=2)
+    t, cache = p.to_gpu(), random_cache(60, 16)
+    for add in ([-3, -1, 20, -7, 5, -33], [-15, 0, -20, 3, -5, -47], [40, -32, 1, -3, 0, 100]):
+        assert dsa.dsa_cache_reserve(cache, t, i32(add)).item() == p.reserve(add)
+        dsa.dsa_sync_status()
+        p.check(t)
+
+
+def test_reserve_does_not_shrink_into_a_shared_page():
+    p = Pages([40, 0, 0], 16, 20, 6, seed=6)
+    t, cache = p.to_gpu(), random_cache(20, 16)
+    dsa.dsa_cache_fork(cache, t, i32([0]), i32([1]))
+    p.fork([0], [1])
+    assert dsa.dsa_cache_reserve(cache, t, i32([-1, -5, 0])).item() == p.reserve([-1, -5, 0])  # inside its own pages
+    dsa.dsa_sync_status()
+    p.check(t)
+    assert dsa.dsa_cache_reserve(cache, t, i32([0, -10, 0])).item() == -2 ** 31  # 25 tokens: inside the second, shared page
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_sync_status()
+    dsa.dsa_clear_status()
+    p.check(t)
+    assert dsa.dsa_cache_reserve(cache, t, i32([-39 + 16, -35 + 32, 0])).item() == p.reserve([-39 + 16, -35 + 32, 0])
+    dsa.dsa_sync_status()
+    p.check(t)
 
 
 def test_reserve_of_many_sequences():
