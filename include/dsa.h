@@ -383,13 +383,19 @@ dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_ba
                               int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
                               int64_t k_idx_stride, void* stream);
 
-/* Copies page src[j] onto page dst[j], all four buffers, for j < n (device
- * int32 arrays).  The copies run in any order: no page may be named in dst
- * twice, or in dst and (for another pair) in src. */
-dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
-                                  void* stream);
+/*
+ * The operators on pages.  Where they move data they take the caches of all
+ * layers whose pages the table numbers (an array of `layers` of them, with the
+ * same num_pages and page_size): one plan, and every layer's pages move alike.
+ */
 
-/* Bytes of workspace the calls below need for a cache of num_pages pages, a
+/* Copies page src[j] onto page dst[j], all four buffers of every layer, for j
+ * < n (device int32 arrays).  The copies run in any order: no page may be named in dst
+ * twice, or in dst and (for another pair) in src. */
+dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* caches, int layers, const int32_t* src, const int32_t* dst,
+                                  int64_t n, void* stream);
+
+/* Bytes of workspace the calls below need for caches of num_pages pages, a
  * table of max_seqs rows and, for the fork, n children (0 for bad sizes).
  * Calls that share a workspace must be ordered on the device. */
 size_t dsa_cache_workspace(int64_t num_pages, int max_seqs, int64_t n);
@@ -415,9 +421,9 @@ dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add
  * ones in the order of j.  A parent may have several children.  Every row
  * dst[j] must be free (length 0) and named once.  *result as above.
  */
-dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, const int32_t* src,
-                            const int32_t* dst, int64_t n, int32_t* result, void* workspace, size_t ws_bytes,
-                            void* stream);
+dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
+                            const int32_t* src, const int32_t* dst, int64_t n, int32_t* result, void* workspace,
+                            size_t ws_bytes, void* stream);
 
 /* Frees sequences seqs[0 .. n-1] (device int32): their pages' counts go down
  * by one, their table entries become -1, their lengths 0.  Freeing a free row,
@@ -429,11 +435,10 @@ dsa_status_t dsa_cache_free(const dsa_page_table_t* pages, const int32_t* seqs, 
  * the free ones below U (the k-th of them to the k-th free one, both
  * ascending); page_count and every entry of block_table that names a moved
  * page follow.  Afterwards pages 0 .. U-1 are in use.  result (device int32
- * [2]): U, and the number of pages moved.  The cache must be the one whose
- * pages the table counts.
+ * [2]): U, and the number of pages moved.
  */
-dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, int32_t* result,
-                               void* workspace, size_t ws_bytes, void* stream);
+dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
+                               int32_t* result, void* workspace, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace dsa_paged_index_topk is best given: 4.5 B per row and
  * pool of max_pages pages (rounded up to 32 pools: the scores, and the largest

@@ -204,13 +204,13 @@ class PageTable:
 def _configure_paged(lib):
     f32, sz, i64, i32, vp = ctypes.c_float, ctypes.c_size_t, _i64, _i32, _vp
     lib.dsa_cache_append.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp]
-    lib.dsa_cache_copy_pages.argtypes = [vp, vp, vp, i64, vp]
+    lib.dsa_cache_copy_pages.argtypes = [vp, i32, vp, vp, i64, vp]
     lib.dsa_cache_workspace.argtypes = [i64, i32, i64]
     lib.dsa_cache_workspace.restype = sz
     lib.dsa_cache_reserve.argtypes = [vp, vp, vp, vp, sz, vp]
-    lib.dsa_cache_fork.argtypes = [vp, vp, vp, vp, i64, vp, vp, sz, vp]
+    lib.dsa_cache_fork.argtypes = [vp, i32, vp, vp, vp, i64, vp, vp, sz, vp]
     lib.dsa_cache_free.argtypes = [vp, vp, i64, vp]
-    lib.dsa_cache_compact.argtypes = [vp, vp, vp, vp, sz, vp]
+    lib.dsa_cache_compact.argtypes = [vp, i32, vp, vp, vp, sz, vp]
     lib.dsa_paged_index_topk_workspace.argtypes = [i64, i32, i32]
     lib.dsa_paged_index_topk_workspace.restype = sz
     lib.dsa_paged_index_topk.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, sz, vp]
@@ -264,13 +264,29 @@ def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=N
                                    k_idx.data_ptr(), kis, _handle(stream, dev)))
 
 
-def dsa_cache_copy_pages(cache: PagedCache, src, dst, stream=None):
-    """Copies page src[j] onto page dst[j] (int32 tensors), all four buffers."""
-    dev = _device_of(cache)
+def _layers(cache):
+    """(first cache, struct array, count) of one cache or of a sequence of the layers' caches."""
+    if isinstance(cache, PagedCache):
+        return cache, cache._ref, 1
+    caches = list(cache)
+    if not caches or not all(isinstance(c, PagedCache) for c in caches):
+        raise TypeError("cache must be a PagedCache or a sequence of the layers' PagedCaches")
+    first = caches[0]
+    for c in caches:
+        if c.device_index != first.device_index:
+            raise ValueError("the layers' caches must be on one device")
+    return first, (_CacheStruct * len(caches))(*[c._struct for c in caches]), len(caches)
+
+
+def dsa_cache_copy_pages(cache, src, dst, stream=None):
+    """Copies page src[j] onto page dst[j] (int32 tensors), all four buffers,
+    of a cache or of every layer's (a sequence of caches)."""
+    first, ref, layers = _layers(cache)
+    dev = _device_of(first)
     n = _ids(src, "src", dev)
     _ids(dst, "dst", dev)
     _shape(dst, "dst", (n,))
-    _check(load().dsa_cache_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(), n, _handle(stream, dev)))
+    _check(load().dsa_cache_copy_pages(ref, layers, src.data_ptr(), dst.data_ptr(), n, _handle(stream, dev)))
 
 
 def cache_workspace_size(num_pages: int, max_seqs: int, n: int = 0) -> int:
@@ -300,17 +316,19 @@ def dsa_cache_reserve(cache: PagedCache, pages: PageTable, add, result=None, wor
     return result
 
 
-def dsa_cache_fork(cache: PagedCache, pages: PageTable, src, dst, result=None, workspace=None, stream=None):
+def dsa_cache_fork(cache, pages: PageTable, src, dst, result=None, workspace=None, stream=None):
     """Row dst[j] becomes a copy of sequence src[j] (int32 tensors): full pages
-    shared, a partly filled last page copied; returns a device word: pages
+    shared, a partly filled last page copied, in a cache or in every layer's (a
+    sequence of caches); returns a device word: pages
     taken, or minus the number lacking (then nothing changed)."""
+    cache, ref, layers = _layers(cache)
     dev, lib = _of_cache(cache, pages), load()
     n = _ids(src, "src", dev)
     _ids(dst, "dst", dev)
     _shape(dst, "dst", (n,))
     result = _result(result, "result", (1,), torch.int32, cache.device, stream)
     ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, n), workspace, cache.device, stream)
-    _check(lib.dsa_cache_fork(cache._ref, pages._with_page(cache.page_size), src.data_ptr(), dst.data_ptr(), n,
+    _check(lib.dsa_cache_fork(ref, layers, pages._with_page(cache.page_size), src.data_ptr(), dst.data_ptr(), n,
                               result.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
 
@@ -322,13 +340,15 @@ def dsa_cache_free(cache: PagedCache, pages: PageTable, seqs, stream=None):
     _check(load().dsa_cache_free(pages._with_page(cache.page_size), seqs.data_ptr(), n, _handle(stream, dev)))
 
 
-def dsa_cache_compact(cache: PagedCache, pages: PageTable, result=None, workspace=None, stream=None):
-    """Moves the used pages down over the free ones; returns device words
-    [pages in use, pages moved]."""
+def dsa_cache_compact(cache, pages: PageTable, result=None, workspace=None, stream=None):
+    """Moves the used pages down over the free ones, in a cache or in every
+    layer's (a sequence of caches); returns device words [pages in use, pages
+    moved]."""
+    cache, ref, layers = _layers(cache)
     dev, lib = _of_cache(cache, pages), load()
     result = _result(result, "result", (2,), torch.int32, cache.device, stream)
     ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, cache.device, stream)
-    _check(lib.dsa_cache_compact(cache._ref, pages._with_page(cache.page_size), result.data_ptr(), ws.data_ptr(),
+    _check(lib.dsa_cache_compact(ref, layers, pages._with_page(cache.page_size), result.data_ptr(), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
 

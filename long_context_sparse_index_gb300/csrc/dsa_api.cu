@@ -319,6 +319,22 @@ size_t index_ws_bytes(int64_t S, int chunk, int topk, int nbuf) {
   return index_layout(S, index_plan(S, chunk, topk), nbuf).total;
 }
 
+// Calls launch(set, first) for the layers, kLayerBatch at a time.
+template <typename F>
+cudaError_t by_layers(const std::vector<dsa::CacheView>& views, F&& launch) {
+  for (size_t l = 0; l < views.size(); l += dsa::kLayerBatch) {
+    dsa::CacheSet set;
+    set.n = static_cast<int>(views.size() - l < dsa::kLayerBatch ? views.size() - l : dsa::kLayerBatch);
+    for (int i = 0; i < dsa::kLayerBatch; ++i) set.v[i] = views[l + (i < set.n ? i : 0)];
+    const cudaError_t e = launch(set, l == 0);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+int layer_launches(const std::vector<dsa::CacheView>& views) {
+  return static_cast<int>((views.size() + dsa::kLayerBatch - 1) / dsa::kLayerBatch);
+}
+
 }  // namespace
 
 namespace dsa {
@@ -1287,6 +1303,20 @@ dsa_status_t table_view(const char* fn, const dsa_page_table_t* t, dsa::PageTabl
   return DSA_OK;
 }
 
+// The caches of the layers that move pages together: the same pages of the same size.
+dsa_status_t cache_views(const char* fn, const dsa_paged_cache_t* caches, int layers, std::vector<dsa::CacheView>* out) {
+  if (!caches) return fail(DSA_ERR_INVALID_ARG, "%s: null cache", fn);
+  if (layers < 1) return fail(DSA_ERR_INVALID_ARG, "%s: layers=%d must be >= 1", fn, layers);
+  out->resize(layers);
+  for (int l = 0; l < layers; ++l) {
+    dsa_status_t st = cache_view(fn, caches + l, &(*out)[l]);
+    if (st != DSA_OK) return st;
+    if (caches[l].num_pages != caches[0].num_pages || caches[l].page_size != caches[0].page_size)
+      return fail(DSA_ERR_INVALID_ARG, "%s: the layers' caches differ in their pages", fn);
+  }
+  return DSA_OK;
+}
+
 dsa_status_t check_ws(const char* fn, const void* workspace, size_t ws_bytes, size_t need) {
   if (!workspace || ws_bytes < need)
     return fail(DSA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
@@ -1363,12 +1393,12 @@ dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_ba
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t n,
-                                  void* stream) try {
+dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* caches, int layers, const int32_t* src, const int32_t* dst,
+                                  int64_t n, void* stream) try {
   const char* fn = "dsa_cache_copy_pages";
   const dsa::CallScope scope(fn);
-  dsa::CacheView c;
-  dsa_status_t st = cache_view(fn, cache, &c);
+  std::vector<dsa::CacheView> views;
+  dsa_status_t st = cache_views(fn, caches, layers, &views);
   if (st != DSA_OK) return st;
   if (n < 0 || n > kIntMax) return fail(DSA_ERR_INVALID_ARG, "%s: n=%lld out of range", fn, (long long)n);
   if (n == 0) return DSA_OK;
@@ -1378,8 +1408,11 @@ dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* cache, const int32_t*
   st = make_ctx(stream, &ctx);
   if (st != DSA_OK) return st;
   dsa::call_param("n", n);
+  dsa::call_param("layers", layers);
   dsa::call_variant("a block per slice of a page");
-  cudaError_t e = timed_launch("copy_pages", ctx.stream, [&] { return dsa::launch_copy_pages(c, src, dst, n, ctx); });
+  cudaError_t e = timed_launch("copy_pages", ctx.stream, [&] {
+    return by_layers(views, [&](const dsa::CacheSet& set, bool) { return dsa::launch_copy_pages(set, src, dst, n, ctx); });
+  }, layer_launches(views));
   if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_copy_pages: launch");
   return DSA_OK;
 } catch (...) {
@@ -1425,17 +1458,17 @@ dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, const int32_t* src,
-                            const int32_t* dst, int64_t n, int32_t* result, void* workspace, size_t ws_bytes,
-                            void* stream) try {
+dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
+                            const int32_t* src, const int32_t* dst, int64_t n, int32_t* result, void* workspace,
+                            size_t ws_bytes, void* stream) try {
   const char* fn = "dsa_cache_fork";
   const dsa::CallScope scope(fn);
-  dsa::CacheView c;
+  std::vector<dsa::CacheView> views;
   dsa::PageTableView t;
-  dsa_status_t st = cache_view(fn, cache, &c);
+  dsa_status_t st = cache_views(fn, caches, layers, &views);
   if (st == DSA_OK) st = table_view(fn, pages, &t);
   if (st != DSA_OK) return st;
-  if (pages->num_pages != cache->num_pages || pages->page_size != cache->page_size)
+  if (pages->num_pages != caches->num_pages || pages->page_size != caches->page_size)
     return fail(DSA_ERR_INVALID_ARG, "%s: the page table is another cache's (pages or page size differ)", fn);
   if (n < 0 || n > t.max_seqs)
     return fail(DSA_ERR_INVALID_ARG, "%s: n=%lld children out of range (0..max_seqs=%d)", fn, (long long)n, t.max_seqs);
@@ -1449,10 +1482,18 @@ dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* cache, const dsa_page_table
   if (st != DSA_OK) return st;
   dsa::call_param("n", n);
   dsa::call_param("max_seqs", t.max_seqs);
+  dsa::call_param("layers", layers);
   dsa::call_variant("plan, then a block per slice of a last page");
-  cudaError_t e = timed_launch("cache_fork", ctx.stream, [&] {
-    return dsa::launch_cache_fork(c, t, src, dst, static_cast<int>(n), result, static_cast<int32_t*>(workspace), ctx);
-  }, n > 0 ? 2 : 1);
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  cudaError_t e = timed_launch("fork_plan", ctx.stream, [&] {
+    return dsa::launch_fork_plan(t, views[0].shift, views[0].num_pages, src, dst, static_cast<int>(n), result, ws, ctx);
+  });
+  if (e == cudaSuccess && n > 0)
+    e = timed_launch("fork_apply", ctx.stream, [&] {
+      return by_layers(views, [&](const dsa::CacheSet& set, bool first) {
+        return dsa::launch_fork_apply(set, first, t, src, dst, static_cast<int>(n), ws, ctx);
+      });
+    }, layer_launches(views));
   if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_fork: launch");
   return DSA_OK;
 } catch (...) {
@@ -1483,29 +1524,37 @@ dsa_status_t dsa_cache_free(const dsa_page_table_t* pages, const int32_t* seqs, 
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* cache, const dsa_page_table_t* pages, int32_t* result,
-                               void* workspace, size_t ws_bytes, void* stream) try {
+dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
+                               int32_t* result, void* workspace, size_t ws_bytes, void* stream) try {
   const char* fn = "dsa_cache_compact";
   const dsa::CallScope scope(fn);
-  dsa::CacheView c;
+  std::vector<dsa::CacheView> views;
   dsa::PageTableView t;
-  dsa_status_t st = cache_view(fn, cache, &c);
+  dsa_status_t st = cache_views(fn, caches, layers, &views);
   if (st == DSA_OK) st = table_view(fn, pages, &t);
   if (st != DSA_OK) return st;
-  if (pages->num_pages != cache->num_pages || pages->page_size != cache->page_size)
+  if (pages->num_pages != caches->num_pages || pages->page_size != caches->page_size)
     return fail(DSA_ERR_INVALID_ARG, "%s: the page table is another cache's (pages or page size differ)", fn);
   if (!result || !aligned4(result)) return fail(DSA_ERR_INVALID_ARG, "%s: result must be 4-byte aligned device words", fn);
-  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(dsa::compact_ws_words(c.num_pages)) * 4);
+  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(dsa::compact_ws_words(views[0].num_pages)) * 4);
   if (st != DSA_OK) return st;
   dsa::LaunchCtx ctx;
   st = make_ctx(stream, &ctx);
   if (st != DSA_OK) return st;
-  dsa::call_param("num_pages", c.num_pages);
+  dsa::call_param("num_pages", views[0].num_pages);
   dsa::call_param("max_seqs", t.max_seqs);
+  dsa::call_param("layers", layers);
   dsa::call_variant("plan, then copies in slices of a page");
-  cudaError_t e = timed_launch("cache_compact", ctx.stream, [&] {
-    return dsa::launch_cache_compact(c, t, result, static_cast<int32_t*>(workspace), ctx);
-  }, 2);
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  cudaError_t e = timed_launch("compact_plan", ctx.stream, [&] {
+    return dsa::launch_compact_plan(t, views[0].num_pages, result, ws, ctx);
+  });
+  if (e == cudaSuccess)
+    e = timed_launch("compact_apply", ctx.stream, [&] {
+      return by_layers(views, [&](const dsa::CacheSet& set, bool first) {
+        return dsa::launch_compact_apply(set, first, t, ws, ctx);
+      });
+    }, layer_launches(views));
   if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_compact: launch");
   return DSA_OK;
 } catch (...) {

@@ -160,8 +160,9 @@ __device__ __forceinline__ void copy_slice(const CacheView& c, int64_t src, int6
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_pages_kernel(const CacheView c, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
-                      unsigned* status) {
+    copy_pages_kernel(const __grid_constant__ CacheSet set, const int32_t* __restrict__ src,
+                      const int32_t* __restrict__ dst, unsigned* status) {
+  const CacheView& c = set.v[blockIdx.z];
   const int s = src[blockIdx.x], d = dst[blockIdx.x];
   if (static_cast<unsigned>(s) >= static_cast<unsigned>(c.num_pages) ||
       static_cast<unsigned>(d) >= static_cast<unsigned>(c.num_pages)) {
@@ -426,11 +427,16 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
   plan_sync<kC>();  // no CTA leaves while another reads its shared memory
 }
 
-// Block (j, y): child j's part y.  Parts 0 .. slices-1 also copy a slice of
-// the last page; all parts share the row and the counts.
+// Block (j, y, z): child j's part y in layer z.  Parts 0 .. slices-1 copy a
+// slice of the last page; all parts of the first layer share the row and the
+// counts.  (No layer reads a row that the first one writes: a child's row was
+// free, and what has no tokens has no pages.)
 __global__ void __launch_bounds__(kCopyThreads)
-    fork_apply_kernel(const CacheView c, const PageTableView t, const int32_t* __restrict__ src,
-                      const int32_t* __restrict__ dst, int n, int32_t* ws_, unsigned* status) {
+    fork_apply_kernel(const __grid_constant__ CacheSet set, bool first, const PageTableView t,
+                      const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, int32_t* ws_,
+                      unsigned* status) {
+  const CacheView& c = set.v[blockIdx.z];
+  first = first && blockIdx.z == 0;
   const ForkWs ws = fork_ws(ws_, n);
   pdl_wait();  // the plan is written
   if (*ws.go == 0) return;
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(kCopyThreads)
   const int32_t* from = t.table + s * t.table_stride;
   int32_t* to = t.table + d * t.table_stride;
   const int fresh = part ? ws.list[ws.off[j]] : -1;
-  for (int x = blockIdx.y * kCopyThreads + threadIdx.x; x < t.max_pages; x += gridDim.y * kCopyThreads) {
+  for (int x = blockIdx.y * kCopyThreads + threadIdx.x; first && x < t.max_pages; x += gridDim.y * kCopyThreads) {
     int p = -1;
     if (x < full) {
       p = from[x];
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
     to[x] = p;
   }
-  if (blockIdx.y == 0 && threadIdx.x == 0) t.lens[d] = len;
+  if (first && blockIdx.y == 0 && threadIdx.x == 0) t.lens[d] = len;
   if (part && static_cast<int>(blockIdx.y) < page_slices(c)) {
     const int old = from[full];
     if (static_cast<unsigned>(old) < static_cast<unsigned>(c.num_pages)) copy_slice(c, old, fresh, blockIdx.y);
@@ -553,7 +559,9 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    compact_apply_kernel(const CacheView c, const PageTableView t, int32_t* ws_) {
+    compact_apply_kernel(const __grid_constant__ CacheSet set, bool first, const PageTableView t, int32_t* ws_) {
+  const CacheView& c = set.v[blockIdx.z];
+  first = first && blockIdx.z == 0;
   const CompactWs ws = compact_ws(ws_, c.num_pages);
   pdl_wait();  // the plan is written
   const int used = ws.head[0], moved = ws.head[1];
@@ -563,11 +571,12 @@ __global__ void __launch_bounds__(kCopyThreads)
     const int m = static_cast<int>(x / slices), sl = static_cast<int>(x % slices);
     const int from = ws.high[m], to = ws.hole[m];
     copy_slice(c, from, to, sl);
-    if (sl == 0 && threadIdx.x == 0) {
+    if (first && sl == 0 && threadIdx.x == 0) {
       t.count[to] = t.count[from];
       t.count[from] = 0;
     }
   }
+  if (!first) return;
   // table entries that name a moved page
   const int64_t entries = static_cast<int64_t>(t.max_seqs) * t.max_pages;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries;
@@ -592,10 +601,10 @@ cudaError_t launch_cache_append(const CacheView& c, const BatchView& b, const Ap
   return cudaGetLastError();
 }
 
-cudaError_t launch_copy_pages(const CacheView& c, const int32_t* src, const int32_t* dst, int64_t n,
+cudaError_t launch_copy_pages(const CacheSet& set, const int32_t* src, const int32_t* dst, int64_t n,
                               const LaunchCtx& ctx) {
-  copy_pages_kernel<<<dim3(static_cast<unsigned>(n), host_slices(c.shift)), kCopyThreads, 0, ctx.stream>>>(
-      c, src, dst, ctx.status);
+  copy_pages_kernel<<<dim3(static_cast<unsigned>(n), host_slices(set.v[0].shift), set.n), kCopyThreads, 0,
+                      ctx.stream>>>(set, src, dst, ctx.status);
   return cudaGetLastError();
 }
 
@@ -613,23 +622,27 @@ cudaError_t launch_cache_reserve(const PageTableView& t, int shift, int num_page
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_fork(const CacheView& c, const PageTableView& t, const int32_t* src, const int32_t* dst,
-                              int n, int32_t* result, int32_t* ws, const LaunchCtx& ctx) {
-  if (c.num_pages <= kPlanAlone)
-    fork_plan_kernel<1>
-        <<<1, kPlanThreads, 0, ctx.stream>>>(t, c.shift, c.num_pages, src, dst, n, result, ws, ctx.status);
+cudaError_t launch_fork_plan(const PageTableView& t, int shift, int num_pages, const int32_t* src, const int32_t* dst,
+                             int n, int32_t* result, int32_t* ws, const LaunchCtx& ctx) {
+  if (num_pages <= kPlanAlone)
+    fork_plan_kernel<1><<<1, kPlanThreads, 0, ctx.stream>>>(t, shift, num_pages, src, dst, n, result, ws, ctx.status);
   else
     fork_plan_kernel<kPlanCtas>
-        <<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, c.shift, c.num_pages, src, dst, n, result, ws, ctx.status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || n == 0) return e;
+        <<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, shift, num_pages, src, dst, n, result, ws, ctx.status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fork_apply(const CacheSet& set, bool first, const PageTableView& t, const int32_t* src,
+                              const int32_t* dst, int n, int32_t* ws, const LaunchCtx& ctx) {
   // parts of a child: one per slice of its last page, and enough that a thread
   // copies at most 4 entries of the row (8 parts at the most for long rows)
-  const int by_row = (t.max_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
-  const int parts = host_slices(c.shift) > by_row ? host_slices(c.shift) : by_row < 8 ? by_row : 8;
+  const int slices = host_slices(set.v[0].shift);
+  const int by_row = first ? (t.max_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads) : 1;
+  const int parts = slices > by_row ? slices : by_row < 8 ? by_row : 8;
   LaunchCtx early = ctx;
-  early.pdl = 1;
-  return launch_ex(early, fork_apply_kernel, dim3(n, parts), dim3(kCopyThreads), 0, c, t, src, dst, n, ws, ctx.status);
+  early.pdl = first;  // (only the plan stands right before the first)
+  return launch_ex(early, fork_apply_kernel, dim3(n, parts, set.n), dim3(kCopyThreads), 0, set, first, t, src, dst, n,
+                   ws, ctx.status);
 }
 
 cudaError_t launch_cache_free(const PageTableView& t, int shift, int num_pages, const int32_t* seqs, int n,
@@ -638,17 +651,21 @@ cudaError_t launch_cache_free(const PageTableView& t, int shift, int num_pages, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_compact(const CacheView& c, const PageTableView& t, int32_t* result, int32_t* ws,
-                                 const LaunchCtx& ctx) {
-  if (c.num_pages <= kPlanAlone)
-    compact_plan_kernel<1><<<1, kPlanThreads, 0, ctx.stream>>>(t, c.num_pages, result, ws);
+cudaError_t launch_compact_plan(const PageTableView& t, int num_pages, int32_t* result, int32_t* ws,
+                                const LaunchCtx& ctx) {
+  if (num_pages <= kPlanAlone)
+    compact_plan_kernel<1><<<1, kPlanThreads, 0, ctx.stream>>>(t, num_pages, result, ws);
   else
-    compact_plan_kernel<kPlanCtas><<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, c.num_pages, result, ws);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+    compact_plan_kernel<kPlanCtas><<<kPlanCtas, kPlanThreads, 0, ctx.stream>>>(t, num_pages, result, ws);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact_apply(const CacheSet& set, bool first, const PageTableView& t, int32_t* ws,
+                                 const LaunchCtx& ctx) {
   LaunchCtx early = ctx;
-  early.pdl = 1;
-  return launch_ex(early, compact_apply_kernel, dim3(ctx.num_sms * 16), dim3(kCopyThreads), 0, c, t, ws);
+  early.pdl = first;  // (only the plan stands right before the first)
+  return launch_ex(early, compact_apply_kernel, dim3((ctx.num_sms * 16 + set.n - 1) / set.n, 1, set.n), dim3(kCopyThreads),
+                   0, set, first, t, ws);
 }
 
 }  // namespace dsa

@@ -48,8 +48,16 @@ struct AppendArgs {
   int64_t k_stride, v_stride, kidx_stride;  // elements from row to row
 };
 
+// The layers of one launch that moves pages: their caches have the same pages
+// of the same size.  Passed by value as a kernel parameter.
+constexpr int kLayerBatch = 32;
+struct CacheSet {
+  int n;
+  CacheView v[kLayerBatch];
+};
+
 cudaError_t launch_cache_append(const CacheView& c, const BatchView& b, const AppendArgs& a, const LaunchCtx& ctx);
-cudaError_t launch_copy_pages(const CacheView& c, const int32_t* src, const int32_t* dst, int64_t n,
+cudaError_t launch_copy_pages(const CacheSet& set, const int32_t* src, const int32_t* dst, int64_t n,
                               const LaunchCtx& ctx);
 // Scratch words (int32) of the page operators below.
 int64_t fork_ws_words(int64_t n, int max_seqs);
@@ -57,11 +65,17 @@ int64_t reserve_ws_words(int max_seqs, int num_pages);
 int64_t compact_ws_words(int num_pages);
 cudaError_t launch_cache_reserve(const PageTableView& t, int shift, int num_pages, const int32_t* add, int32_t* result,
                                  int32_t* ws, const LaunchCtx& ctx);
-cudaError_t launch_cache_fork(const CacheView& c, const PageTableView& t, const int32_t* src, const int32_t* dst,
-                              int n, int32_t* result, int32_t* ws, const LaunchCtx& ctx);
+// Forking and compacting: the plan, then apply once per batch of layers; `first`
+// also changes the table and the counts.
+cudaError_t launch_fork_plan(const PageTableView& t, int shift, int num_pages, const int32_t* src, const int32_t* dst,
+                             int n, int32_t* result, int32_t* ws, const LaunchCtx& ctx);
+cudaError_t launch_fork_apply(const CacheSet& set, bool first, const PageTableView& t, const int32_t* src,
+                              const int32_t* dst, int n, int32_t* ws, const LaunchCtx& ctx);
 cudaError_t launch_cache_free(const PageTableView& t, int shift, int num_pages, const int32_t* seqs, int n,
                               const LaunchCtx& ctx);
-cudaError_t launch_cache_compact(const CacheView& c, const PageTableView& t, int32_t* result, int32_t* ws,
+cudaError_t launch_compact_plan(const PageTableView& t, int num_pages, int32_t* result, int32_t* ws,
+                                const LaunchCtx& ctx);
+cudaError_t launch_compact_apply(const CacheSet& set, bool first, const PageTableView& t, int32_t* ws,
                                  const LaunchCtx& ctx);
 
 // Indexer over the pages: scores of launch rows [row0, row0 + nrows) into

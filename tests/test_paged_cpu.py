@@ -103,24 +103,38 @@ def test_page_operators_are_checked(lib):
     assert lib.dsa_cache_reserve(t, FAKE, FAKE, FAKE, 4, None) == WORKSPACE
     assert lib.dsa_cache_reserve(t, None, FAKE, FAKE, size, None) == INVALID
     assert lib.dsa_cache_reserve(t, FAKE, FAKE, FAKE + 4, size, None) == INVALID
-    assert lib.dsa_cache_fork(c, t, FAKE, FAKE, 3, FAKE, FAKE, size, None) == INVALID  # more children than rows
-    assert lib.dsa_cache_fork(c, t, FAKE, None, 2, FAKE, FAKE, size, None) == INVALID
-    assert lib.dsa_cache_fork(c, t, FAKE, FAKE, 2, FAKE, None, 0, None) == WORKSPACE
+    assert lib.dsa_cache_fork(c, 1, t, FAKE, FAKE, 3, FAKE, FAKE, size, None) == INVALID  # more children than rows
+    assert lib.dsa_cache_fork(c, 1, t, FAKE, None, 2, FAKE, FAKE, size, None) == INVALID
+    assert lib.dsa_cache_fork(c, 1, t, FAKE, FAKE, 2, FAKE, None, 0, None) == WORKSPACE
     assert lib.dsa_cache_free(t, None, 2, None) == INVALID and lib.dsa_cache_free(t, FAKE, -1, None) == INVALID
     assert lib.dsa_cache_free(t, None, 0, None) == OK
-    assert lib.dsa_cache_compact(c, t, None, FAKE, size, None) == INVALID
-    assert lib.dsa_cache_compact(c, t, FAKE, FAKE, 16, None) == WORKSPACE
-    assert lib.dsa_cache_copy_pages(c, None, FAKE, 1, None) == INVALID
-    assert lib.dsa_cache_copy_pages(c, None, None, 0, None) == OK
+    assert lib.dsa_cache_compact(c, 1, t, None, FAKE, size, None) == INVALID
+    assert lib.dsa_cache_compact(c, 1, t, FAKE, FAKE, 16, None) == WORKSPACE
+    assert lib.dsa_cache_copy_pages(c, 1, None, FAKE, 1, None) == INVALID
+    assert lib.dsa_cache_copy_pages(c, 1, None, None, 0, None) == OK
     for kw in (dict(t_pages=11), dict(t_page=32)):  # another cache's table
         c, _, t = structs(**kw)
-        assert lib.dsa_cache_fork(c, t, FAKE, FAKE, 1, FAKE, FAKE, BIG, None) == INVALID
-        assert lib.dsa_cache_compact(c, t, FAKE, FAKE, BIG, None) == INVALID
+        assert lib.dsa_cache_fork(c, 1, t, FAKE, FAKE, 1, FAKE, FAKE, BIG, None) == INVALID
+        assert lib.dsa_cache_compact(c, 1, t, FAKE, FAKE, BIG, None) == INVALID
     for kw, status in ((dict(t_page=20), UNSUPPORTED), (dict(max_seqs=0), INVALID), (dict(count=None), INVALID),
                        (dict(stride=7), INVALID), (dict(t_pages=0), INVALID)):
         _, _, t = structs(**kw)
         assert lib.dsa_cache_free(t, FAKE, 1, None) == status, kw
         assert lib.dsa_cache_reserve(t, FAKE, FAKE, FAKE, BIG, None) == status, kw
+
+
+def test_layers_are_checked(lib):
+    from long_context_sparse_index_gb300 import _paged as p
+    one, _, t = structs()
+    size = lib.dsa_cache_workspace(10, 2, 2)
+    assert lib.dsa_cache_copy_pages(one, 0, FAKE, FAKE, 1, None) == INVALID
+    assert lib.dsa_cache_copy_pages(None, 1, FAKE, FAKE, 1, None) == INVALID
+    a = structs()[0]._obj
+    for kw in (dict(num_pages=11), dict(page=32, ks=4096, vs=4096, kis=2048, khs=1024), dict(v=None)):
+        two = (p._CacheStruct * 2)(a, structs(**kw)[0]._obj)
+        assert lib.dsa_cache_copy_pages(two, 2, FAKE, FAKE, 1, None) == INVALID, kw
+        assert lib.dsa_cache_fork(two, 2, t, FAKE, FAKE, 1, FAKE, FAKE, size, None) == INVALID, kw
+        assert lib.dsa_cache_compact(two, 2, t, FAKE, FAKE, size, None) == INVALID, kw
 
 
 def test_workspace_sizes(lib):

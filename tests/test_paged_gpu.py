@@ -405,6 +405,29 @@ def test_compact_shared_pages_and_large_pages():
     check_moves(cache, before, moves)
 
 
+@pytest.mark.parametrize("layers", [2, 33])
+def test_layers_move_together(layers):
+    """fork, compact and copy_pages of several layers' caches (more than one launch takes): one table, every layer's
+    pages alike."""
+    caches = [random_cache(24, 16, seed=l, apart=8 * (l % 3)) for l in range(layers)]
+    p = Pages([40, 17, 0, 0], 16, 24, 5, seed=3)
+    t, before = p.to_gpu(), [[b.clone() for b in buffers(c)] for c in caches]
+    got = dsa.dsa_cache_fork(caches, t, i32([0, 1]), i32([2, 3]))
+    dsa.dsa_cache_free(caches[0], t, i32([0]))
+    info = dsa.dsa_cache_compact(tuple(caches), t)
+    dsa.dsa_cache_copy_pages(caches, i32([0, 1]), i32([22, 23]))
+    dsa.dsa_sync_status()
+    taken, moves = p.fork([0, 1], [2, 3])
+    p.free([0])
+    used, more = p.compact()
+    assert got.item() == taken and info.tolist() == [used, len(more)]
+    p.check(t)
+    for c, b in zip(caches, before):
+        check_moves(c, b, moves + more + [(0, 22), (1, 23)])
+    with pytest.raises(TypeError):
+        dsa.dsa_cache_compact([], t)
+
+
 # --------------------------------------------------------------------------- indexer + top-k
 
 def index_inputs(m, Hi, ints=True, seed=7, pad=0):
