@@ -294,18 +294,19 @@ def cache_workspace_size(num_pages: int, max_seqs: int, n: int = 0) -> int:
     return int(load().dsa_cache_workspace(num_pages, max_seqs, n))
 
 
-def _of_cache(cache: PagedCache, pages: PageTable) -> int:
+def _of_cache(cache, pages: PageTable) -> int:
     dev = _device_of(cache, pages)
     if pages.num_pages != cache.num_pages:
         raise ValueError(f"the page table counts {pages.num_pages} pages, the cache has {cache.num_pages}")
     return dev
 
 
-def dsa_cache_reserve(cache: PagedCache, pages: PageTable, add, result=None, workspace=None, stream=None):
+def dsa_cache_reserve(cache, pages: PageTable, add, result=None, workspace=None, stream=None):
     """Changes the length of every sequence s by add[s] tokens (int32
     [max_seqs]): longer ones take the lowest free pages, shorter ones give
     theirs back; returns a device word: pages taken, or minus the number
-    lacking (then nothing changed)."""
+    lacking (then nothing changed).  cache: the one, or the layers'."""
+    cache = _layers(cache)[0]
     dev, lib = _of_cache(cache, pages), load()
     _ids(add, "add", dev)
     _shape(add, "add", (pages.max_seqs,))
@@ -319,8 +320,8 @@ def dsa_cache_reserve(cache: PagedCache, pages: PageTable, add, result=None, wor
 def dsa_cache_fork(cache, pages: PageTable, src, dst, result=None, workspace=None, stream=None):
     """Row dst[j] becomes a copy of sequence src[j] (int32 tensors): full pages
     shared, a partly filled last page copied, in a cache or in every layer's (a
-    sequence of caches); returns a device word: pages
-    taken, or minus the number lacking (then nothing changed)."""
+    sequence of caches); returns a device word: pages taken, or minus the
+    number lacking (then nothing changed)."""
     cache, ref, layers = _layers(cache)
     dev, lib = _of_cache(cache, pages), load()
     n = _ids(src, "src", dev)
@@ -333,8 +334,10 @@ def dsa_cache_fork(cache, pages: PageTable, src, dst, result=None, workspace=Non
     return result
 
 
-def dsa_cache_free(cache: PagedCache, pages: PageTable, seqs, stream=None):
-    """Frees the sequences named in seqs (int32 tensor)."""
+def dsa_cache_free(cache, pages: PageTable, seqs, stream=None):
+    """Frees the sequences named in seqs (int32 tensor).  cache: the one, or
+    the layers'."""
+    cache = _layers(cache)[0]
     dev = _of_cache(cache, pages)
     n = _ids(seqs, "seqs", dev)
     _check(load().dsa_cache_free(pages._with_page(cache.page_size), seqs.data_ptr(), n, _handle(stream, dev)))

@@ -1220,11 +1220,16 @@ constexpr int64_t kIntMax = 0x7FFFFFFFLL;
 constexpr int64_t kPagedScratch = int64_t{1} << 28;  // scores of a pass in the recommended workspace (1 GiB)
 constexpr int64_t kPagedPassMax = int64_t{1} << 31;  // scores of a pass however large the workspace
 constexpr int kPagedMinRows = 8;
-// Rows per sequence (on average) from which the tcgen05 scores are taken: their
-// 128-row tiles cost the same however few rows they hold, the mma.sync kernel
-// grows with every 8.  Measured at 32 heads, mma.sync / tcgen05: one sequence of
-// 131072 tokens 31 / 33 us at 16 rows and 36 / 33 at 24; 16 sequences of 32768
-// tokens 76 / 102 and 105 / 102; 64 of 8192 76 / 104 and 107 / 105.
+// Rows from which a sequence's scores are taken on tcgen05: its 128-row tiles
+// cost the same however few rows they hold, the mma.sync kernel grows with
+// every 8.  Measured at 32 heads, mma.sync / tcgen05: one sequence of 131072
+// tokens 31 / 33 us at 16 rows and 36 / 33 at 24; 16 sequences of 32768 tokens
+// 76 / 102 and 105 / 102; 64 of 8192 76 / 104 and 107 / 105.  Each sequence goes
+// by its own rows, which the device knows: both kernels are launched, each for
+// its own, unless the host can tell that one of them has none.  A chunk of 2048
+// rows at 131072 tokens among 63 single tokens takes 502 us; by the average, on
+// one kernel, it took 1045 (and one of 512 rows 99 against 327); a launch
+// without work of its own costs 2.6 us (16 drafts of 7 tokens: 53.3 against 50.7).
 constexpr int kPagedTcRows = 24;
 
 bool page_size_ok(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
@@ -1604,9 +1609,14 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
   dsa::call_param("Hi", Hi);
   dsa::call_param("topk", topk);
   dsa::call_param("rows_per_pass", pass);
-  const bool tc = b.rows >= kPagedTcRows * b.batch && dsa::paged_scores_tc_fits(b);
-  dsa::call_variant(tc ? "tcgen05 scores of 128-row tiles, then a row's top-k per CTA"
-                       : "mma.sync scores of a few rows a sequence, then a row's top-k per CTA");
+  // (the others' rows taken off, one each: what the longest may have)
+  const bool tc = b.rows - b.batch + 1 >= kPagedTcRows && dsa::paged_scores_tc_fits(b);
+  const bool few = !tc || b.batch > 1;
+  const int tc_rows = !tc ? INT32_MAX : few ? kPagedTcRows : 0;
+  dsa::call_variant(!few ? "tcgen05 scores of 128-row tiles, then a row's top-k per CTA"
+                    : !tc ? "mma.sync scores of a few rows a sequence, then a row's top-k per CTA"
+                          : "tcgen05 scores of sequences with many rows and mma.sync scores of those with few, then a "
+                            "row's top-k per CTA");
   CUtensorMap q_map, k_map;
   if (tc) {
     st = paged_score_maps(fn, c, q_idx, b.rows, Hi, &q_map, &k_map);
@@ -1616,10 +1626,15 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
   float* tops = scores + pass * ld;
   for (int64_t r = 0; r < b.rows; r += pass) {
     const int64_t n = b.rows - r < pass ? b.rows - r : pass;
-    cudaError_t e = timed_launch(tc ? "paged_scores_tc" : "paged_scores", ctx.stream, [&] {
-      return tc ? dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, scores, tops, ld, ctx)
-                : dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, scores, tops, ld, ctx);
-    });
+    cudaError_t e = cudaSuccess;
+    if (tc)
+      e = timed_launch("paged_scores_tc", ctx.stream, [&] {
+        return dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, tc_rows, scores, tops, ld, ctx);
+      });
+    if (e == cudaSuccess && few)
+      e = timed_launch("paged_scores", ctx.stream, [&] {
+        return dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, tc_rows, scores, tops, ld, tc, ctx);
+      });
     if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: scores launch");
     e = timed_launch("paged_select", ctx.stream, [&] {
       return dsa::launch_paged_select(b, c.shift, r, n, scores, tops, ld, topk, pool_idx, ctx);

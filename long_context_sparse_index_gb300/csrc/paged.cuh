@@ -65,6 +65,11 @@ __device__ __forceinline__ int page_of(const BatchView& b, int num_pages, int s,
   return -1;
 }
 
+// New tokens of sequence s in the whole call.
+__device__ __forceinline__ int64_t call_rows(const BatchView& b, int s) {
+  return static_cast<int64_t>(__ldg(b.cu + s + 1)) - __ldg(b.cu + s);
+}
+
 // ----------------------------------------------------------------- thread-block clusters
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");

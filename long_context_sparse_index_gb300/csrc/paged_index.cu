@@ -134,8 +134,8 @@ __device__ __noinline__ Run next_run(const BatchView& b, int shift, const int* o
 template <int kMt>
 __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
     paged_score_kernel(const CacheView c, const BatchView b, const __nv_bfloat16* __restrict__ q,
-                       const float* __restrict__ w, int Hi, int64_t row0, int64_t row1, float* __restrict__ scores,
-                       float* __restrict__ tops, int64_t ld, unsigned* status) {
+                       const float* __restrict__ w, int Hi, int64_t row0, int64_t row1, int tc_rows,
+                       float* __restrict__ scores, float* __restrict__ tops, int64_t ld, unsigned* status) {
   extern __shared__ int off[];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -143,11 +143,12 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
   item_prefix(off, b.batch, [&](int s) {
     int64_t first;
     const int n = seq_rows(b, s, row0, row1, &first);
-    if (n == 0) return 0;
+    if (n == 0 || call_rows(b, s) >= tc_rows) return 0;
     const int64_t tiles = (seq_pools(b, c.shift, s, first, n) + kTile - 1) / kTile;
     const int64_t items = tiles * ((n + kRows - 1) / kRows);
     return static_cast<int>(items < kMaxItems ? items : kMaxItems);
   });
+  pdl_wait();  // launched early behind the chunk scores (what was read above is older than their launch)
   const int total = off[b.batch];
   int it = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
   const int it1 = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
@@ -700,12 +701,13 @@ __global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kThr == 256 ? 5 : 2)
 
 template <int kMt>
 cudaError_t launch_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                          int64_t row0, int64_t nrows, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx) {
+                          int64_t row0, int64_t nrows, int tc_rows, float* scores, float* tops, int64_t ld,
+                          const LaunchCtx& ctx) {
   const size_t smem = static_cast<size_t>(b.batch + 1) * sizeof(int);
   const int grid = ctx.num_sms * (kMt <= 2 ? 3 : 2);
-  paged_score_kernel<kMt><<<grid, kThreads, smem, ctx.stream>>>(c, b, static_cast<const __nv_bfloat16*>(q_idx), w, Hi,
-                                                                row0, row0 + nrows, scores, tops, ld, ctx.status);
-  return cudaGetLastError();
+  return launch_ex(ctx, paged_score_kernel<kMt>, dim3(grid), dim3(kThreads), smem, c, b,
+                   static_cast<const __nv_bfloat16*>(q_idx), w, Hi, row0, row0 + nrows, tc_rows, scores, tops, ld,
+                   ctx.status);
 }
 
 template <int kCap, int kThr>
@@ -729,11 +731,13 @@ cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t n
 }  // namespace
 
 cudaError_t launch_paged_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                                int64_t row0, int64_t nrows, float* scores, float* tops, int64_t ld,
-                                const LaunchCtx& ctx) {
-  if (Hi <= 16) return launch_scores<1>(c, b, q_idx, w, Hi, row0, nrows, scores, tops, ld, ctx);
-  if (Hi <= 32) return launch_scores<2>(c, b, q_idx, w, Hi, row0, nrows, scores, tops, ld, ctx);
-  return launch_scores<4>(c, b, q_idx, w, Hi, row0, nrows, scores, tops, ld, ctx);
+                                int64_t row0, int64_t nrows, int tc_rows, float* scores, float* tops, int64_t ld,
+                                bool early, const LaunchCtx& call) {
+  LaunchCtx ctx = call;
+  ctx.pdl = early;
+  if (Hi <= 16) return launch_scores<1>(c, b, q_idx, w, Hi, row0, nrows, tc_rows, scores, tops, ld, ctx);
+  if (Hi <= 32) return launch_scores<2>(c, b, q_idx, w, Hi, row0, nrows, tc_rows, scores, tops, ld, ctx);
+  return launch_scores<4>(c, b, q_idx, w, Hi, row0, nrows, tc_rows, scores, tops, ld, ctx);
 }
 
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,

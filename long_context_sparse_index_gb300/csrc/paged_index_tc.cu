@@ -61,6 +61,7 @@ struct TcArgs {
   const float* w;
   int Hi;
   int64_t row0, row1;
+  int tc_rows;  // sequences of fewer rows in the call are the other kernel's
   float* scores;
   float* tops;
   int64_t ld;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s < a.b.batch) {
         int64_t first;
         const int n = seq_rows(a, s, &first);
-        if (n > 0) {
+        if (n > 0 && call_rows(a.b, s) >= a.tc_rows) {
           const int64_t items = (seq_pools(a, s, first, n) + kBN - 1) / kBN * ((n + kBM - 1) / kBM);
           v = static_cast<int>(min(items, static_cast<int64_t>(kMaxItems)));
         }
@@ -400,12 +401,12 @@ bool paged_scores_tc_fits(const BatchView& b) { return b.batch <= kMaxBatchTc; }
 
 cudaError_t launch_paged_scores_tc(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                    const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
-                                   float* scores, float* tops, int64_t ld, const LaunchCtx& ctx) {
+                                   int tc_rows, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx) {
   static std::atomic<bool> attr_done[kAttrDevices];
   const cudaError_t e =
       set_smem_limit_once(paged_score_tc_kernel, static_cast<int>(smem_bytes(kMaxBatchTc)), attr_done);
   if (e != cudaSuccess) return e;
-  const TcArgs a{c, b, w, Hi, row0, row0 + nrows, scores, tops, ld, ctx.status, ctx.wait_limit_ns, ctx.inject_timeout};
+  const TcArgs a{c, b, w, Hi, row0, row0 + nrows, tc_rows, scores, tops, ld, ctx.status, ctx.wait_limit_ns, ctx.inject_timeout};
   paged_score_tc_kernel<<<ctx.num_sms, kThreads, smem_bytes(b.batch), ctx.stream>>>(q_map, k_map, a);
   return cudaGetLastError();
 }

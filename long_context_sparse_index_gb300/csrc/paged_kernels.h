@@ -81,16 +81,19 @@ cudaError_t launch_compact_apply(const CacheSet& set, bool first, const PageTabl
 // Indexer over the pages: scores of launch rows [row0, row0 + nrows) into
 // scores [nrows][ld] (pool p of a row's sequence in column p) and the largest
 // of each eight pools into tops [nrows][ld / 8], then each row's top-k.  ld is
-// a multiple of 32.
+// a multiple of 32.  Only sequences with fewer than tc_rows rows in the call;
+// early: launched early behind the tcgen05 scores of the others.
 cudaError_t launch_paged_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                                int64_t row0, int64_t nrows, float* scores, float* tops, int64_t ld,
-                                const LaunchCtx& ctx);
-// The same on tcgen05, 128 rows of a sequence at a time: for chunks.  q_map: [64, Hi, rows], box {64, 1, 128}; k_map:
-// [128, pools per page, pages], box {64, pools per page, 1}; both swizzled by 128 bytes.
+                                int64_t row0, int64_t nrows, int tc_rows, float* scores, float* tops, int64_t ld,
+                                bool early, const LaunchCtx& ctx);
+// The same on tcgen05, 128 rows of a sequence at a time, for sequences with at
+// least tc_rows rows: chunks.  q_map: [64, Hi, rows], box {64, 1, 128}; k_map:
+// [128, pools per page, pages], box {64, pools per page, 1}; both swizzled by
+// 128 bytes.
 bool paged_scores_tc_fits(const BatchView& b);
 cudaError_t launch_paged_scores_tc(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                    const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
-                                   float* scores, float* tops, int64_t ld, const LaunchCtx& ctx);
+                                   int tc_rows, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx);
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,
                                 const float* tops, int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx);
 

@@ -413,7 +413,7 @@ def test_layers_move_together(layers):
     p = Pages([40, 17, 0, 0], 16, 24, 5, seed=3)
     t, before = p.to_gpu(), [[b.clone() for b in buffers(c)] for c in caches]
     got = dsa.dsa_cache_fork(caches, t, i32([0, 1]), i32([2, 3]))
-    dsa.dsa_cache_free(caches[0], t, i32([0]))
+    dsa.dsa_cache_free(caches, t, i32([0]))
     info = dsa.dsa_cache_compact(tuple(caches), t)
     dsa.dsa_cache_copy_pages(caches, i32([0, 1]), i32([22, 23]))
     dsa.dsa_sync_status()
@@ -424,8 +424,9 @@ def test_layers_move_together(layers):
     p.check(t)
     for c, b in zip(caches, before):
         check_moves(c, b, moves + more + [(0, 22), (1, 23)])
-    with pytest.raises(TypeError):
-        dsa.dsa_cache_compact([], t)
+    for bad in ([], None, [t], 3):
+        with pytest.raises(TypeError):
+            dsa.dsa_cache_compact(bad, t)
 
 
 # --------------------------------------------------------------------------- indexer + top-k
@@ -474,6 +475,26 @@ def test_index_long_bit_exact(new, old, page, Hi, topk):
     got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
     dsa.dsa_sync_status()
     check_topk(m, q, w, topk, got)
+
+
+@pytest.mark.parametrize("new,kernels", [
+    ([1, 1, 200, 1, 0, 1], ["paged_scores_tc", "paged_scores"]),      # a chunk among single tokens
+    ([23, 24, 25, 1], ["paged_scores_tc", "paged_scores"]),           # on both sides of the rule
+    ([4, 6, 4, 5, 5, 6], ["paged_scores_tc", "paged_scores"]),        # one of them could be long; none is
+    ([30, 150], ["paged_scores_tc", "paged_scores"]),                 # all of them are
+    ([23], ["paged_scores"]), ([24], ["paged_scores_tc"]), ([24] + [0] * 30, ["paged_scores"])])
+def test_index_takes_each_sequence_by_its_own_rows(new, kernels):
+    m = Model(new, [2500 + 700 * j for j in range(len(new))], 64, seed=15, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 8, pad=0)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 100)
+    ran = [k for k, _ in dsa.last_kernel_config()["kernels"]]
+    least = torch.empty(8 * (m.width * 16 + 31) // 32 * 36 * 4 + 8 * 36 * 4, dtype=torch.uint8, device=DEV)
+    small = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 100, workspace=least)
+    dsa.dsa_sync_status()
+    assert ran == kernels + ["paged_select"]
+    check_topk(m, q, w, 100, got)
+    assert torch.equal(got, small)
 
 
 @pytest.mark.parametrize("case", ["zeros", "two_values", "huge", "one_high", "overflow", "negative", "runs"])
