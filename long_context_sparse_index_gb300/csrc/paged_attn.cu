@@ -6,12 +6,12 @@
 // share one KV head:
 //   o = sum_j exp(s q.k_j - lse) v_j,  lse = log sum_j exp(s q.k_j)
 // in fp32, over bf16 products; P is rounded to bf16 for its product with V
-// (relative 2^-9 of each weight, averaged over the keys; the normaliser sums
+// (at most 2^-8 of each weight, either way over the keys; the normaliser sums
 // the unrounded weights), and o once more at the end.
 //
-// Layout of the work: a cluster of C CTAs (1 to 8) of four warps per row.  CTA c takes the row's 64-key blocks c, c + C, ...; each warp gathers
-// the K and V rows of its own 16 keys of a block with 16-byte cp.async copies
-// into its quarter of a ring of kStages blocks (rows XOR-swizzled in 16-B
+// Layout of the work: a cluster of C CTAs (1 to 8) of four warps per row.  CTA
+// c takes the row's 64-key blocks c, c + C, ...; each warp gathers the K and V
+// rows of its own 16 keys of a block with 16-byte cp.async copies into its quarter of a ring of kStages blocks (rows XOR-swizzled in 16-B
 // chunks so that ldmatrix reads are conflict-free) and waits only for its own
 // copies.  S = Q K^T and O += P V run on mma.sync m16n8k16 (M = the 16 heads).
 // The warps' partial softmax states (m, l, O) are merged through shared

@@ -553,6 +553,45 @@ def check_selected(m, q, w, topk, got):
         assert ((s + slack)[kept].min() >= (s - slack)[~kept].max()), (r, b, i)
 
 
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("new,old", [([1, 2, 5], [3000, 701, 40]), ([130, 1, 27], [3001, 5000, 0])])
+def test_index_reads_nothing_it_may_not_see(new, old, page):
+    """NaN and infinities in every pooled key that no row may see: pools past a row's end, later pages, other pages."""
+    m = Model(new, old, page, seed=16, ints=True)
+    seen = torch.zeros(m.khat.shape[0] * m.khat.shape[1], dtype=torch.bool)
+    for b, n in enumerate(m.lens):
+        for p in range((n - 1) // 4):
+            seen[m.slot(b, 4 * p) // 4] = True
+    flat = m.khat.view(-1, 2 * DI)
+    flat[~seen] = math.nan
+    flat[(~seen).nonzero()[::2, 0], :DI] = math.inf
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 8)
+    for topk in (5, 600):
+        got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+        dsa.dsa_sync_status()
+        check_topk(m, q, w, topk, got)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [40]])
+@pytest.mark.parametrize("topk", [7, 512])
+def test_index_of_a_row_of_nan_stays_in_bounds(new, topk):
+    """A row whose weights are NaN selects topk different pools that it may see, ascending; the rows beside it are as ever."""
+    m = Model(new, [9000 + 4 * j for j in range(len(new))], 64, seed=20, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 4)
+    bad = w.clone()
+    bad[1] = math.nan
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), bad.to(DEV), topk).cpu()
+    dsa.dsa_sync_status()
+    (_, _, i), = [x for x in m.rows() if x[0] == 1]
+    row = got[1].long()
+    assert row[0] >= 0 and row[-1] < i // 4 and torch.all(row[1:] > row[:-1])
+    good = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk).cpu()
+    got[1] = good[1]
+    assert torch.equal(got, good)
+
+
 @pytest.mark.parametrize("case", ["zeros", "two_values", "one_high", "negative", "few_values"])
 @pytest.mark.parametrize("topk", [1, 300, 512])
 def test_index_ties_of_many_rows(case, topk):
