@@ -1220,17 +1220,25 @@ constexpr int64_t kIntMax = 0x7FFFFFFFLL;
 constexpr int64_t kPagedScratch = int64_t{1} << 28;  // scores of a pass in the recommended workspace (1 GiB)
 constexpr int64_t kPagedPassMax = int64_t{1} << 31;  // scores of a pass however large the workspace
 constexpr int kPagedMinRows = 8;
-// Rows from which a sequence's scores are taken on tcgen05: its 128-row tiles
-// cost the same however few rows they hold, the mma.sync kernel grows with
-// every 8.  Measured at 32 heads, mma.sync / tcgen05: one sequence of 131072
-// tokens 31 / 33 us at 16 rows and 36 / 33 at 24; 16 sequences of 32768 tokens
-// 76 / 102 and 105 / 102; 64 of 8192 76 / 104 and 107 / 105.  Each sequence goes
-// by its own rows, which the device knows: both kernels are launched, each for
-// its own, unless the host can tell that one of them has none.  A chunk of 2048
-// rows at 131072 tokens among 63 single tokens takes 502 us; by the average, on
-// one kernel, it took 1045 (and one of 512 rows 99 against 327); a launch
-// without work of its own costs 2.6 us (16 drafts of 7 tokens: 53.3 against 50.7).
-constexpr int kPagedTcRows = 24;
+// Three kernels make the scores; all give a sequence's rows the same work, with
+// different waste.  Measured at 32 heads where nothing else is said, the
+// score kernels alone, in us.
+//   paged_scores        mma.sync, a row at a time; reads nearest to the copy rate
+//   paged_scores_rows   tcgen05, pools x (row, head) pairs: 256 / Hi rows together
+//   paged_scores_tc     tcgen05, 128 rows x pools, a head at a time
+// paged_scores or paged_scores_rows, by the average: 64 sequences of 65536 tokens
+// with a row each 50 / 56 us; 64 of 32768 with 2 rows 45 / 35, with 7 rows 120 /
+// 43.  With more than 32 heads the first one's queries fill its registers: a row
+// each at 64 heads 77 / 57.
+// paged_scores_tc for a sequence whose own rows reach paged_tc_rows: both tcgen05
+// kernels run then, each for its own sequences, which the device knows, unless
+// the host can tell that one of them has none (a launch without work costs 2.6
+// us).  16 sequences of 32768 tokens, rows / tc: at 64 heads 96 rows 179 / 197 and
+// 128 rows 236 / 201; at 32 heads 96 rows 99 / 111; at 16 heads 64 rows 50 / 65; at
+// 8 heads 32 rows 37 / 40 and 48 rows 62 / 41; at 4 heads 16 rows 25 / 29 and 24
+// rows 31 / 29.  A chunk of 2048 rows at 131072 tokens among 63 single tokens takes
+// 505 us in all; by the batch's average, on one kernel, it took 1045.
+int paged_tc_rows(int Hi) { return Hi >= 24 ? 96 : Hi > 6 ? 4 * Hi : 24; }
 
 bool page_size_ok(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 int log2_of(int x) {
@@ -1331,10 +1339,11 @@ dsa_status_t check_ws(const char* fn, const void* workspace, size_t ws_bytes, si
   return DSA_OK;
 }
 
-// Tensor maps of the chunk scores: the queries [rows][Hi][64] and the pooled
+// Tensor maps of the tcgen05 scores: the queries [rows][Hi][64] and the pooled
 // keys [pages][pools per page][128].
 dsa_status_t paged_score_maps(const char* fn, const dsa::CacheView& c, const void* q_idx, int64_t rows, int Hi,
-                              CUtensorMap* q_map, CUtensorMap* k_map) {
+                              cuuint32_t box_heads, cuuint32_t box_rows, cuuint32_t box_pools, CUtensorMap* q_map,
+                              CUtensorMap* k_map) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return fail(DSA_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable from the driver", fn);
   const cuuint32_t per_page = 1u << (c.shift - 2);
@@ -1343,7 +1352,7 @@ dsa_status_t paged_score_maps(const char* fn, const dsa::CacheView& c, const voi
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kDi), static_cast<cuuint64_t>(Hi),
                                 static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kDi) * 2, static_cast<cuuint64_t>(Hi) * kDi * 2};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kDi), 1u, 128u};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kDi), box_heads, box_rows};
     const CUresult r = enc(q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q_idx), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1351,7 +1360,7 @@ dsa_status_t paged_score_maps(const char* fn, const dsa::CacheView& c, const voi
   }
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(2 * kDi), per_page, static_cast<cuuint64_t>(c.num_pages)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * kDi) * 2, static_cast<cuuint64_t>(c.khat_stride) * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kDi), per_page, 1u};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kDi), per_page < box_pools ? per_page : box_pools, 1u};
   const CUresult r = enc(k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.khat, dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1610,16 +1619,24 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
   dsa::call_param("topk", topk);
   dsa::call_param("rows_per_pass", pass);
   // (the others' rows taken off, one each: what the longest may have)
-  const bool tc = b.rows - b.batch + 1 >= kPagedTcRows && dsa::paged_scores_tc_fits(b);
+  const bool tc = b.rows - b.batch + 1 >= paged_tc_rows(Hi) && dsa::paged_scores_tc_fits(b);
   const bool few = !tc || b.batch > 1;
-  const int tc_rows = !tc ? INT32_MAX : few ? kPagedTcRows : 0;
-  dsa::call_variant(!few ? "tcgen05 scores of 128-row tiles, then a row's top-k per CTA"
-                    : !tc ? "mma.sync scores of a few rows a sequence, then a row's top-k per CTA"
-                          : "tcgen05 scores of sequences with many rows and mma.sync scores of those with few, then a "
-                            "row's top-k per CTA");
+  const int tc_rows = !tc ? INT32_MAX : few ? paged_tc_rows(Hi) : 0;  // from which a sequence goes to paged_scores_tc
+  const bool pairs = few && (b.rows >= 2 * static_cast<int64_t>(b.batch) || Hi > 32) && dsa::paged_scores_rows_fits(b);
+  dsa::call_variant(!few     ? "tcgen05 scores of 128-row tiles, then a row's top-k per CTA"
+                    : !tc    ? pairs ? "tcgen05 scores of a sequence's rows and heads together, then a row's top-k per CTA"
+                                     : "mma.sync scores of a few rows a sequence, then a row's top-k per CTA"
+                    : pairs  ? "tcgen05 scores, 128-row tiles or rows and heads together, then a row's top-k per CTA"
+                             : "tcgen05 scores of 128-row tiles and mma.sync scores, then a row's top-k per CTA");
   CUtensorMap q_map, k_map;
   if (tc) {
-    st = paged_score_maps(fn, c, q_idx, b.rows, Hi, &q_map, &k_map);
+    st = paged_score_maps(fn, c, q_idx, b.rows, Hi, 1u, 128u, 256u, &q_map, &k_map);
+    if (st != DSA_OK) return st;
+  }
+  CUtensorMap q2_map, k2_map;
+  if (pairs) {
+    st = paged_score_maps(fn, c, q_idx, b.rows, Hi, static_cast<cuuint32_t>(Hi),
+                          static_cast<cuuint32_t>(dsa::paged_scores_rows_group(Hi)), 128u, &q2_map, &k2_map);
     if (st != DSA_OK) return st;
   }
   float* scores = static_cast<float*>(workspace);
@@ -1631,7 +1648,11 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
       e = timed_launch("paged_scores_tc", ctx.stream, [&] {
         return dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, tc_rows, scores, tops, ld, ctx);
       });
-    if (e == cudaSuccess && few)
+    if (e == cudaSuccess && pairs)
+      e = timed_launch("paged_scores_rows", ctx.stream, [&] {
+        return dsa::launch_paged_scores_rows(q2_map, k2_map, c, b, w, Hi, r, n, tc_rows, scores, tops, ld, tc, ctx);
+      });
+    else if (e == cudaSuccess && few)
       e = timed_launch("paged_scores", ctx.stream, [&] {
         return dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, tc_rows, scores, tops, ld, tc, ctx);
       });

@@ -65,6 +65,68 @@ __device__ __forceinline__ int page_of(const BatchView& b, int num_pages, int s,
   return -1;
 }
 
+// Rows of sequence s within launch rows [row0, row1): first row and count.
+__device__ __forceinline__ int seq_rows(const BatchView& b, int s, int64_t row0, int64_t row1, int64_t* first) {
+  const int64_t c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1);
+  const int64_t lo = c0 > row0 ? c0 : row0, hi = c1 < row1 ? c1 : row1;
+  *first = lo;
+  return hi > lo ? static_cast<int>(hi - lo) : 0;
+}
+
+// Pools that the last of rows [first, first + n) of sequence s may see; 0 for
+// lengths and offsets that contradict each other (the selection records them).
+__device__ __forceinline__ int64_t seq_pools(const BatchView& b, int shift, int s, int64_t first, int64_t n) {
+  const int64_t c1 = __ldg(b.cu + s + 1), len = __ldg(b.lens + s);
+  if (len > (static_cast<int64_t>(b.max_pages) << shift)) return 0;
+  const int64_t i = len - c1 + first + n - 1;
+  return i >= 4 ? i >> 2 : 0;
+}
+
+// A stretch of a CTA's walk over the scores: pools [p0, p1) of one sequence, a
+// tile of kRunTile at a time, against up to `group` of its rows.
+constexpr int kRunTile = 128;
+struct Run {
+  int64_t ra;            // first row
+  const int32_t* table;  // the sequence's pages
+  int nr;                // rows; 0: the walk has ended
+  int pools;             // pools that the last row may see
+  int p0, p1;            // multiples of kRunTile (p1 may lie past `pools`)
+};
+
+// Items of a walk are (sequence, group of rows, tile); off[s]: items before
+// sequence s.  The run that begins at item `*it` (or at the first one behind it
+// that has anything to score) and ends with its rows, or with the walk at it1;
+// moves *it past it.  *s is a cursor that only moves forward.
+static __device__ __noinline__ Run next_run(const BatchView& b, int shift, int group, const int* off, int64_t row0,
+                                            int64_t row1, int it1, int* it, int* s) {
+  Run x;
+  x.nr = 0;
+  while (*it < it1) {
+    while (*s + 1 < b.batch && *it >= off[*s + 1]) ++*s;
+    int64_t first;
+    const int n = seq_rows(b, *s, row0, row1, &first);
+    const int tiles = static_cast<int>((seq_pools(b, shift, *s, first, n) + kRunTile - 1) / kRunTile);
+    if (tiles == 0) {
+      ++*it;
+      continue;
+    }
+    const int rg = (*it - off[*s]) / tiles, tile = (*it - off[*s]) % tiles;
+    const int many = min(tiles - tile, it1 - *it);
+    *it += many;
+    x.ra = first + static_cast<int64_t>(rg) * group;
+    x.nr = static_cast<int>(min(static_cast<int64_t>(group), first + n - x.ra));
+    if (x.nr > 0) {
+      x.pools = static_cast<int>(seq_pools(b, shift, *s, x.ra, x.nr));
+      x.p0 = tile * kRunTile;
+      x.p1 = min((tile + many) * kRunTile, (x.pools + kRunTile - 1) / kRunTile * kRunTile);
+      x.table = b.table + *s * b.table_stride;
+      if (x.p0 < x.p1) return x;
+    }
+    x.nr = 0;
+  }
+  return x;
+}
+
 // New tokens of sequence s in the whole call.
 __device__ __forceinline__ int64_t call_rows(const BatchView& b, int s) {
   return static_cast<int64_t>(__ldg(b.cu + s + 1)) - __ldg(b.cu + s);

@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kDi = 64;
 
-// ================================================================= scores, few rows a sequence
+// ================================================================= scores, single tokens
 // Memory-bound: each pooled key is read once for up to kRows rows of its
 // sequence.  A warp takes 32 pools (four MMA n-tiles of 8).  The k order of a
 // dot product is free, so the MMA fragments are read straight from global
@@ -32,25 +32,9 @@ constexpr int kDi = 64;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32 * kWarps;  // pools of an item
+static_assert(kTile == kRunTile, "the walk's tiles");
 constexpr int kRows = 8;            // rows of an item
 constexpr int kMaxItems = 1 << 22;  // items of one sequence (a pass scores at most 2^31 pairs: fewer than half of it)
-
-// Rows of sequence s within launch rows [row0, row1): first row and count.
-__device__ __forceinline__ int seq_rows(const BatchView& b, int s, int64_t row0, int64_t row1, int64_t* first) {
-  const int64_t c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1);
-  const int64_t lo = c0 > row0 ? c0 : row0, hi = c1 < row1 ? c1 : row1;
-  *first = lo;
-  return hi > lo ? static_cast<int>(hi - lo) : 0;
-}
-
-// Pools that the last of rows [first, first + n) of sequence s may see; 0 for
-// lengths and offsets that contradict each other (the selection records them).
-__device__ __forceinline__ int64_t seq_pools(const BatchView& b, int shift, int s, int64_t first, int64_t n) {
-  const int64_t c1 = __ldg(b.cu + s + 1), len = __ldg(b.lens + s);
-  if (len > (static_cast<int64_t>(b.max_pages) << shift)) return 0;
-  const int64_t i = len - c1 + first + n - 1;
-  return i >= 4 ? i >> 2 : 0;
-}
 
 // Exclusive prefix of the sequences' item counts into off[0 .. batch] (shared
 // memory), by all kThreads threads.  The sums saturate, so that offsets which
@@ -86,49 +70,6 @@ __device__ __forceinline__ void item_prefix(int* off, int batch, F&& items_of) {
   }
   if (threadIdx.x == 0) off[batch] = s_base;
   __syncthreads();
-}
-
-// A stretch of a CTA's walk: pools [p0, p1) of one sequence, a tile of 128 at a
-// time, against up to kRows of its rows.
-struct Run {
-  int64_t ra;            // first row
-  const int32_t* table;  // the sequence's pages
-  int nr;                // rows; 0: the walk has ended
-  int pools;             // pools that the last row may see
-  int p0, p1;            // multiples of 128 (p1 may lie past `pools`)
-};
-
-// The run that begins at item `*it` (or at the first one behind it that has
-// anything to score) and ends with its rows, or with the walk at it1; moves
-// *it past it.  *s is a cursor that only moves forward.
-__device__ __noinline__ Run next_run(const BatchView& b, int shift, const int* off, int64_t row0, int64_t row1,
-                                     int it1, int* it, int* s) {
-  Run x;
-  x.nr = 0;
-  while (*it < it1) {
-    while (*s + 1 < b.batch && *it >= off[*s + 1]) ++*s;
-    int64_t first;
-    const int n = seq_rows(b, *s, row0, row1, &first);
-    const int tiles = static_cast<int>((seq_pools(b, shift, *s, first, n) + kTile - 1) / kTile);
-    if (tiles == 0) {
-      ++*it;
-      continue;
-    }
-    const int rg = (*it - off[*s]) / tiles, tile = (*it - off[*s]) % tiles;
-    const int many = min(tiles - tile, it1 - *it);
-    *it += many;
-    x.ra = first + static_cast<int64_t>(rg) * kRows;
-    x.nr = static_cast<int>(min(static_cast<int64_t>(kRows), first + n - x.ra));
-    if (x.nr > 0) {
-      x.pools = static_cast<int>(seq_pools(b, shift, *s, x.ra, x.nr));
-      x.p0 = tile * kTile;
-      x.p1 = min((tile + many) * kTile, (x.pools + kTile - 1) / kTile * kTile);
-      x.table = b.table + *s * b.table_stride;
-      if (x.p0 < x.p1) return x;
-    }
-    x.nr = 0;
-  }
-  return x;
 }
 
 template <int kMt>
@@ -188,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
   // The pooled keys of the next tile are fetched n-tile by n-tile into the
   // registers that the last row of this one has just used, so that the loads
   // of three n-tiles are always in flight behind the products of the fourth.
-  Run cur = next_run(b, c.shift, off, row0, row1, it1, &it, &s);
+  Run cur = next_run(b, c.shift, kRows, off, row0, row1, it1, &it, &s);
   if (cur.nr == 0) return;
   int p = cur.p0 + warp * 32;  // the warp's first pool
 #pragma unroll
@@ -197,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
     Run nxt = cur;
     int pn = p + kTile;
     if (pn >= cur.p1) {
-      nxt = next_run(b, c.shift, off, row0, row1, it1, &it, &s);
+      nxt = next_run(b, c.shift, kRows, off, row0, row1, it1, &it, &s);
       pn = nxt.p0 + warp * 32;
     }
     const uint4* ahead[4];

@@ -78,33 +78,18 @@ struct TcItem {
   int64_t pools;   // pools that the last row may see
 };
 
-__device__ __forceinline__ int seq_rows(const TcArgs& a, int s, int64_t* first) {
-  const int64_t c0 = __ldg(a.b.cu + s), c1 = __ldg(a.b.cu + s + 1);
-  const int64_t lo = c0 > a.row0 ? c0 : a.row0, hi = c1 < a.row1 ? c1 : a.row1;
-  *first = lo;
-  return hi > lo ? static_cast<int>(hi - lo) : 0;
-}
-// pools that the last of rows [first, first + n) may see; 0 for lengths and
-// offsets that contradict each other (the selection records them)
-__device__ __forceinline__ int64_t seq_pools(const TcArgs& a, int s, int64_t first, int64_t n) {
-  const int64_t c1 = __ldg(a.b.cu + s + 1), len = __ldg(a.b.lens + s);
-  if (len > (static_cast<int64_t>(a.b.max_pages) << a.c.shift)) return 0;
-  const int64_t i = len - c1 + first + n - 1;
-  return i >= 4 ? i >> 2 : 0;
-}
-
 // Item `it`; *s is a cursor that only moves forward.  False: nothing to score.
 __device__ __forceinline__ bool item_at(const TcArgs& a, const int* off, int it, int* s, TcItem* x) {
   while (*s + 1 < a.b.batch && it >= off[*s + 1]) ++*s;
   int64_t first;
-  const int n = seq_rows(a, *s, &first);
+  const int n = seq_rows(a.b, *s, a.row0, a.row1, &first);
   if (n == 0) return false;
   const int row_tiles = (n + kBM - 1) / kBM, local = it - off[*s];
   x->s = *s;
   x->ra = first + static_cast<int64_t>(local % row_tiles) * kBM;
   x->nr = static_cast<int>(min(static_cast<int64_t>(kBM), first + n - x->ra));
   x->p0 = static_cast<int64_t>(local / row_tiles) * kBN;
-  x->pools = seq_pools(a, *s, x->ra, x->nr);
+  x->pools = seq_pools(a.b, a.c.shift, *s, x->ra, x->nr);
   return x->nr > 0 && x->p0 < x->pools;
 }
 
@@ -152,9 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int v = 0;
       if (s < a.b.batch) {
         int64_t first;
-        const int n = seq_rows(a, s, &first);
+        const int n = seq_rows(a.b, s, a.row0, a.row1, &first);
         if (n > 0 && call_rows(a.b, s) >= a.tc_rows) {
-          const int64_t items = (seq_pools(a, s, first, n) + kBN - 1) / kBN * ((n + kBM - 1) / kBM);
+          const int64_t items = (seq_pools(a.b, a.c.shift, s, first, n) + kBN - 1) / kBN * ((n + kBM - 1) / kBM);
           v = static_cast<int>(min(items, static_cast<int64_t>(kMaxItems)));
         }
       }

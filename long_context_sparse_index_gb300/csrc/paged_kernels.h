@@ -94,6 +94,15 @@ bool paged_scores_tc_fits(const BatchView& b);
 cudaError_t launch_paged_scores_tc(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                    const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
                                    int tc_rows, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx);
+// The same on tcgen05 with (row, head) pairs as columns, for sequences with
+// fewer than tc_rows rows.  q_map: [64, Hi, rows], box {64, Hi, group}; k_map as
+// above, box {64, min(pools per page, 128), 1}.
+bool paged_scores_rows_fits(const BatchView& b);
+int paged_scores_rows_group(int Hi);  // rows of an item
+cudaError_t launch_paged_scores_rows(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
+                                     const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
+                                     int tc_rows, float* scores, float* tops, int64_t ld, bool early,
+                                     const LaunchCtx& ctx);
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,
                                 const float* tops, int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx);
 

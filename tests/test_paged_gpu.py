@@ -477,14 +477,19 @@ def test_index_long_bit_exact(new, old, page, Hi, topk):
     check_topk(m, q, w, topk, got)
 
 
+TC, PAIRS, MMA = "paged_scores_tc", "paged_scores_rows", "paged_scores"
+
+
 @pytest.mark.parametrize("new,kernels", [
-    ([1, 1, 200, 1, 0, 1], ["paged_scores_tc", "paged_scores"]),      # a chunk among single tokens
-    ([23, 24, 25, 1], ["paged_scores_tc", "paged_scores"]),           # on both sides of the rule
-    ([4, 6, 4, 5, 5, 6], ["paged_scores_tc", "paged_scores"]),        # one of them could be long; none is
-    ([30, 150], ["paged_scores_tc", "paged_scores"]),                 # all of them are
-    ([23], ["paged_scores"]), ([24], ["paged_scores_tc"]), ([24] + [0] * 30, ["paged_scores"])])
+    ([1, 1, 200, 1, 0, 1], [TC, PAIRS]),       # a chunk among single tokens
+    ([31, 32, 33, 1], [TC, PAIRS]),            # on both sides of the rule (8 heads: 32)
+    ([4, 6, 9, 5, 9, 6], [TC, PAIRS]),         # one of them could be long; none is
+    ([40, 150], [TC, PAIRS]),                  # all of them are
+    ([31], [PAIRS]), ([32], [TC]), ([2], [PAIRS]), ([1], [MMA]), ([1] * 9, [MMA]), ([5, 1, 2, 1], [PAIRS]),
+    ([3, 1, 1, 0, 0], [MMA]), ([40] + [0] * 30, [MMA]), ([70] + [0] * 30, [TC, PAIRS]),
+    ([100] + [1] * 60, [TC, PAIRS]), ([40] + [1] * 60, [TC, MMA])])
 def test_index_takes_each_sequence_by_its_own_rows(new, kernels):
-    m = Model(new, [2500 + 700 * j for j in range(len(new))], 64, seed=15, ints=True)
+    m = Model(new, [2500 + 700 * (j % 7) for j in range(len(new))], 64, seed=15, ints=True)
     cache, batch = m.to_gpu(dsa)
     q, w = index_inputs(m, 8, pad=0)
     got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 100)
@@ -553,8 +558,23 @@ def check_selected(m, q, w, topk, got):
         assert ((s + slack)[kept].min() >= (s - slack)[~kept].max()), (r, b, i)
 
 
-@pytest.mark.parametrize("page", [16, 128])
-@pytest.mark.parametrize("new,old", [([1, 2, 5], [3000, 701, 40]), ([130, 1, 27], [3001, 5000, 0])])
+@pytest.mark.parametrize("Hi", [1, 2, 3, 4, 5, 7, 8, 12, 15, 16, 17, 20, 24, 31, 32, 33, 48, 63, 64])
+@pytest.mark.parametrize("new,old,page", [([2, 7, 11], [1200, 37, 517], 32), ([21, 3], [2047, 5000], 256),
+                                          ([23], [1500], 1024)])
+def test_index_of_every_number_of_heads(Hi, new, old, page):
+    """Groups of 256 / Hi rows whose heads lie across the columns in every alignment."""
+    m = Model(new, old, page, seed=14, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, Hi)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 33)
+    assert any(k == PAIRS for k, _ in dsa.last_kernel_config()["kernels"])
+    dsa.dsa_sync_status()
+    check_topk(m, q, w, 33, got)
+
+
+@pytest.mark.parametrize("page", [16, 128, 1024])
+@pytest.mark.parametrize("new,old", [([1, 2, 1], [3000, 701, 40]), ([1, 2, 5], [3000, 701, 40]),
+                                     ([130, 1, 27], [3001, 5000, 0])])
 def test_index_reads_nothing_it_may_not_see(new, old, page):
     """NaN and infinities in every pooled key that no row may see: pools past a row's end, later pages, other pages."""
     m = Model(new, old, page, seed=16, ints=True)
@@ -573,7 +593,7 @@ def test_index_reads_nothing_it_may_not_see(new, old, page):
         check_topk(m, q, w, topk, got)
 
 
-@pytest.mark.parametrize("new", [[1, 1, 1], [40]])
+@pytest.mark.parametrize("new", [[1, 1, 1], [8], [40]])
 @pytest.mark.parametrize("topk", [7, 512])
 def test_index_of_a_row_of_nan_stays_in_bounds(new, topk):
     """A row whose weights are NaN selects topk different pools that it may see, ascending; the rows beside it are as ever."""
@@ -974,10 +994,11 @@ def test_page_operators_in_a_replayed_graph():
         check_moves(cache, before, moves + more)
 
 
-def test_chunk_scores_time_out_and_the_next_call_is_right():
+@pytest.mark.parametrize("rows", [200, 20])
+def test_tcgen05_scores_time_out_and_the_next_call_is_right(rows):
     """With fault injection the tcgen05 scores' producer issues no copies: every bounded wait runs out, the call
     reports DSA_ERR_TIMEOUT, and the context stays usable."""
-    m = Model([200], [3000], 64, seed=62, ints=True)
+    m = Model([rows], [3000], 64, seed=62, ints=True)
     cache, batch = m.to_gpu(dsa)
     q, w = index_inputs(m, 8)
     dsa.dsa_clear_status()
