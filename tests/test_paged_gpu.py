@@ -832,6 +832,42 @@ def test_what_is_out_of_range_is_reported_and_not_followed(what, rows):
         dsa.dsa_clear_status()
 
 
+@pytest.mark.parametrize("what", ["page", "page_high", "length", "offsets", "backwards", "past_the_rows"])
+@pytest.mark.parametrize("new,kernels", [([1, 1, 1, 1], [MMA]), ([5, 7, 3, 4], [PAIRS]), ([40, 50, 60, 33], [TC, PAIRS])])
+def test_index_out_of_range_on_every_kernel(what, new, kernels):
+    """As above for the three kernels of the scores, and offsets that run backwards or past the call's rows."""
+    old = [900, 1300, 700, 1111]
+    m, good = (Model(new, old, 32, seed=54, ints=True) for _ in range(2))
+    q, w = index_inputs(m, 8)
+    bad = 2
+    if what in ("page", "page_high"):
+        m.table[bad] = -1 if what == "page" else m.pages
+    elif what == "length":
+        m.lens[bad] = m.width * 32 + 1
+    elif what == "offsets":
+        m.lens[bad] = 0
+    elif what == "backwards":
+        m.cu[bad], m.cu[bad + 1] = m.cu[bad + 1], m.cu[bad]
+    else:
+        m.cu[-1] += 1 << 20
+    cache, batch = m.to_gpu(dsa)
+    got = torch.full((m.T, 20), -7, dtype=torch.int32, device=DEV)
+    dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 20, pool_idx=got)
+    assert [k for k, _ in dsa.last_kernel_config()["kernels"]] == kernels + ["paged_select"]
+    got = got.cpu()
+    if what != "backwards":  # (rows that another sequence then claims too may be anybody's, with or without a status)
+        with pytest.raises(dsa.DsaError) as e:
+            dsa.dsa_sync_status()
+        assert e.value.status == dsa.DSA_ERR_INTERNAL
+    dsa.dsa_clear_status()
+    assert torch.all((got >= -7) & (got < 1400))
+    scores, _ = good.scores(q, w)
+    hit = {"backwards": (1, 2, 3), "past_the_rows": (3,)}.get(what, (bad,))
+    for r, b, i in good.rows():
+        if b not in hit:
+            assert np.array_equal(got[r].numpy(), top_pools(scores[r], 20)), (r, b, i)
+
+
 # --------------------------------------------------------------------------- together
 
 def test_prompts_in_chunks_then_tokens_with_forks_and_compaction():
