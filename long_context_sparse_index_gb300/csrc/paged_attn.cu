@@ -21,9 +21,8 @@
 // Measured with 512 pools a row:
 //   1 row          7.8 us, latency: three dependent reads (selection, page,
 //                  key), the copies of five blocks at once, the merge.
-//   64 rows        13.4 us of which the gather takes 9: 68 MB from HBM at the
-//                  rate of the copy peak; 2 to 6 CTAs a row measured within 3 %
-//                  of each other, 7 and 8 a row (three CTAs an SM) 30 % slower.
+//   64 rows        12.0 us of which the gather takes 9: 68 MB from HBM at the
+//                  rate of the copy peak.
 //   4096 rows      284 us: 15.2 TB/s of keys and values from L2, 0.75 of the
 //                  1 KB-gather rate, and half of the issue slots: the chains of
 //                  12 warps an SM (168 registers) bound it.  Fewer instructions
@@ -420,63 +419,122 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
   }
 }
 
+template <int kStages>
+size_t smem_bytes(int blocks, int split) {
+  return 128 + static_cast<size_t>(kStages) * kStageBytes +
+         static_cast<size_t>((blocks + split - 1) / split) * kBlkKeys * sizeof(int32_t);
+}
+constexpr int row_blocks(int topk) { return (topk + 1 + kBlkPools - 1) / kBlkPools; }
+constexpr int kBlocksOf[2] = {row_blocks(512), row_blocks(2048)};  // the longest rows of two classes
+
 template <int kStages, bool kSplit, bool kFlat>
-cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
-                           float scale, void* o, float* lse, int split, const LaunchCtx& ctx) {
-  const int blocks = (topk + 1 + kBlkPools - 1) / kBlkPools;
-  const size_t fixed = 128 + static_cast<size_t>(kStages) * kStageBytes;
-  const size_t smem = fixed + static_cast<size_t>((blocks + split - 1) / split) * kBlkKeys * sizeof(int32_t);
-  constexpr int kMaxBlocks = (2048 + 1 + kBlkPools - 1) / kBlkPools;
+cudaError_t allow_smem() {
   // (a split of one never has the long ring)
   constexpr size_t kMost = 128 + static_cast<size_t>(kStages) * kStageBytes +
-                           static_cast<size_t>(kStages == 2 ? kMaxBlocks : (kMaxBlocks + 1) / 2) * kBlkKeys *
+                           static_cast<size_t>(kStages == 2 ? kBlocksOf[1] : (kBlocksOf[1] + 1) / 2) * kBlkKeys *
                                sizeof(int32_t);
   static_assert(kMost <= 232448 - 1024, "shared memory per CTA");
   static_assert(kWarps * kSlabBytes <= kStages * kStageBytes, "the merge slabs fit in the ring");
   static std::atomic<bool> attr_done[kAttrDevices];
-  cudaError_t e = set_smem_limit_once(paged_attn_kernel<kStages, kSplit, kFlat>, static_cast<int>(kMost), attr_done);
-  if (e != cudaSuccess) return e;
+  return set_smem_limit_once(paged_attn_kernel<kStages, kSplit, kFlat>, static_cast<int>(kMost), attr_done);
+}
+
+// A launch of clusters of `split` CTAs; attr has room for two.
+cudaLaunchConfig_t split_config(cudaLaunchAttribute* attr, int64_t rows, int split, size_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(b.rows * split));
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = ctx.stream;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cfg;
+}
+
+// How many rows' clusters of `split` CTAs the device holds at once, at the
+// longest rows of the class; asked for once per device, class and split.
+template <int kStages, bool kFlat>
+cudaError_t rows_at_once(int cls, int split, int* rows) {
+  static std::atomic<int> known[kAttrDevices][2][kMaxSplit + 1];  // plus one; 0: not asked for yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < kAttrDevices;
+  const int k = cached ? known[dev][cls][split].load(std::memory_order_relaxed) : 0;
+  if (k > 0) {
+    *rows = k - 1;
+    return cudaSuccess;
+  }
+  e = allow_smem<kStages, true, kFlat>();
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = kSplit ? attr : attr + 1;
-  cfg.numAttrs = kSplit ? 2 : 1;
+  cudaLaunchConfig_t cfg = split_config(attr, 1, split, smem_bytes<kStages>(kBlocksOf[cls], split), nullptr);
+  e = cudaOccupancyMaxActiveClusters(rows, paged_attn_kernel<kStages, true, kFlat>, &cfg);
+  if (e == cudaSuccess && cached) known[dev][cls][split].store(*rows + 1, std::memory_order_relaxed);
+  return e;
+}
+
+template <int kStages, bool kSplit, bool kFlat>
+cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
+                           float scale, void* o, float* lse, int split, const LaunchCtx& ctx) {
+  const cudaError_t e = allow_smem<kStages, kSplit, kFlat>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = split_config(attr, b.rows, split, smem_bytes<kStages>(row_blocks(topk), split), ctx.stream);
   return cudaLaunchKernelEx(&cfg, paged_attn_kernel<kStages, kSplit, kFlat>, c, b,
                             static_cast<const __nv_bfloat16*>(q), pool_idx, topk, scale * kLog2e,
                             static_cast<__nv_bfloat16*>(o), lse, split, ctx.status);
 }
 
-template <int kStages, bool kSplit>
-cudaError_t launch_layout(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
-                          float scale, void* o, float* lse, int split, const LaunchCtx& ctx) {
-  const int64_t page = static_cast<int64_t>(kD) << c.shift;
-  if (c.k_stride == page && c.v_stride == page)
-    return launch_variant<kStages, kSplit, true>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
-  return launch_variant<kStages, kSplit, false>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
+// The CTAs of a row: as many as let all rows run at once.  A cluster lies
+// within a part of the chip, so this is less than the CTAs that fit (16 rows of
+// 8 CTAs with the long ring take two turns, 13.8 us; of 6, 8.0), and the
+// runtime is asked.  With 5 CTAs or more a row the long ring, one CTA an SM, is
+// taken if it fits: it has all of a CTA's blocks under way at once (25 rows of 5:
+// 8.8 us, of 8 with two stages 9.1; 30 rows of 4 9.9 against 9.3).  Rows of up to
+// 6 blocks are not split: 5 blocks take 5.6 us with one CTA, 6.6 with two, 5.5
+// with five and up to 8.2 at 100 rows.  Otherwise, at 512 pools: 64 rows 22.4 us
+// with one CTA each, 14.4 / 14.1 / 12.3 / 12.0 with 2 / 3 / 4 / 6; 100 rows 31 / 21.5
+// / 18.5 / 17.0 with 1 to 4 and 24.7 with 5 (two turns); 200 rows 41.7 / 38.3.
+constexpr int kWhole = 6;
+constexpr int kRing = 5;
+
+template <bool kFlat>
+cudaError_t launch_rows(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
+                        float scale, void* o, float* lse, const LaunchCtx& ctx) {
+  const int blocks = row_blocks(topk), cls = blocks <= kBlocksOf[0] ? 0 : 1;
+  const int most = blocks <= kWhole ? 1 : blocks / 2 < kMaxSplit ? blocks / 2 : kMaxSplit;
+  // (three CTAs an SM at the most, so no more rows than this have two each)
+  if (most > 1 && b.rows <= 3 * static_cast<int64_t>(ctx.num_sms) / 2) {
+    int fit = 0;
+    for (int split = most; split >= (most < kRing ? most : kRing); --split) {
+      const cudaError_t e = rows_at_once<6, kFlat>(cls, split, &fit);
+      if (e != cudaSuccess) return e;
+      if (b.rows <= fit) return launch_variant<6, true, kFlat>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
+    }
+    for (int split = most; split > 1; --split) {
+      const cudaError_t e = rows_at_once<2, kFlat>(cls, split, &fit);
+      if (e != cudaSuccess) return e;
+      if (b.rows <= fit) return launch_variant<2, true, kFlat>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
+    }
+  }
+  return launch_variant<2, false, kFlat>(c, b, q, pool_idx, topk, scale, o, lse, 1, ctx);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn(const CacheView& c, const BatchView& b, const void* q, const int32_t* pool_idx, int topk,
                               float scale, void* o, float* lse, const LaunchCtx& ctx) {
-  // as many CTAs per row as give every SM two; with one CTA an SM or fewer, a
-  // ring that takes all of a CTA's blocks at once
-  const int64_t fit = 2 * static_cast<int64_t>(ctx.num_sms) / b.rows;
-  const int blocks = (topk + 1 + kBlkPools - 1) / kBlkPools;
-  int split = static_cast<int>(fit < 1 ? 1 : fit < kMaxSplit ? fit : kMaxSplit);
-  split = split < blocks ? split : blocks;
-  if (split == 1) return launch_layout<2, false>(c, b, q, pool_idx, topk, scale, o, lse, 1, ctx);
-  if (b.rows * split <= ctx.num_sms) return launch_layout<6, true>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
-  return launch_layout<2, true>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
+  const int64_t page = static_cast<int64_t>(kD) << c.shift;
+  if (c.k_stride == page && c.v_stride == page)
+    return launch_rows<true>(c, b, q, pool_idx, topk, scale, o, lse, ctx);
+  return launch_rows<false>(c, b, q, pool_idx, topk, scale, o, lse, ctx);
 }
 
 }  // namespace dsa

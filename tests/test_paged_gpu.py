@@ -727,8 +727,8 @@ def test_attention_small(layout, page, topk):
     check_attention(m, q, sel, 1 / math.sqrt(D), o, lse)
 
 
-@pytest.mark.parametrize("rows", [1, 2, 38, 39, 152, 153, 400])
-@pytest.mark.parametrize("topk", [512, 300])
+@pytest.mark.parametrize("rows", [1, 2, 14, 16, 25, 38, 39, 60, 76, 100, 128, 152, 153, 228, 229, 400])
+@pytest.mark.parametrize("topk", [512, 300, 96, 80])
 def test_attention_every_split(rows, topk):
     """Every number of CTAs per row; rows that keep fewer pools than the others leave CTAs without keys."""
     m = Model([1] * rows, [50 + 37 * j % 3000 for j in range(rows)], 64, seed=37)
@@ -741,7 +741,8 @@ def test_attention_every_split(rows, topk):
     check_attention(m, q, sel, 1 / math.sqrt(D), o, lse)
 
 
-@pytest.mark.parametrize("new,old,topk", [([1], [9000], 2048), ([3], [70000], 1000), ([200], [8200], 2048)])
+@pytest.mark.parametrize("new,old,topk", [([1], [9000], 2048), ([3], [70000], 1000), ([200], [8200], 2048),
+                                          ([19], [8300], 2048), ([60], [9000], 1500)])
 def test_attention_long(new, old, topk):
     m = Model(new, old, 128, seed=41, pages_apart=24)
     cache, batch = m.to_gpu(dsa)
