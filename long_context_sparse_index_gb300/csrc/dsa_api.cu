@@ -1230,15 +1230,23 @@ constexpr int kPagedMinRows = 8;
 // with a row each 50 / 56 us; 64 of 32768 with 2 rows 45 / 35, with 7 rows 120 /
 // 43.  With more than 32 heads the first one's queries fill its registers: a row
 // each at 64 heads 77 / 57.
-// paged_scores_tc for a sequence whose own rows reach paged_tc_rows: both tcgen05
-// kernels run then, each for its own sequences, which the device knows, unless
-// the host can tell that one of them has none (a launch without work costs 2.6
-// us).  16 sequences of 32768 tokens, rows / tc: at 64 heads 96 rows 179 / 197 and
-// 128 rows 236 / 201; at 32 heads 96 rows 99 / 111; at 16 heads 64 rows 50 / 65; at
-// 8 heads 32 rows 37 / 40 and 48 rows 62 / 41; at 4 heads 16 rows 25 / 29 and 24
-// rows 31 / 29.  A chunk of 2048 rows at 131072 tokens among 63 single tokens takes
-// 505 us in all; by the batch's average, on one kernel, it took 1045.
-int paged_tc_rows(int Hi) { return Hi >= 24 ? 96 : Hi > 6 ? 4 * Hi : 24; }
+// paged_scores_tc for a sequence whose own rows and tiles reach paged_tc_rule: both
+// tcgen05 kernels run then, each for its own sequences, which the device knows,
+// unless the host can tell that one of them has none (a launch without work costs
+// 2.6 us).  16 sequences of 32768 tokens, rows / tc: at 64 heads 96 rows 179 / 197
+// and 128 rows 236 / 201; at 32 heads 96 rows 99 / 111; at 16 heads 64 rows 50 / 65;
+// at 8 heads 32 rows 37 / 40 and 48 rows 62 / 41; at 4 heads 16 rows 25 / 29 and 24
+// rows 31 / 29.  With many heads a 128-row tile is long (27 us at 32), so a chunk of
+// few tiles leaves most of the SMs idle: 1000 rows at 8192 tokens (64 tiles) 26 / 35,
+// 256 rows at 32768 (64) 26 / 35, 2048 rows at 2048 (32) 21 / 34; 4096 rows at 8192
+// (256) 68 / 62, 1024 rows at 32768 (256) 65 / 62; at 64 heads 38 / 57, 37 / 56, 29 /
+// 56, 118 / 104 and 113 / 105; at 8 heads 25 / 19 for the first, and no such rule.
+// A chunk of 2048 rows at 131072 tokens among 63 single tokens takes 505 us in all;
+// by the batch's average, on one kernel, it took 1045.
+dsa::TcRule paged_tc_rule(int Hi) {
+  if (Hi >= 24) return {96, 100};
+  return {Hi > 6 ? 4 * Hi : 24, 0};
+}
 
 bool page_size_ok(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 int log2_of(int x) {
@@ -1619,9 +1627,13 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
   dsa::call_param("topk", topk);
   dsa::call_param("rows_per_pass", pass);
   // (the others' rows taken off, one each: what the longest may have)
-  const bool tc = b.rows - b.batch + 1 >= paged_tc_rows(Hi) && dsa::paged_scores_tc_fits(b);
-  const bool few = !tc || b.batch > 1;
-  const int tc_rows = !tc ? INT32_MAX : few ? paged_tc_rows(Hi) : 0;  // from which a sequence goes to paged_scores_tc
+  dsa::TcRule rule = paged_tc_rule(Hi);
+  const int64_t long_rows = b.rows - b.batch + 1;
+  const bool tc = long_rows >= rule.rows && (long_rows + 127) / 128 * ((ld + 255) / 256) >= rule.tiles &&
+                  dsa::paged_scores_tc_fits(b);
+  const bool few = !tc || b.batch > 1 || rule.tiles > 0;
+  if (!tc) rule = {INT32_MAX, 0};
+  if (!few) rule = {0, 0};
   const bool pairs = few && (b.rows >= 2 * static_cast<int64_t>(b.batch) || Hi > 32) && dsa::paged_scores_rows_fits(b);
   dsa::call_variant(!few     ? "tcgen05 scores of 128-row tiles, then a row's top-k per CTA"
                     : !tc    ? pairs ? "tcgen05 scores of a sequence's rows and heads together, then a row's top-k per CTA"
@@ -1646,15 +1658,15 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
     cudaError_t e = cudaSuccess;
     if (tc)
       e = timed_launch("paged_scores_tc", ctx.stream, [&] {
-        return dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, tc_rows, scores, tops, ld, ctx);
+        return dsa::launch_paged_scores_tc(q_map, k_map, c, b, w, Hi, r, n, rule, scores, tops, ld, ctx);
       });
     if (e == cudaSuccess && pairs)
       e = timed_launch("paged_scores_rows", ctx.stream, [&] {
-        return dsa::launch_paged_scores_rows(q2_map, k2_map, c, b, w, Hi, r, n, tc_rows, scores, tops, ld, tc, ctx);
+        return dsa::launch_paged_scores_rows(q2_map, k2_map, c, b, w, Hi, r, n, rule, scores, tops, ld, tc, ctx);
       });
     else if (e == cudaSuccess && few)
       e = timed_launch("paged_scores", ctx.stream, [&] {
-        return dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, tc_rows, scores, tops, ld, tc, ctx);
+        return dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, rule, scores, tops, ld, tc, ctx);
       });
     if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: scores launch");
     e = timed_launch("paged_select", ctx.stream, [&] {

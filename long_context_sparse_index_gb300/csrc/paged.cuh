@@ -127,9 +127,11 @@ static __device__ __noinline__ Run next_run(const BatchView& b, int shift, int g
   return x;
 }
 
-// New tokens of sequence s in the whole call.
-__device__ __forceinline__ int64_t call_rows(const BatchView& b, int s) {
-  return static_cast<int64_t>(__ldg(b.cu + s + 1)) - __ldg(b.cu + s);
+// Whether the 128-row tiles take sequence s: by its rows and pools in the whole
+// call, so that every kernel and pass of the call answers alike.
+__device__ __forceinline__ bool tc_takes(const BatchView& b, const TcRule& tc, int s) {
+  const int64_t rows = static_cast<int64_t>(__ldg(b.cu + s + 1)) - __ldg(b.cu + s), pools = __ldg(b.lens + s) >> 2;
+  return rows >= tc.rows && (rows + 127) / 128 * ((pools + 255) / 256) >= tc.tiles;
 }
 
 // ----------------------------------------------------------------- thread-block clusters

@@ -75,7 +75,7 @@ __device__ __forceinline__ void item_prefix(int* off, int batch, F&& items_of) {
 template <int kMt>
 __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
     paged_score_kernel(const CacheView c, const BatchView b, const __nv_bfloat16* __restrict__ q,
-                       const float* __restrict__ w, int Hi, int64_t row0, int64_t row1, int tc_rows,
+                       const float* __restrict__ w, int Hi, int64_t row0, int64_t row1, const TcRule tc,
                        float* __restrict__ scores, float* __restrict__ tops, int64_t ld, unsigned* status) {
   extern __shared__ int off[];
 
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
   item_prefix(off, b.batch, [&](int s) {
     int64_t first;
     const int n = seq_rows(b, s, row0, row1, &first);
-    if (n == 0 || call_rows(b, s) >= tc_rows) return 0;
+    if (n == 0 || tc_takes(b, tc, s)) return 0;
     const int64_t tiles = (seq_pools(b, c.shift, s, first, n) + kTile - 1) / kTile;
     const int64_t items = tiles * ((n + kRows - 1) / kRows);
     return static_cast<int>(items < kMaxItems ? items : kMaxItems);
@@ -642,12 +642,12 @@ __global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kThr == 256 ? 5 : 2)
 
 template <int kMt>
 cudaError_t launch_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                          int64_t row0, int64_t nrows, int tc_rows, float* scores, float* tops, int64_t ld,
+                          int64_t row0, int64_t nrows, TcRule tc, float* scores, float* tops, int64_t ld,
                           const LaunchCtx& ctx) {
   const size_t smem = static_cast<size_t>(b.batch + 1) * sizeof(int);
   const int grid = ctx.num_sms * (kMt <= 2 ? 3 : 2);
   return launch_ex(ctx, paged_score_kernel<kMt>, dim3(grid), dim3(kThreads), smem, c, b,
-                   static_cast<const __nv_bfloat16*>(q_idx), w, Hi, row0, row0 + nrows, tc_rows, scores, tops, ld,
+                   static_cast<const __nv_bfloat16*>(q_idx), w, Hi, row0, row0 + nrows, tc, scores, tops, ld,
                    ctx.status);
 }
 
@@ -672,13 +672,13 @@ cudaError_t launch_select(const BatchView& b, int shift, int64_t row0, int64_t n
 }  // namespace
 
 cudaError_t launch_paged_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                                int64_t row0, int64_t nrows, int tc_rows, float* scores, float* tops, int64_t ld,
+                                int64_t row0, int64_t nrows, TcRule tc, float* scores, float* tops, int64_t ld,
                                 bool early, const LaunchCtx& call) {
   LaunchCtx ctx = call;
   ctx.pdl = early;
-  if (Hi <= 16) return launch_scores<1>(c, b, q_idx, w, Hi, row0, nrows, tc_rows, scores, tops, ld, ctx);
-  if (Hi <= 32) return launch_scores<2>(c, b, q_idx, w, Hi, row0, nrows, tc_rows, scores, tops, ld, ctx);
-  return launch_scores<4>(c, b, q_idx, w, Hi, row0, nrows, tc_rows, scores, tops, ld, ctx);
+  if (Hi <= 16) return launch_scores<1>(c, b, q_idx, w, Hi, row0, nrows, tc, scores, tops, ld, ctx);
+  if (Hi <= 32) return launch_scores<2>(c, b, q_idx, w, Hi, row0, nrows, tc, scores, tops, ld, ctx);
+  return launch_scores<4>(c, b, q_idx, w, Hi, row0, nrows, tc, scores, tops, ld, ctx);
 }
 
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,

@@ -14,12 +14,14 @@
 // Every persistent CTA takes an equal, contiguous stretch of all tiles.
 //
 // Measured at 32 heads: 64 sequences of 32768 tokens (134 MB) in 35 us with 2
-// rows each, 43 with 7; 16 of them in 16 and 19 us.  The mma.sync kernel, which
+// rows each, 40 with 7; 16 of them in 16 and 18 us.  The mma.sync kernel, which
 // goes row by row and leaves the heads' sum to shuffles, takes 45, 120, 20 and 42.
-// Bound by latency up to a few tiles a CTA, then by the reads (4.8 TB/s), and with
-// all 256 columns in use by the epilogue's 28 thousand values a tile: with 8
-// epilogue warps 7 rows took 53 us.  One TMA warp issued a box every 25 ns, so that
-// pages of 16 tokens (64 boxes a tile) took 77 us; four warps take 44.
+// Bound by latency up to a few tiles a CTA, then by the reads (537 MB in 97 us,
+// 5.5 TB/s), and with all 256 columns in use by the epilogue's 32 thousand values a
+// tile: 8 epilogue warps took 53 us for 7 rows, 16 that go row by row 45.  One TMA
+// warp issued a box every 25 ns, so that pages of 16 tokens (64 boxes a tile) took
+// 77 us; three warps take 45, and leave the epilogue its 94 registers (with four
+// it had 80 and took 2 to 4 us more).  Five stages were no faster than four.
 #include "paged.cuh"
 
 namespace dsa {
@@ -35,7 +37,7 @@ constexpr uint32_t kABytes = 2 * kHalf;
 constexpr uint32_t kBBytes = kBN * kDi * 2;   // 32 KB: queries of a run; two buffers
 constexpr int kEpiSubs = 4;                   // warps that share a lane quarter's rows
 constexpr int kEpiWarps = 4 * kEpiSubs;
-constexpr int kTmaWarps = 4;                  // the pages of a tile are shared out over them
+constexpr int kTmaWarps = 3;                  // the pages of a tile are shared out over them
 constexpr int kMmaWarp = kTmaWarps;
 constexpr int kEpiWarp0 = kTmaWarps + 1;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
@@ -59,7 +61,7 @@ struct RowsArgs {
   int Hi;
   int group;  // rows of an item
   int64_t row0, row1;
-  int tc_rows;  // sequences of at least so many rows in the call are the other kernel's
+  TcRule tc;
   float* scores;
   float* tops;
   int64_t ld;
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s < a.b.batch) {
         int64_t first;
         const int n = seq_rows(a.b, s, a.row0, a.row1, &first);
-        if (n > 0 && call_rows(a.b, s) < a.tc_rows) {
+        if (n > 0 && !tc_takes(a.b, a.tc, s)) {
           const int64_t items = (seq_pools(a.b, a.c.shift, s, first, n) + kBM - 1) / kBM * ((n + a.group - 1) / a.group);
           v = static_cast<int>(min(items, static_cast<int64_t>(kMaxItems)));
         }
@@ -282,10 +284,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ew = warp - kEpiWarp0, lq = warp & 3, sub = ew >> 2;
     float* wt = reinterpret_cast<float*>(gbase + kWOff) + ew * kBN;
     const uint32_t tlane = tmem + (static_cast<uint32_t>(lq * 32) << 16);
+    const int ld = static_cast<int>(a.ld);
+    // 16 heads of a row, added to acc
+    auto fold = [](float2& acc, const uint32_t (&v)[16], const float* wc) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 w4 = *reinterpret_cast<const float4*>(wc + 4 * j);
+        acc = __ffma2_rn(make_float2(w4.x, w4.y), make_float2(fmaxf(__uint_as_float(v[4 * j]), 0.f),
+                                                              fmaxf(__uint_as_float(v[4 * j + 1]), 0.f)), acc);
+        acc = __ffma2_rn(make_float2(w4.z, w4.w), make_float2(fmaxf(__uint_as_float(v[4 * j + 2]), 0.f),
+                                                              fmaxf(__uint_as_float(v[4 * j + 3]), 0.f)), acc);
+      }
+    };
     for (Run x = next_run(a.b, a.c.shift, a.group, off, a.row0, a.row1, it1, &it, &s); x.nr > 0 && ok; x = next_run(a.b, a.c.shift, a.group, off, a.row0, a.row1, it1, &it, &s)) {
       __syncwarp();
       for (int j = lane; j < kBN; j += 32) wt[j] = j < x.nr * a.Hi ? __ldg(a.w + x.ra * a.Hi + j) : 0.f;
       __syncwarp();
+      const int64_t first = (x.ra - a.row0) * a.ld + lq * 32 + lane;  // (a multiple of 8 but for the lane)
+      float* out = a.scores + first;
+      float* otop = a.tops + (first >> 3);
       for (int p = x.p0; p < x.p1; p += kBM) {
         // (the loads below are the whole warp's: its lanes agree)
         if (!__all_sync(0xffffffffu, mbar_wait(bar_acc_full + 8 * cs, cph, a.limit_ns, abort_flag))) {
@@ -293,61 +310,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const int at = p + lq * 32 + lane;
-        for (int r = sub; r < x.nr; r += kEpiSubs) {
-          float2 acc = make_float2(0.f, 0.f);
-          auto fold = [&](const uint32_t (&v)[16], int col) {  // 16 heads of this row
+        const uint32_t from = tlane + cs * kBN;
+        const bool in = p + lq * 32 + lane < x.pools;
+        int r = sub;
+        // two rows at a time, so that each one's reads and shuffles hide behind the other's
+        for (; r + kEpiSubs < x.nr && (a.Hi & 15) == 0; r += 2 * kEpiSubs) {
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          int col = r * a.Hi;
+          const int apart = kEpiSubs * a.Hi;
+          for (const int end = col + a.Hi; col < end; col += 16) {
+            uint32_t v[2][16];
+            tmem_ld16(from + col, v[0]);
+            tmem_ld16(from + col + apart, v[1]);
+            tmem_ld_wait();
+            fold(acc[0], v[0], wt + col);
+            fold(acc[1], v[1], wt + col + apart);
+          }
+          float sum[2], top[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 w4 = *reinterpret_cast<const float4*>(wt + col + 4 * j);
-              acc = __ffma2_rn(make_float2(w4.x, w4.y), make_float2(fmaxf(__uint_as_float(v[4 * j]), 0.f),
-                                                                    fmaxf(__uint_as_float(v[4 * j + 1]), 0.f)), acc);
-              acc = __ffma2_rn(make_float2(w4.z, w4.w), make_float2(fmaxf(__uint_as_float(v[4 * j + 2]), 0.f),
-                                                                    fmaxf(__uint_as_float(v[4 * j + 3]), 0.f)), acc);
-            }
-          };
-          int h0 = 0;
-          if ((a.Hi & 3) == 0) {
-            for (; h0 + 32 <= a.Hi; h0 += 32) {
-              const int col = r * a.Hi + h0;
-              uint32_t v[16], u[16];
-              tmem_ld16(tlane + cs * kBN + col, v);
-              tmem_ld16(tlane + cs * kBN + col + 16, u);
-              tmem_ld_wait();
-              fold(v, col);
-              fold(u, col + 16);
-            }
-            if (h0 + 16 <= a.Hi) {
-              const int col = r * a.Hi + h0;
-              uint32_t v[16];
-              tmem_ld16(tlane + cs * kBN + col, v);
-              tmem_ld_wait();
-              fold(v, col);
-              h0 += 16;
+          for (int e = 0; e < 2; ++e) {
+            sum[e] = acc[e].x + acc[e].y;
+            top[e] = in ? sum[e] : -INFINITY;
+          }
+          // the largest of each eight pools
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int64_t to = static_cast<int64_t>(r + e * kEpiSubs) * ld + p;
+              out[to] = sum[e];
+              if ((lane & 7) == 0) otop[to >> 3] = top[e];
             }
           }
-          for (; h0 < a.Hi; h0 += 16) {
-            const int col = r * a.Hi + h0, from = min(col, kBN - 16);  // (never past the accumulator)
+        }
+        for (; r < x.nr; r += kEpiSubs) {
+          float2 acc = make_float2(0.f, 0.f);
+          int h0 = 0;
+          for (; h0 + 16 <= a.Hi && (a.Hi & 3) == 0; h0 += 16) {
+            const int col = r * a.Hi + h0;
             uint32_t v[16];
-            tmem_ld16(tlane + cs * kBN + from, v);
+            tmem_ld16(from + col, v);
+            tmem_ld_wait();
+            fold(acc, v, wt + col);
+          }
+          for (; h0 < a.Hi; h0 += 16) {
+            const int col = r * a.Hi + h0, c0 = min(col, kBN - 16);  // (never past the accumulator)
+            uint32_t v[16];
+            tmem_ld16(from + c0, v);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int c = from + j;  // this row's heads from h0 on lie in columns col ..; the others are another row's
+              const int c = c0 + j;  // this row's heads from h0 on lie in columns col ..; the others are another row's
               if (c >= col && c < (r + 1) * a.Hi) acc.x = fmaf(wt[c], fmaxf(__uint_as_float(v[j]), 0.f), acc.x);
             }
           }
           const float sum = acc.x + acc.y;
-          float top = -INFINITY;
-          const int64_t to = (x.ra - a.row0 + r) * a.ld + at;
-          if (at < x.pools) {
-            a.scores[to] = sum;
-            top = sum;
-          }
-          // the largest of each eight pools
+          float top = in ? sum : -INFINITY;
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if ((lane & 7) == 0 && at < x.pools) a.tops[to >> 3] = top;
+          if (in) {
+            const int64_t to = static_cast<int64_t>(r) * ld + p;
+            out[to] = sum;
+            if ((lane & 7) == 0) otop[to >> 3] = top;
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -374,13 +402,13 @@ int paged_scores_rows_group(int Hi) { return kBN / Hi < 32 ? kBN / Hi : 32; }
 
 cudaError_t launch_paged_scores_rows(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                      const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
-                                     int tc_rows, float* scores, float* tops, int64_t ld, bool early,
+                                     TcRule tc, float* scores, float* tops, int64_t ld, bool early,
                                      const LaunchCtx& call) {
   static std::atomic<bool> attr_done[kAttrDevices];
   const cudaError_t e =
       set_smem_limit_once(paged_score_rows_kernel, static_cast<int>(smem_bytes(kMaxBatchRows)), attr_done);
   if (e != cudaSuccess) return e;
-  const RowsArgs a{c, b, w, Hi, paged_scores_rows_group(Hi), row0, row0 + nrows, tc_rows, scores, tops, ld,
+  const RowsArgs a{c, b, w, Hi, paged_scores_rows_group(Hi), row0, row0 + nrows, tc, scores, tops, ld,
                    call.status, call.wait_limit_ns, call.inject_timeout};
   LaunchCtx ctx = call;
   ctx.pdl = early;

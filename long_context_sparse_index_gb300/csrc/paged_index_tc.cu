@@ -61,7 +61,7 @@ struct TcArgs {
   const float* w;
   int Hi;
   int64_t row0, row1;
-  int tc_rows;  // sequences of fewer rows in the call are the other kernel's
+  TcRule tc;
   float* scores;
   float* tops;
   int64_t ld;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s < a.b.batch) {
         int64_t first;
         const int n = seq_rows(a.b, s, a.row0, a.row1, &first);
-        if (n > 0 && call_rows(a.b, s) >= a.tc_rows) {
+        if (n > 0 && tc_takes(a.b, a.tc, s)) {
           const int64_t items = (seq_pools(a.b, a.c.shift, s, first, n) + kBN - 1) / kBN * ((n + kBM - 1) / kBM);
           v = static_cast<int>(min(items, static_cast<int64_t>(kMaxItems)));
         }
@@ -386,12 +386,12 @@ bool paged_scores_tc_fits(const BatchView& b) { return b.batch <= kMaxBatchTc; }
 
 cudaError_t launch_paged_scores_tc(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                    const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
-                                   int tc_rows, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx) {
+                                   TcRule tc, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx) {
   static std::atomic<bool> attr_done[kAttrDevices];
   const cudaError_t e =
       set_smem_limit_once(paged_score_tc_kernel, static_cast<int>(smem_bytes(kMaxBatchTc)), attr_done);
   if (e != cudaSuccess) return e;
-  const TcArgs a{c, b, w, Hi, row0, row0 + nrows, tc_rows, scores, tops, ld, ctx.status, ctx.wait_limit_ns, ctx.inject_timeout};
+  const TcArgs a{c, b, w, Hi, row0, row0 + nrows, tc, scores, tops, ld, ctx.status, ctx.wait_limit_ns, ctx.inject_timeout};
   paged_score_tc_kernel<<<ctx.num_sms, kThreads, smem_bytes(b.batch), ctx.stream>>>(q_map, k_map, a);
   return cudaGetLastError();
 }

@@ -78,30 +78,36 @@ cudaError_t launch_compact_plan(const PageTableView& t, int num_pages, int32_t* 
 cudaError_t launch_compact_apply(const CacheSet& set, bool first, const PageTableView& t, int32_t* ws,
                                  const LaunchCtx& ctx);
 
+// Which sequences' scores the kernel of 128-row tiles makes: those of at least
+// so many rows and so many tiles (128 rows x 256 pools) in the call.
+struct TcRule {
+  int rows, tiles;
+};
+
 // Indexer over the pages: scores of launch rows [row0, row0 + nrows) into
 // scores [nrows][ld] (pool p of a row's sequence in column p) and the largest
 // of each eight pools into tops [nrows][ld / 8], then each row's top-k.  ld is
-// a multiple of 32.  Only sequences with fewer than tc_rows rows in the call;
-// early: launched early behind the tcgen05 scores of the others.
+// a multiple of 32.  Only the sequences that the rule leaves; early: launched
+// early behind the tcgen05 scores of the others.
 cudaError_t launch_paged_scores(const CacheView& c, const BatchView& b, const void* q_idx, const float* w, int Hi,
-                                int64_t row0, int64_t nrows, int tc_rows, float* scores, float* tops, int64_t ld,
+                                int64_t row0, int64_t nrows, TcRule tc, float* scores, float* tops, int64_t ld,
                                 bool early, const LaunchCtx& ctx);
-// The same on tcgen05, 128 rows of a sequence at a time, for sequences with at
-// least tc_rows rows: chunks.  q_map: [64, Hi, rows], box {64, 1, 128}; k_map:
+// The same on tcgen05, 128 rows of a sequence at a time, for the sequences that
+// the rule names: chunks.  q_map: [64, Hi, rows], box {64, 1, 128}; k_map:
 // [128, pools per page, pages], box {64, pools per page, 1}; both swizzled by
 // 128 bytes.
 bool paged_scores_tc_fits(const BatchView& b);
 cudaError_t launch_paged_scores_tc(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                    const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
-                                   int tc_rows, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx);
-// The same on tcgen05 with (row, head) pairs as columns, for sequences with
-// fewer than tc_rows rows.  q_map: [64, Hi, rows], box {64, Hi, group}; k_map as
+                                   TcRule tc, float* scores, float* tops, int64_t ld, const LaunchCtx& ctx);
+// The same on tcgen05 with (row, head) pairs as columns, for the sequences that
+// the rule leaves.  q_map: [64, Hi, rows], box {64, Hi, group}; k_map as
 // above, box {64, min(pools per page, 128), 1}.
 bool paged_scores_rows_fits(const BatchView& b);
 int paged_scores_rows_group(int Hi);  // rows of an item
 cudaError_t launch_paged_scores_rows(const CUtensorMap& q_map, const CUtensorMap& k_map, const CacheView& c,
                                      const BatchView& b, const float* w, int Hi, int64_t row0, int64_t nrows,
-                                     int tc_rows, float* scores, float* tops, int64_t ld, bool early,
+                                     TcRule tc, float* scores, float* tops, int64_t ld, bool early,
                                      const LaunchCtx& ctx);
 cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int64_t nrows, const float* scores,
                                 const float* tops, int64_t ld, int topk, int32_t* pool_idx, const LaunchCtx& ctx);

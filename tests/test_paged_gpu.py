@@ -502,6 +502,20 @@ def test_index_takes_each_sequence_by_its_own_rows(new, kernels):
     assert torch.equal(got, small)
 
 
+@pytest.mark.parametrize("new,old,kernels", [
+    ([200, 1], [1000, 60000], [TC, PAIRS]),  # long enough by its rows, not by its tiles
+    ([200, 1], [52000, 10], [TC, PAIRS]),    # by both
+    ([200], [52000], [TC, PAIRS]), ([200], [20000], [PAIRS])])
+def test_index_takes_each_sequence_by_its_own_tiles(new, old, kernels):
+    m = Model(new, old, 64, seed=25, ints=True)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 24)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 40)
+    assert [k for k, _ in dsa.last_kernel_config()["kernels"]] == kernels + ["paged_select"]
+    dsa.dsa_sync_status()
+    check_topk(m, q, w, 40, got)
+
+
 @pytest.mark.parametrize("case", ["zeros", "two_values", "huge", "one_high", "overflow", "negative", "runs"])
 def test_index_ties_and_extreme_scores(case):
     """All scores equal; nearly all equal; magnitudes near the type's end; one score far above the rest (the bins of
