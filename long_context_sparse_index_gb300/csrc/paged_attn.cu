@@ -460,18 +460,15 @@ cudaLaunchConfig_t split_config(cudaLaunchAttribute* attr, int64_t rows, int spl
 // How many rows' clusters of `split` CTAs the device holds at once, at the
 // longest rows of the class; asked for once per device, class and split.
 template <int kStages, bool kFlat>
-cudaError_t rows_at_once(int cls, int split, int* rows) {
+cudaError_t rows_at_once(int dev, int cls, int split, int* rows) {
   static std::atomic<int> known[kAttrDevices][2][kMaxSplit + 1];  // plus one; 0: not asked for yet
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
   const bool cached = dev >= 0 && dev < kAttrDevices;
   const int k = cached ? known[dev][cls][split].load(std::memory_order_relaxed) : 0;
   if (k > 0) {
     *rows = k - 1;
     return cudaSuccess;
   }
-  e = allow_smem<kStages, true, kFlat>();
+  cudaError_t e = allow_smem<kStages, true, kFlat>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = split_config(attr, 1, split, smem_bytes<kStages>(kBlocksOf[cls], split), nullptr);
@@ -512,14 +509,16 @@ cudaError_t launch_rows(const CacheView& c, const BatchView& b, const void* q, c
   const int most = blocks <= kWhole ? 1 : blocks / 2 < kMaxSplit ? blocks / 2 : kMaxSplit;
   // (three CTAs an SM at the most, so no more rows than this have two each)
   if (most > 1 && b.rows <= 3 * static_cast<int64_t>(ctx.num_sms) / 2) {
-    int fit = 0;
+    int fit = 0, dev = 0;
+    const cudaError_t got = cudaGetDevice(&dev);
+    if (got != cudaSuccess) return got;
     for (int split = most; split >= (most < kRing ? most : kRing); --split) {
-      const cudaError_t e = rows_at_once<6, kFlat>(cls, split, &fit);
+      const cudaError_t e = rows_at_once<6, kFlat>(dev, cls, split, &fit);
       if (e != cudaSuccess) return e;
       if (b.rows <= fit) return launch_variant<6, true, kFlat>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
     }
     for (int split = most; split > 1; --split) {
-      const cudaError_t e = rows_at_once<2, kFlat>(cls, split, &fit);
+      const cudaError_t e = rows_at_once<2, kFlat>(dev, cls, split, &fit);
       if (e != cudaSuccess) return e;
       if (b.rows <= fit) return launch_variant<2, true, kFlat>(c, b, q, pool_idx, topk, scale, o, lse, split, ctx);
     }
