@@ -232,13 +232,15 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
 //      32-bit keys narrows it; the few left are ranked against each other.
 //   3. Scores above T set a bit each, those equal to T one in a second map; the
 //      set bits in order are the row, ascending, the first ties with them.
-// Latency bounds it: 10.6 us for one row or 64 of 32768 (1024 threads each), 77
-// us for 2048 rows (256 threads, five rows an SM at a time).  A threshold from a
-// sample and one pass over the row took 118 us for those; a warp per row 270.
+// Latency bounds it: 10.6 us for one row or 64 of 32768 (1024 threads each), 66
+// us for 2048 rows (256 threads, five rows an SM at a time; six, at 40 registers,
+// 80).  A threshold from a sample and one pass over the row took 118 us for those; a
+// warp per row 270.
 // Should the list run over (hundreds of ties or of neighbours alike), or the
 // maxima have no finite range, a long row goes the short rows' way: the same
 // result, more passes.
-constexpr int kBins = 2048;
+constexpr int kBinBits = 10;  // (11 took 80 us for the 2048 rows)
+constexpr int kBins = 1 << kBinBits;
 constexpr int kFew = 512;
 constexpr int kSelMaxWarps = 32;
 constexpr int kSegment = 1 << 17;  // pools whose bits are held at once (2 x 16 KB of bits)
@@ -313,6 +315,7 @@ __device__ __forceinline__ void sel_scan2(SelSmem& sm, uint32_t& v, uint32_t& u,
 template <int kThr>
 __device__ __forceinline__ void sel_find(SelSmem& sm, uint32_t need, int& turn) {
   constexpr int kPer = kBins / kThr;
+  static_assert(kPer * kThr == kBins, "a thread's bins");
   uint32_t cnt[kPer], sum = 0;  // bins in descending order: thread 0 has the highest
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -389,7 +392,7 @@ __device__ __forceinline__ void sel_kth(SelSmem& sm, uint32_t need, int cnt, con
     windowed = true;
     if (lo == hi) break;
     const int bits = 32 - __clz(hi - lo);
-    const int sh = bits > 11 ? bits - 11 : 0;
+    const int sh = bits > kBinBits ? bits - kBinBits : 0;
     for (int j = tid; j < cnt; j += kThr) {
       const uint32_t k = score_key(v[j]);
       if (k >= lo && k <= hi) atomicAdd(&sm.hist[(k - lo) >> sh], 1u);
@@ -437,7 +440,7 @@ __device__ __forceinline__ void sel_kth(SelSmem& sm, uint32_t need, int cnt, con
 }
 
 template <int kCap, int kThr>
-__global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kThr == 256 ? 5 : 2)
+__global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kThr == 256 ? 5 : kThr == 128 ? 10 : 2)
     paged_select_kernel(const BatchView b, int shift, int64_t row0, const float* __restrict__ scores, int64_t ld,
                         const float* __restrict__ tops, int topk, int words_room, int32_t* __restrict__ pool_idx,
                         unsigned* status) {
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kThr, kThr == 1024 ? 1 : kThr == 256 ? 5 : 2)
   bool listed = false;
   int m = n;  // scores that T is looked for in: the list's, or the row's
   Steps st{0.f, 0.f};
-  if (n > 8 * topk) {
+  if (kCap > 0 && n > 8 * topk) {
     const int groups = n >> 3;  // whole groups of eight; what is left of the row is listed in any case
     const float* trow = tops + ((lrow * ld) >> 3);
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
@@ -688,6 +691,12 @@ cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int
   // share an SM.  1024 / 256 threads at 131072 tokens, with 4 us of event
   // overhead: 14.4 / 17.4 us for 128 rows, 22.9 / 19.9 for 192, 31.7 / 22.7 for 384.
   const bool few = nrows <= ctx.num_sms;
+  // Short rows by the thousand: no list is ever made, and ten of 128 threads
+  // share an SM.  256 / 128 threads, 2048 pools: 4096 rows 51.5 / 38.2, 1000 rows 20.5
+  // / 16.6, 300 rows (one turn either way) 12.3 / 14.3; 4096 pools, 2000 rows 44.3 / 45.3.
+  const int64_t pools = static_cast<int64_t>(b.max_pages) << (shift - 2);
+  if (nrows > 5 * static_cast<int64_t>(ctx.num_sms) && pools <= 2048 && pools <= 8 * topk)
+    return launch_select<0, 128>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx);
   if (topk <= 512)
     return few ? launch_select<2048, 1024>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx)
                : launch_select<2048, 256>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx);

@@ -626,6 +626,18 @@ def test_index_of_a_row_of_nan_stays_in_bounds(new, topk):
     assert torch.equal(got, good)
 
 
+@pytest.mark.parametrize("ints", [True, False])
+@pytest.mark.parametrize("old,page,topk", [(600, 16, 64), (0, 64, 200), (1000, 32, 512)])
+def test_index_of_many_short_rows(ints, old, page, topk):
+    """More rows than the chip takes at once, in a table that is never wider than 8 * topk pools."""
+    m = Model([900], [old], page, seed=26, ints=ints)
+    cache, batch = m.to_gpu(dsa)
+    q, w = index_inputs(m, 4, ints=ints)
+    got = dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), topk)
+    dsa.dsa_sync_status()
+    (check_topk if ints else check_selected)(m, q, w, topk, got)
+
+
 @pytest.mark.parametrize("case", ["zeros", "two_values", "one_high", "negative", "few_values"])
 @pytest.mark.parametrize("topk", [1, 300, 512])
 def test_index_ties_of_many_rows(case, topk):
