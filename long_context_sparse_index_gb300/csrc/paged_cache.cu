@@ -189,7 +189,7 @@ struct PlanSmem {
   int warp[kPlanWarps];  // this CTA's warps' counts, then their exclusive prefix
   int total;             // read by the other CTAs
   int below;             // compaction: used pages below n_used, from the CTA that finds it (-1: not here)
-  int scan[kPlanWarps];
+  int64_t scan[kPlanWarps];
   int bad;
   int carry;
 };
@@ -205,20 +205,22 @@ __device__ __forceinline__ uint32_t plan_peer(const int* p, uint32_t u) {
   return kC > 1 ? cluster_ld_u32(cluster_map(smem_u32(p), u)) : static_cast<uint32_t>(*reinterpret_cast<const volatile int*>(p));
 }
 
-// Exclusive prefix of v over the block's threads; *total: the sum.  sm.scan is free again on return.
-__device__ __forceinline__ int block_excl(PlanSmem& sm, int v, int* total) {
+// Exclusive prefix of v over the block's threads; *total: the sum.  In 64 bits:
+// one request may be 2^27 pages, so those of a block pass 32.  sm.scan is free
+// again on return.
+__device__ __forceinline__ int64_t block_excl(PlanSmem& sm, int v, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  int64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) sm.scan[warp] = x;
   __syncthreads();
-  int before = 0, all = 0;
+  int64_t before = 0, all = 0;
   for (int w = 0; w < kPlanWarps; ++w) {
-    const int t = sm.scan[w];
+    const int64_t t = sm.scan[w];
     before += w < warp ? t : 0;
     all += t;
   }
@@ -319,8 +321,8 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
         }
       }
     }
-    int tile;
-    const int before = block_excl(sm, v, &tile);
+    int64_t tile;
+    const int64_t before = block_excl(sm, v, &tile);
     // (a request too large for the cache is refused below; its prefix is not used)
     if (rank == 0 && s < t.max_seqs) off[s] = static_cast<int32_t>(min(need + before, static_cast<int64_t>(num_pages)));
     need += tile;
@@ -404,13 +406,13 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
     const int j = j0 + static_cast<int>(threadIdx.x);
     int len = 0;
     if (j < n && static_cast<unsigned>(src[j]) < seqs) len = t.lens[src[j]];
-    int tile;
-    const int before = block_excl(sm, (len & ((1 << shift) - 1)) != 0, &tile);
+    int64_t tile;
+    const int64_t before = block_excl(sm, (len & ((1 << shift) - 1)) != 0, &tile);
     if (rank == 0 && j < n) {
       ws.len[j] = len;
-      ws.off[j] = need + before;
+      ws.off[j] = need + static_cast<int>(before);
     }
-    need += tile;
+    need += static_cast<int>(tile);
   }
   int used;
   const int before = plan_scan<kC>(sm, t.count, num_pages, rank, &used);

@@ -299,6 +299,24 @@ def test_reserve_of_many_sequences():
     p.check(t)
 
 
+def test_reserve_of_more_pages_than_32_bits_count():
+    """1024 sequences that each ask for 2^21 pages: 2^31 in one block's sum.  Nothing changes."""
+    seqs, width = 1025, 1 << 21
+    cache = random_cache(40, 16)
+    t = dsa.PageTable.empty(cache, seqs, width)
+    t.seq_lens[1024], t.block_table[1024, 0], t.page_count[7] = 16, 7, 1
+    add = torch.full((seqs,), 16 * width, dtype=torch.int32, device=DEV)
+    keep = [x.clone() for x in (t.seq_lens, t.page_count)]
+    for last, pages in ((0, 0), (16, 1), (-5, 0)):
+        add[1024] = last
+        assert dsa.dsa_cache_reserve(cache, t, add).item() == 39 - (1024 * width + pages)
+        dsa.dsa_sync_status()
+        assert torch.equal(t.seq_lens, keep[0]) and torch.equal(t.page_count, keep[1])
+    assert t.block_table[1024, 0].item() == 7
+    t.block_table[1024, 0] = -1
+    assert t.block_table.amax().item() == t.block_table.amin().item() == -1
+
+
 def check_moves(cache, before, moves):
     for b, w in zip(buffers(cache), before):
         for s, d in moves:
