@@ -377,7 +377,8 @@ typedef struct {
  * to the slots of their positions, and khat of every pool that they complete,
  * from its four indexer keys (older ones from the page).  Appending again at
  * earlier positions (a rejected draft) rewrites the slots and recomputes the
- * pools.  No two sequences of the batch may write the same page.
+ * pools.  No two sequences of the batch may write the same page.  With cu_q that
+ * descends, starts below 0 or ends past `rows`, nothing at all is written.
  */
 dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
                               int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,

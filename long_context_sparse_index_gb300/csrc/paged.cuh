@@ -46,8 +46,9 @@ __device__ __forceinline__ RowAt warp_locate(const BatchView& b, int shift, int6
       const int64_t n = __shfl_sync(0xffffffffu, len[u], src);
       x.seq = j0 + 32 * u + src;
       x.pos = n - last + row;
-      // the sequence must be as long as its new tokens, and its table as long as it
-      if (x.pos < row - first || n > (static_cast<int64_t>(b.max_pages) << shift)) {
+      // the sequence's rows must be the call's, the sequence as long as its new
+      // tokens, and its table as long as it
+      if (first < 0 || last > b.rows || x.pos < row - first || n > (static_cast<int64_t>(b.max_pages) << shift)) {
         x.pos = -1;
         if (lane == 0) record_status(status, kStatusInternal);
       }

@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int mine = lane >> 3;
   const int64_t row = r0 + mine;
   int page = -1, off = 0, older = 0;  // older: how many of the pool's tokens come before the call's rows
+  bool astray = false;                // offsets that descend or leave the call's rows
   for (int j0 = 0; j0 < b.batch; j0 += 32) {
     const int j = j0 + lane;
     int c0 = 0, c1 = 0, len = 0;
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
       c0 = __ldg(b.cu + j);
       c1 = __ldg(b.cu + j + 1);
       len = __ldg(b.lens + j);
+      astray |= c0 < 0 || c1 < c0 || c1 > b.rows;
     }
     int src = -1;
 #pragma unroll
@@ -65,6 +67,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
         older = static_cast<int>(before < 3 ? 3 - before : 0);
       }
     }
+  }
+  // With such offsets no row's position is sure, and what it would overwrite
+  // may be a live token: nothing is written.  (Every warp has seen them all.)
+  if (__any_sync(0xffffffffu, astray)) {
+    if (lane == 0) record_status(status, kStatusInternal);
+    return;
   }
   // keys and values: lanes 0..15 the key, 16..31 the value
   const int half = lane >> 4, ch = lane & 15;

@@ -913,6 +913,49 @@ def test_index_out_of_range_on_every_kernel(what, new, kernels):
             assert np.array_equal(got[r].numpy(), top_pools(scores[r], 20)), (r, b, i)
 
 
+@pytest.mark.parametrize("cu,first_bad", [([-3, 5, 8], (0, 5)), ([-3, -3, 8], (0, 8)), ([0, 5, 9], (5, 8)),
+                                          ([0, 5, 3], (8, 8)), ([0, -2, 8], (0, 8))])
+def test_offsets_that_leave_the_rows(cu, first_bad):
+    """Offsets below 0, past the call's rows, and backwards: the append writes nothing, the rows of such a sequence get
+    no selection and no output, and the status says so; the other sequence's rows are right."""
+    m, good = (Model([5, 3], [59, 41], 16, seed=55, ints=True) for _ in range(2))
+    m.cu, (lo, hi) = cu, first_bad
+    cache, batch = m.to_gpu(dsa)
+
+    def reported():
+        with pytest.raises(dsa.DsaError) as e:
+            dsa.dsa_sync_status()
+        assert e.value.status == dsa.DSA_ERR_INTERNAL
+        dsa.dsa_clear_status()
+
+    new = [m.fill(m.T, d).to(DEV) for d in (D, D, DI)]
+    assert new[0].shape[0] == 8
+    dsa.dsa_cache_append(cache, batch, *new)
+    reported()
+    check_cache(cache, m)
+    if cu == [0, 5, 3]:  # (rows 5..7 are then behind the last sequence)
+        return
+    q, w = index_inputs(m, 4)
+    sel = torch.full((8, 6), -7, dtype=torch.int32, device=DEV)
+    dsa.dsa_paged_index_topk(cache, batch, q.to(DEV), w.to(DEV), 6, pool_idx=sel)
+    reported()
+    assert torch.all(sel[lo:hi] == -1)
+    qa = m.fill(m.T, HQ, D)
+    o = torch.full((8, HQ, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((8, HQ), 5.0, device=DEV)
+    dsa.dsa_paged_sparse_attn_fwd(cache, batch, qa.to(DEV), sel, o=o, lse=lse)
+    reported()
+    assert torch.all(o[lo:hi] == 3.0) and torch.all(lse[lo:hi] == 5.0)
+    ok = [r for r in range(8) if not lo <= r < hi]
+    scores, _ = good.scores(q, w)
+    for r in ok:
+        assert np.array_equal(sel[r].cpu().numpy(), top_pools(scores[r], 6)), r
+    ro, rl, av, mag = good.attention(qa, sel.cpu(), 1 / math.sqrt(D))
+    bo, bl = attention_bounds(ro, av, rl, mag)
+    assert torch.all((o.cpu().double() - ro).abs()[ok] <= bo[ok])
+    assert torch.all((lse.cpu().double() - rl).abs()[ok] <= bl[ok])
+
+
 # --------------------------------------------------------------------------- together
 
 def test_prompts_in_chunks_then_tokens_with_forks_and_compaction():
