@@ -359,6 +359,7 @@ typedef struct {
  *                past a sequence's pages are -1 or anything
  *   seq_lens     int32 [max_seqs]  0: the row is free
  *   page_count   int32 [num_pages] how many sequences hold the page (0: free)
+ * max_seqs 1..2^27; pages as in dsa_paged_cache_t and dsa_paged_batch_t.
  */
 typedef struct {
   int32_t* block_table;

@@ -1216,6 +1216,7 @@ void dsa_launch_count_reset(void) { g_launches.store(0); }
 namespace {
 
 constexpr int kMaxPagedBatch = 8192;  // the sequences' work prefix lies in shared memory
+constexpr int kMaxTableSeqs = 1 << 27;  // the page operators count sequences in 32 bits, a block or more at a time
 constexpr int64_t kIntMax = 0x7FFFFFFFLL;
 constexpr int64_t kPagedScratch = int64_t{1} << 28;  // scores of a pass in the recommended workspace (1 GiB)
 constexpr int64_t kPagedPassMax = int64_t{1} << 31;  // scores of a pass however large the workspace
@@ -1313,7 +1314,8 @@ dsa_status_t table_view(const char* fn, const dsa_page_table_t* t, dsa::PageTabl
   if (t->num_pages < 1 || t->num_pages > kIntMax / t->page_size)
     return fail(DSA_ERR_INVALID_ARG, "%s: num_pages=%lld out of range (num_pages * page_size <= 2^31 - 1)", fn,
                 (long long)t->num_pages);
-  if (t->max_seqs < 1) return fail(DSA_ERR_INVALID_ARG, "%s: max_seqs=%d must be >= 1", fn, t->max_seqs);
+  if (t->max_seqs < 1 || t->max_seqs > kMaxTableSeqs)
+    return fail(DSA_ERR_INVALID_ARG, "%s: max_seqs=%d out of range (1..2^27)", fn, t->max_seqs);
   if (t->max_pages < 1 || t->max_pages > kIntMax / t->page_size)
     return fail(DSA_ERR_INVALID_ARG, "%s: max_pages=%d out of range (max_pages * page_size <= 2^31 - 1)", fn,
                 t->max_pages);
@@ -1442,7 +1444,7 @@ dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* caches, int layers, c
 }
 
 size_t dsa_cache_workspace(int64_t num_pages, int max_seqs, int64_t n) {
-  if (num_pages < 1 || num_pages > kIntMax || max_seqs < 1 || n < 0 || n > kIntMax) return 0;
+  if (num_pages < 1 || num_pages > kIntMax || max_seqs < 1 || max_seqs > kMaxTableSeqs || n < 0 || n > kIntMax) return 0;
   // the fork's list holds one page per child
   int64_t w = dsa::fork_ws_words(n, max_seqs);
   const int64_t r = dsa::reserve_ws_words(max_seqs, static_cast<int>(num_pages));

@@ -123,6 +123,19 @@ def test_page_operators_are_checked(lib):
         assert lib.dsa_cache_reserve(t, FAKE, FAKE, FAKE, BIG, None) == status, kw
 
 
+def test_tables_of_more_rows_than_the_kernels_count_are_refused(lib):
+    """The planners walk the sequences in 32-bit steps of a block or more: 2^31 - 1 rows would pass the end."""
+    size = lib.dsa_cache_workspace(10, 2, 2)
+    for seqs in (0, -1, (1 << 27) + 1, 2 ** 31 - 1):
+        c, _, t = structs(max_seqs=seqs)
+        assert lib.dsa_cache_reserve(t, FAKE, FAKE, FAKE, 1 << 40, None) == INVALID, seqs
+        assert lib.dsa_cache_free(t, FAKE, 1, None) == INVALID, seqs
+        assert lib.dsa_cache_fork(c, 1, t, FAKE, FAKE, 1, FAKE, FAKE, 1 << 40, None) == INVALID, seqs
+        assert lib.dsa_cache_compact(c, 1, t, FAKE, FAKE, size, None) == INVALID, seqs
+        assert lib.dsa_cache_workspace(10, seqs, 0) == 0
+    assert lib.dsa_cache_workspace(10, 1 << 27, 0) == ((1 << 27) + 10) * 4 // 256 * 256 + 256
+
+
 def test_layers_are_checked(lib):
     from long_context_sparse_index_gb300 import _paged as p
     one, _, t = structs()
