@@ -380,10 +380,28 @@ typedef struct {
  * earlier positions (a rejected draft) rewrites the slots and recomputes the
  * pools.  No two sequences of the batch may write the same page.  With cu_q that
  * descends, starts below 0 or ends past `rows`, nothing at all is written.
+ *
+ * The rows of cu_q must be tokens that seq_lens counts, on pages that no other
+ * sequence holds.  After a dsa_cache_reserve that found too few pages they are
+ * not: the lengths are the old ones, the rows stand on the sequences' last live
+ * tokens, and an append would overwrite those (and a forked sibling's).  So do
+ * not append after a negative result; where the host cannot look at it in
+ * between (a captured step), append with dsa_cache_append_reserved.
  */
 dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
                               int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
                               int64_t k_idx_stride, void* stream);
+
+/*
+ * dsa_cache_append that looks, on the device, at the result word of the
+ * dsa_cache_reserve before it (device int32, 4-byte aligned; NULL: none): when
+ * it is negative, nothing is written and the status reports DSA_ERR_INTERNAL.
+ * (The indexer and the attention of such a step write nothing but their
+ * outputs, which are then of no use.)
+ */
+dsa_status_t dsa_cache_append_reserved(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                                       int64_t k_idx_stride, const int32_t* reserved, void* stream);
 
 /*
  * The operators on pages.  Where they move data they take the caches of all

@@ -32,7 +32,8 @@ EXPORTED = ("dsa_index_topk_workspace", "dsa_index_topk", "dsa_sparse_attn_fwd",
             "dsa_sparse_attn_bwd_deterministic_workspace", "dsa_sparse_attn_bwd_deterministic",
             "dsa_index_topk_stats", "dsa_measure_l2", "dsa_index_topk_workspace_slots", "dsa_trace_configure",
             "dsa_last_kernel_config", "dsa_sparse_attn_fwd_tc", "dsa_measure_umma",
-            "dsa_fwd_tc_profile", "dsa_measure_fold", "dsa_cache_append", "dsa_cache_copy_pages",
+            "dsa_fwd_tc_profile", "dsa_measure_fold", "dsa_cache_append", "dsa_cache_append_reserved",
+            "dsa_cache_copy_pages",
             "dsa_cache_workspace", "dsa_cache_reserve", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
             "dsa_paged_index_topk_workspace", "dsa_paged_index_topk", "dsa_paged_sparse_attn_fwd")
 

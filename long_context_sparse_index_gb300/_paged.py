@@ -204,6 +204,7 @@ class PageTable:
 def _configure_paged(lib):
     f32, sz, i64, i32, vp = ctypes.c_float, ctypes.c_size_t, _i64, _i32, _vp
     lib.dsa_cache_append.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.dsa_cache_append_reserved.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp, vp]
     lib.dsa_cache_copy_pages.argtypes = [vp, i32, vp, vp, i64, vp]
     lib.dsa_cache_workspace.argtypes = [i64, i32, i64]
     lib.dsa_cache_workspace.restype = sz
@@ -215,8 +216,9 @@ def _configure_paged(lib):
     lib.dsa_paged_index_topk_workspace.restype = sz
     lib.dsa_paged_index_topk.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, sz, vp]
     lib.dsa_paged_sparse_attn_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp]
-    for f in (lib.dsa_cache_append, lib.dsa_cache_copy_pages, lib.dsa_cache_reserve, lib.dsa_cache_fork,
-              lib.dsa_cache_free, lib.dsa_cache_compact, lib.dsa_paged_index_topk, lib.dsa_paged_sparse_attn_fwd):
+    for f in (lib.dsa_cache_append, lib.dsa_cache_append_reserved, lib.dsa_cache_copy_pages, lib.dsa_cache_reserve,
+              lib.dsa_cache_fork, lib.dsa_cache_free, lib.dsa_cache_compact, lib.dsa_paged_index_topk,
+              lib.dsa_paged_sparse_attn_fwd):
         f.restype = ctypes.c_int
 
 
@@ -249,10 +251,16 @@ def _ids(t, name: str, device: int) -> int:
     return t.shape[0]
 
 
-def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=None):
+def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=None, reserved=None):
     """Writes the new tokens' k, v [rows, 128] and k_idx [rows, 64] (bf16, rows
     any multiple of 8 elements apart) into their pages, and the pooled key of
-    every pool that they complete."""
+    every pool that they complete.
+
+    reserved: the word that dsa_cache_reserve returned for these tokens.  When
+    it is negative the sequences have their old lengths and the rows would
+    overwrite their last tokens; given it, the append then writes nothing and
+    dsa_sync_status reports DSA_ERR_INTERNAL.  Without it, look at the word
+    before appending."""
     dev = _device_of(cache, batch)
     ks = _rows_strided(k, "k", torch.bfloat16, 128, dev)
     vs = _rows_strided(v, "v", torch.bfloat16, 128, dev)
@@ -260,8 +268,13 @@ def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=N
     rows = k.shape[0]
     if v.shape[0] != rows or k_idx.shape[0] != rows:
         raise ValueError(f"k, v and k_idx must have the same rows (got {rows}, {v.shape[0]} and {k_idx.shape[0]})")
-    _check(load().dsa_cache_append(cache._ref, batch._with_rows(rows), k.data_ptr(), ks, v.data_ptr(), vs,
-                                   k_idx.data_ptr(), kis, _handle(stream, dev)))
+    args = (cache._ref, batch._with_rows(rows), k.data_ptr(), ks, v.data_ptr(), vs, k_idx.data_ptr(), kis)
+    if reserved is None:
+        _check(load().dsa_cache_append(*args, _handle(stream, dev)))
+        return
+    _full(reserved, "reserved", torch.int32, 1, dev)
+    _shape(reserved, "reserved", (1,))
+    _check(load().dsa_cache_append_reserved(*args, reserved.data_ptr(), _handle(stream, dev)))
 
 
 def _layers(cache):

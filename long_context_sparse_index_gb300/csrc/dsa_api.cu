@@ -1384,12 +1384,10 @@ int64_t paged_score_ld(int max_pages, int page_size) {
 }
 size_t paged_scratch_bytes(int64_t rows, int64_t ld) { return static_cast<size_t>(rows) * (ld + ld / 8) * 4; }
 
-}  // namespace
-
-dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
-                              int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
-                              int64_t k_idx_stride, void* stream) try {
-  const char* fn = "dsa_cache_append";
+// Both appends; `reserved` may be null.
+dsa_status_t append(const char* fn, const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx, int64_t k_idx_stride,
+                    const int32_t* reserved, void* stream) try {
   const dsa::CallScope scope(fn);
   dsa::CacheView c;
   dsa::BatchView b;
@@ -1402,6 +1400,7 @@ dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_ba
     return fail(DSA_ERR_INVALID_ARG, "%s: k, v and k_idx must be 16-byte aligned", fn);
   if (k_stride < kD || v_stride < kD || k_idx_stride < kDi || ((k_stride | v_stride | k_idx_stride) & 7) != 0)
     return fail(DSA_ERR_INVALID_ARG, "%s: row strides must be multiples of 8 elements, at least a row", fn);
+  if (!aligned4(reserved)) return fail(DSA_ERR_INVALID_ARG, "%s: reserved must be a 4-byte aligned device word", fn);
   dsa::LaunchCtx ctx;
   st = make_ctx(stream, &ctx);
   if (st != DSA_OK) return st;
@@ -1409,12 +1408,27 @@ dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_ba
   dsa::call_param("batch", b.batch);
   dsa::call_variant("a warp per four rows");
   const dsa::AppendArgs a{static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
-                          static_cast<const __nv_bfloat16*>(k_idx), k_stride, v_stride, k_idx_stride};
+                          static_cast<const __nv_bfloat16*>(k_idx), k_stride, v_stride, k_idx_stride, reserved};
   cudaError_t e = timed_launch("cache_append", ctx.stream, [&] { return dsa::launch_cache_append(c, b, a, ctx); });
-  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_append: launch");
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "%s: launch: %s", fn, cudaGetErrorString(e));
   return DSA_OK;
 } catch (...) {
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+}  // namespace
+
+dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                              int64_t k_idx_stride, void* stream) {
+  return append("dsa_cache_append", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, nullptr, stream);
+}
+
+dsa_status_t dsa_cache_append_reserved(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                                       int64_t k_idx_stride, const int32_t* reserved, void* stream) {
+  return append("dsa_cache_append_reserved", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, reserved,
+                stream);
 }
 
 dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* caches, int layers, const int32_t* src, const int32_t* dst,

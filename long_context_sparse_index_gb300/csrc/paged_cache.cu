@@ -38,7 +38,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int mine = lane >> 3;
   const int64_t row = r0 + mine;
   int page = -1, off = 0, older = 0;  // older: how many of the pool's tokens come before the call's rows
-  bool astray = false;                // offsets that descend or leave the call's rows
+  // offsets that descend or leave the call's rows, or a reservation that found too few pages
+  bool astray = a.reserved != nullptr && __ldg(a.reserved) < 0;
   for (int j0 = 0; j0 < b.batch; j0 += 32) {
     const int j = j0 + lane;
     int c0 = 0, c1 = 0, len = 0;
@@ -68,8 +69,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
       }
     }
   }
-  // With such offsets no row's position is sure, and what it would overwrite
-  // may be a live token: nothing is written.  (Every warp has seen them all.)
+  // Then no row's position is sure, and what it would overwrite may be a live
+  // token: nothing is written.  (Every warp has seen all offsets.)
   if (__any_sync(0xffffffffu, astray)) {
     if (lane == 0) record_status(status, kStatusInternal);
     return;

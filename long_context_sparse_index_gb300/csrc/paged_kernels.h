@@ -46,6 +46,7 @@ struct PageTableView {
 struct AppendArgs {
   const __nv_bfloat16 *k, *v, *k_idx;       // rows of the new tokens
   int64_t k_stride, v_stride, kidx_stride;  // elements from row to row
+  const int32_t* reserved;                  // a reservation's result, or null
 };
 
 // The layers of one launch that moves pages: their caches have the same pages

@@ -97,6 +97,15 @@ def test_append_arguments_are_checked(lib):
     assert append(lib, rows=0, nk=None, nv=None, nki=None) == OK
 
 
+def test_append_after_a_reservation_is_checked(lib):
+    def call(reserved, rows=4, **kw):
+        c, b, _ = structs(rows=rows, **kw)
+        return lib.dsa_cache_append_reserved(c, b, FAKE, 128, FAKE, 128, FAKE, 64, reserved, None)
+    assert call(FAKE + 2) == INVALID and b"dsa_cache_append_reserved: reserved" in lib.dsa_last_error()
+    assert call(FAKE, page=24) == UNSUPPORTED and call(None, k=None) == INVALID
+    assert call(FAKE, rows=0) == OK
+
+
 def test_page_operators_are_checked(lib):
     c, _, t = structs()
     size = lib.dsa_cache_workspace(10, 2, 2)

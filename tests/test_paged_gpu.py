@@ -1079,6 +1079,61 @@ def test_decoding_step_in_a_replayed_graph():
         m.lens = [n + 1 for n in m.lens]
 
 
+def test_a_step_that_found_too_few_pages_overwrites_nothing():
+    """reserve and append captured and replayed until the pages run out: the refused steps leave every live token (a
+    forked sibling's among them) as it was, and say so; with pages free again the next replay goes on."""
+    cache = random_cache(8, 16)
+    t = dsa.PageTable.empty(cache, max_seqs=3, max_pages=6)
+    cu = i32([0, 40, 40, 40])
+    new = [torch.randn(40, d, device=DEV).to(torch.bfloat16) for d in (D, D, DI)]
+    taken, add = i32([0]), i32([48, 0, 48])
+    assert dsa.dsa_cache_reserve(cache, t, add).item() == 6
+    dsa.dsa_cache_fork(cache, t, i32([0]), i32([1]))  # three full pages, shared
+    ws = torch.empty(dsa.cache_workspace_size(8, 3), dtype=torch.uint8, device=DEV)
+    cu.copy_(i32([0, 1, 2, 2]))
+    add.copy_(i32([1, 1, 0]))
+    batch = dsa.PagedBatch(t.block_table, t.seq_lens, cu)
+    k, v, ki = (x[:2] for x in new)
+
+    def step():
+        dsa.dsa_cache_reserve(cache, t, add, result=taken, workspace=ws)
+        dsa.dsa_cache_append(cache, batch, k, v, ki, reserved=taken)
+
+    step()  # warm-up: the last two pages
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(15):
+        g.replay()
+    dsa.dsa_sync_status()
+    assert taken.item() == 0 and t.seq_lens.tolist() == [64, 64, 48] and torch.all(t.page_count > 0)
+    keep = [x.clone() for x in buffers(cache) + [t.block_table, t.seq_lens, t.page_count]]
+    for add_now in ([1, 1, 0], [0, 0, 200]):  # no page left; more than a row of the table holds
+        add.copy_(i32(add_now))
+        cu.copy_(i32([0, 1, 2, 2] if add_now[0] else [0, 0, 0, 2]))
+        g.replay()
+        with pytest.raises(dsa.DsaError) as e:
+            dsa.dsa_sync_status()
+        assert e.value.status == dsa.DSA_ERR_INTERNAL
+        dsa.dsa_clear_status()
+        assert taken.item() == (-2 if add_now[0] else -2 ** 31)
+        for x, y in zip(buffers(cache) + [t.block_table, t.seq_lens, t.page_count], keep):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    dsa.dsa_cache_free(cache, t, i32([2]))
+    add.copy_(i32([1, 1, 0]))
+    cu.copy_(i32([0, 1, 2, 2]))
+    g.replay()
+    dsa.dsa_sync_status()
+    assert taken.item() == 2 and t.seq_lens.tolist() == [65, 65, 0]
+    for s_ in (0, 1):
+        page = t.block_table[s_, 4].item()
+        assert same_bits(cache.k[page, 0], k[s_]) and same_bits(cache.v[page, 0], v[s_])
+    for bad in (i32([0, 0]), torch.zeros(1, device=DEV), taken.cpu()):
+        with pytest.raises((TypeError, ValueError)):
+            dsa.dsa_cache_append(cache, batch, k, v, ki, reserved=bad)
+
+
 def test_page_operators_in_a_replayed_graph():
     """fork, reserve, free and compact captured once and replayed on changing tables."""
     p = Pages([40, 33, 0, 0, 0], 16, 30, 6, seed=12)
