@@ -86,6 +86,15 @@ __device__ __forceinline__ int64_t seq_pools(const BatchView& b, int shift, int 
 // A stretch of a CTA's walk over the scores: pools [p0, p1) of one sequence, a
 // tile of kRunTile at a time, against up to `group` of its rows.
 constexpr int kRunTile = 128;
+// Items of one sequence in a pass of the scores, and where the sum over the
+// sequences saturates.  A pass has up to eight rows of up to 2^29 pools, or more
+// rows with 2^31 scores in all; an item is four rows or more by 128 pools or
+// more.  So a sequence of eight rows has at most 2 * 2^22 items, one of n > 8
+// rows fewer than n / 3 * 2^24 / n, all of a pass together at most 2^25.  Only
+// offsets that contradict each other ask for more.  They are cut off, so that a
+// scan of 128 sequences on top of the saturated sum stays in 32 bits.
+constexpr int kMaxItems = 1 << 23;
+constexpr int kMaxTotal = 1 << 29;
 struct Run {
   int64_t ra;            // first row
   const int32_t* table;  // the sequence's pages

@@ -34,7 +34,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32 * kWarps;  // pools of an item
 static_assert(kTile == kRunTile, "the walk's tiles");
 constexpr int kRows = 8;            // rows of an item
-constexpr int kMaxItems = 1 << 22;  // items of one sequence (a pass scores at most 2^31 pairs: fewer than half of it)
 
 // Exclusive prefix of the sequences' item counts into off[0 .. batch] (shared
 // memory), by all kThreads threads.  The sums saturate, so that offsets which
@@ -65,7 +64,7 @@ __device__ __forceinline__ void item_prefix(int* off, int batch, F&& items_of) {
     }
     if (s < batch) off[s] = before + x - v;
     __syncthreads();
-    if (threadIdx.x == 0) s_base = min(s_base + all, 1 << 30);
+    if (threadIdx.x == 0) s_base = min(s_base + all, kMaxTotal);
     __syncthreads();
   }
   if (threadIdx.x == 0) off[batch] = s_base;

@@ -52,7 +52,6 @@ static_assert(smem_bytes(kMaxBatchRows) <= 232448, "shared memory per CTA");
 constexpr uint32_t kBarAFull = 0, kBarAEmpty = 32, kBarBFull = 64, kBarBEmpty = 80, kBarAccFull = 96, kBarAccEmpty = 112,
                    kBarDrain = 128, kTmemSlot = 136, kAbort = 140;
 static_assert(kStages * 8 <= 32, "the control block's barriers");
-constexpr int kMaxItems = 1 << 22;  // items of one sequence
 
 struct RowsArgs {
   CacheView c;
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= o) x += y;
       }
       if (s < a.b.batch) off[s] = sum + x - v;
-      sum = min(sum + __shfl_sync(0xffffffffu, x, 31), 1 << 30);
+      sum = min(sum + __shfl_sync(0xffffffffu, x, 31), kMaxTotal);
     }
     if (lane == 0) off[a.b.batch] = sum;
   }

@@ -53,7 +53,6 @@ static_assert(smem_bytes(kMaxBatchTc) <= 232448, "shared memory per CTA");
 // control block (bytes from kCtlOff)
 constexpr uint32_t kBarAFull = 0, kBarAEmpty = 32, kBarBFull = 64, kBarBEmpty = 72, kBarAccFull = 80, kBarAccEmpty = 96,
                    kBarDrain = 112, kTmemSlot = 120, kAbort = 124;
-constexpr int kMaxItems = 1 << 22;  // items of one sequence
 
 struct TcArgs {
   CacheView c;
@@ -150,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= o) x += y;
       }
       if (s < a.b.batch) off[s] = sum + x - v;
-      sum = min(sum + __shfl_sync(0xffffffffu, x, 31), 1 << 30);
+      sum = min(sum + __shfl_sync(0xffffffffu, x, 31), kMaxTotal);
     }
     if (lane == 0) off[a.b.batch] = sum;
   }

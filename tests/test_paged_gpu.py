@@ -705,6 +705,32 @@ def test_index_of_rows_longer_than_a_segment(topk):
     check_topk(m, q, w, topk, got)
 
 
+@pytest.mark.parametrize("Hi", [64, 2])
+def test_index_of_eight_rows_past_2_28_pools(Hi):
+    """A table of 2^20 + 1 pages of 1024 tokens, all but the last one page of zeros: the passes' least, eight rows, then
+    has more tiles than a pass of 2^31 scores, and the best pools lie in its last tiles."""
+    page, width, topk, rows = 1024, (1 << 20) + 1, 8, 8
+    cache = dsa.PagedCache.empty(2, page)
+    cache.khat.zero_()
+    best = torch.randperm(256, generator=torch.Generator().manual_seed(4)).float()
+    cache.khat[1, :, 0] = best.to(torch.bfloat16).to(DEV)
+    table = torch.zeros(1, width, dtype=torch.int32, device=DEV)
+    table[0, -1] = 1
+    n = width * page
+    batch = dsa.PagedBatch(table, i32([n]), i32([0, rows]))
+    q = torch.zeros(rows, Hi, DI, dtype=torch.bfloat16, device=DEV)
+    q[:, 0, 0] = 1
+    ws = torch.full((dsa.paged_index_topk_workspace_size(rows, width, page),), 255, dtype=torch.uint8, device=DEV)
+    got = dsa.dsa_paged_index_topk(cache, batch, q, torch.ones(rows, Hi, device=DEV), topk, workspace=ws)
+    dsa.dsa_sync_status()
+    assert [k for k, _ in dsa.last_kernel_config()["kernels"]] == [PAIRS, "paged_select"]
+    for r in range(rows):
+        first = (width - 1) * page // 4
+        mine = best[:(n - rows + r) // 4 - first]
+        want = sorted(first + j for j in mine.topk(topk).indices.tolist())
+        assert got[r].tolist() == want, r
+
+
 @pytest.mark.parametrize("Hi,topk", [(32, 512), (5, 100)])
 @pytest.mark.parametrize("new,old", [([1, 1, 1], [33000, 4097, 12003]), ([140], [10000]), ([350], [10000])])
 def test_index_real_values(new, old, Hi, topk):
