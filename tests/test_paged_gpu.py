@@ -423,6 +423,67 @@ def test_compact_shared_pages_and_large_pages():
     check_moves(cache, before, moves)
 
 
+@pytest.mark.parametrize("num_pages", [16384, 16385, 70001])
+@pytest.mark.parametrize("fill", [0.0, 0.05, 0.5, 0.97, 1.0])
+def test_compact_of_many_pages(num_pages, fill):
+    """One CTA's plan at its largest, and a cluster's: the number of used pages is a page of the first, a middle and
+    the last CTA's stretch, or of none."""
+    used, width = int(num_pages * fill), 1200
+    lens = [16 * min(width, used - at) - 3 for at in range(0, used, width)]
+    p = Pages(lens + [0], 16, num_pages, width + 1, seed=num_pages)
+    cache = random_cache(num_pages, 16)
+    t, before = p.to_gpu(), [b.clone() for b in buffers(cache)]
+    got = dsa.dsa_cache_compact(cache, t)
+    dsa.dsa_sync_status()
+    n, moves = p.compact()
+    assert n == used and got.tolist() == [used, len(moves)] and bool(moves) == (0 < used < num_pages)
+    p.check(t)
+    for b, w in zip(buffers(cache), before):
+        if moves:
+            src, dst = (list(x) for x in zip(*moves))
+            w[dst] = w[src]
+        assert same_bits(b, w)
+
+
+@pytest.mark.parametrize("num_pages", [16384, 20000])
+def test_fork_of_many_children(num_pages):
+    """More children than a CTA has threads, planned by one CTA and by a cluster; requests that only one of its CTAs
+    can see to be bad, and one that two see half of, change nothing."""
+    parents, n = 90, 9000
+    lens = [1 + 7 * s % 45 for s in range(parents)]  # some end with a page
+    p = Pages(lens + [0] * (n + 10), 16, num_pages, 5, seed=num_pages)
+    cache = random_cache(num_pages, 16)
+    t, before = p.to_gpu(), [b.clone() for b in buffers(cache)]
+    order = np.random.default_rng(7).permutation(n + 10) + parents
+    src, dst = [j % parents for j in range(n)], order[:n].tolist()
+    for j, to in ((8191, dst[2]), (8999, dst[8191]), (0, dst[1]), (5000, 3), (7000, n + 10 + parents), (2500, -1)):
+        bad = dst[:j] + [to] + dst[j + 1:]
+        assert dsa.dsa_cache_fork(cache, t, i32(src), i32(bad)).item() == -2 ** 31, j
+        with pytest.raises(dsa.DsaError):
+            dsa.dsa_sync_status()
+        dsa.dsa_clear_status()
+        p.check(t)
+    got = dsa.dsa_cache_fork(cache, t, i32(src), i32(dst))
+    dsa.dsa_sync_status()
+    taken, moves = p.fork(src, dst)
+    assert got.item() == taken and taken > 8000
+    p.check(t)
+    froms, tos = (list(x) for x in zip(*moves))
+    for b, w in zip(buffers(cache), before):
+        w[tos] = w[froms]
+        assert same_bits(b, w)
+    left = len(p.free_pages())
+    more = order[n:].tolist()
+    dsa.dsa_cache_free(cache, t, i32(dst[::2]))
+    p.free(dst[::2])
+    p.check(t)
+    assert len(p.free_pages()) > left
+    got = dsa.dsa_cache_fork(cache, t, i32([0] * 10), i32(more))
+    dsa.dsa_sync_status()
+    assert got.item() == p.fork([0] * 10, more)[0]
+    p.check(t)
+
+
 @pytest.mark.parametrize("layers", [2, 33])
 def test_layers_move_together(layers):
     """fork, compact and copy_pages of several layers' caches (more than one launch takes): one table, every layer's
