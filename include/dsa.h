@@ -333,7 +333,8 @@ typedef struct {
  *                cu_q[s+1]-1 of the call's tensors are sequence s's new tokens,
  *                the last of the sequence, in order (none is allowed)
  *   rows         rows of the call's tensors, at least cu_q[batch]; the rows
- *                behind the last sequence are padding: neither read nor written
+ *                behind the last sequence are padding: what they hold does not
+ *                matter, and their outputs are not written
  * batch 1..8192; max_pages * page_size <= 2^31 - 1.  Row r of sequence s has
  * position i = seq_lens[s] - cu_q[s+1] + r.
  * These arrays are read when the kernels run, so they cannot be checked before
@@ -462,8 +463,8 @@ dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* caches, int layers, cons
 
 /* Bytes of workspace dsa_paged_index_topk is best given: 4.5 B per row and
  * pool of max_pages pages (rounded up to 32 pools: the scores, and the largest
- * of each eight), in passes of rows whose scores stay under 1 GiB.  It
- * accepts less, down to the bytes for min(rows, 8) rows, with the same result.
+ * of each eight), in passes of rows whose scores stay under 1 GiB (or of eight
+ * rows, where those are more).  It accepts less, down to the bytes for min(rows, 8) rows, with the same result.
  * Returns 0 for invalid sizes (and for rows = 0, which needs none). */
 size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size);
 
@@ -475,7 +476,11 @@ size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size
  * ascending, ties to the lower pool, then -1, as dsa_index_topk writes them.
  *   q_idx  bf16 [rows, Hi, Di]   w  fp32 [rows, Hi]   (Hi 1..64, Di = 64)
  * The new tokens must have been appended.  Scores are fp32 sums over the bf16
- * pair; the selection is exact with respect to them, and the same on every run.
+ * pair; the selection is exact with respect to them, and the same on every run
+ * of the same call.  Which of three kernels makes a sequence's scores depends on
+ * the call's rows, sequences and table width too, and each sums in an order of
+ * its own: where scores differ by no more than their rounding, another batch
+ * around the same row may select another pool.
  */
 dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
                                   const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,

@@ -1642,7 +1642,10 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
   dsa::call_param("Hi", Hi);
   dsa::call_param("topk", topk);
   dsa::call_param("rows_per_pass", pass);
-  // (the others' rows taken off, one each: what the longest may have)
+  // What the longest sequence may have when every other one has a row.  Idle
+  // slots make it too low, and `pairs` below false: then a sequence that a
+  // tcgen05 kernel would score faster is left to a slower one, with the same
+  // result.  (The host does not know the sequences' rows, only their sum.)
   dsa::TcRule rule = paged_tc_rule(Hi);
   const int64_t long_rows = b.rows - b.batch + 1;
   const bool tc = long_rows >= rule.rows && (long_rows + 127) / 128 * ((ld + 255) / 256) >= rule.tiles &&

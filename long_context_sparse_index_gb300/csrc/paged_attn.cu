@@ -18,12 +18,16 @@
 // memory, the CTAs' through distributed shared memory, always in the same
 // order: no atomics, no workspace, one launch, the same bits on every run.
 //
-// Measured with 512 pools a row:
-//   1 row          7.8 us, latency: three dependent reads (selection, page,
+// Measured with 512 pools a row (launches in a graph; keys and values from HBM,
+// by selections in turn that L2 cannot hold together, as one layer of many finds
+// them; in brackets the same selection again, which L2 holds):
+//   1 row          7.2 us, latency: three dependent reads (selection, page,
 //                  key), the copies of five blocks at once, the merge.
-//   64 rows        12.0 us of which the gather takes 9: 68 MB from HBM at the
-//                  rate of the copy peak.
-//   4096 rows      284 us: 15.2 TB/s of keys and values from L2, 0.75 of the
+//   64 rows        18.0 us (12.3): 67 MB at 3.7 TB/s, 0.55 of the copy peak.  The
+//                  copies begin when the row's table of keys is complete, and
+//                  two stages of a ring keep too few of them under way.
+//   256 rows       49 us: 269 MB at 5.5 TB/s.
+//   4096 rows      284 us (a chunk: its rows share keys, which come from L2): 15.2 TB/s of keys and values from L2, 0.75 of the
 //                  1 KB-gather rate, and half of the issue slots: the chains of
 //                  12 warps an SM (168 registers) bound it.  Fewer instructions
 //                  (precomputed addresses, no predicates: 283 us) changed
@@ -491,14 +495,17 @@ cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q
 
 // The CTAs of a row: as many as let all rows run at once.  A cluster lies
 // within a part of the chip, so this is less than the CTAs that fit (16 rows of
-// 8 CTAs with the long ring take two turns, 13.8 us; of 6, 8.0), and the
+// 8 CTAs with the long ring take two turns, 15.0 us; of 6, 9.6), and the
 // runtime is asked.  With 5 CTAs or more a row the long ring, one CTA an SM, is
 // taken if it fits: it has all of a CTA's blocks under way at once (25 rows of 5:
-// 8.8 us, of 8 with two stages 9.1; 30 rows of 4 9.9 against 9.3).  Rows of up to
-// 6 blocks are not split: 5 blocks take 5.6 us with one CTA, 6.6 with two, 5.5
-// with five and up to 8.2 at 100 rows.  Otherwise, at 512 pools: 64 rows 22.4 us
-// with one CTA each, 14.4 / 14.1 / 12.3 / 12.0 with 2 / 3 / 4 / 6; 100 rows 31 / 21.5
-// / 18.5 / 17.0 with 1 to 4 and 24.7 with 5 (two turns); 200 rows 41.7 / 38.3.
+// 11.0 us, of 8 with two stages 11.5; 30 rows of 4 13.0 against 11.7).  Rows of up
+// to 6 blocks are not split: 5 blocks of 64 rows take 7.8 us with one CTA, 8.4 with
+// two, 8.5 with five; of 8 rows 6.9, 7.3 and 6.1; of 100 rows 8.1, 9.4 and 13.6.
+// Otherwise, at 512 pools: 64 rows 31.1 us with one CTA each, 21.7 / 19.0 / 18.0 /
+// 17.7 / 17.5 with 2 to 6 and 24.0 with 8 (two turns); 100 rows 34.1 / 26.5 / 24.7 /
+// 24.6 with 1 to 4 and 31.6 with 5; 128 rows 36.4 / 30.3 / 29.4 with 1 to 3 and 37.9
+// with 4; 200 rows 42.7 / 40.2; 256 rows 49.3 / 61.3.  All with keys and values
+// from HBM; those that L2 holds take 12.3 us for 64 rows of 4 and the same choices.
 constexpr int kWhole = 6;
 constexpr int kRing = 5;
 

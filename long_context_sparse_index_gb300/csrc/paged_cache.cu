@@ -26,7 +26,9 @@ constexpr int kDi = 64;
 // key: its three predecessors come from the call's rows, or from the page
 // where they are older than the call.  Each row's bytes are read once (the
 // three indexer keys a second time, from L1 or L2); nothing is staged.
-// Bound by latency: 3.4 us for 64 rows, 4.3 us for 9815 rows (13 MB, 3 TB/s).
+// Bound by latency: 3.4 us for 64 rows, 5.4 us for 9816 rows (13 MB, 2.4 TB/s)
+// with inputs and pages in turn, 3.9 with the same ones, which L2 then holds
+// (launches in a graph; alone and with all caches empty 6.2 and 7.0).
 constexpr int kAppendWarps = 4;
 
 __global__ void __launch_bounds__(32 * kAppendWarps)
@@ -137,8 +139,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 constexpr int kCopyThreads = 256;
 // 16-byte vectors a block copies at a time: a page of 64 tokens, or half of one
 // of 128, and so on (704 B a token), so that no block has a remainder to copy
-// from pages of 64 tokens on.  Blocks of 32 KB left a third of every second one
-// idle: a compaction of 165 MB took 28 us.
+// from pages of 64 tokens on.  8 vectors a thread, which leave a third of every
+// second block idle there, take as long: 32.6 us against 33.2 for the copies of a
+// compaction of 165 MB, with events around the launch, in turn.
 constexpr int kCopyUnroll = 11;
 constexpr int kCopyVecs = kCopyThreads * kCopyUnroll;
 
@@ -301,7 +304,13 @@ __device__ __forceinline__ void plan_free_list(const int32_t* count, int num_pag
 
 // ----------------------------------------------------------------- reserve
 // ws: off [max_seqs], list [num_pages].  One launch: the plan, then a warp per
-// sequence takes its pages.
+// sequence takes its pages, or gives them back.  Bound by latency: 5.1 us for
+// 64 sequences of which none needs a page, 5.9 when each takes (or returns) one
+// (growing and shrinking in turn in a graph; 7.1 with 70000 pages).  A long
+// request is walked 32 pages at a time, each round waiting for memory: 23 us to
+// take the 8192 pages of a prompt of 131072 tokens in pages of 16, 119 to give
+// them back; 4096 sequences share the warps of one CTA (83 and 126 us) or of a
+// cluster (29 and 33).
 template <int kC>
 __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
     cache_reserve_kernel(const PageTableView t, int shift, int num_pages, const int32_t* __restrict__ add,
@@ -513,8 +522,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 // ----------------------------------------------------------------- compact
 // With U used pages, those at or above U move into the free ones below: the
 // k-th to the k-th, both ascending, so every page moves at most once and no
-// page is both read and written.  The copies run at 5.5 TB/s (165 MB read and
-// written in 30 us), 0.8 of the copy peak.  ws: {U, moved}, hole [num_pages], high
+// page is both read and written.  The copies run at 5.5 TB/s (165 MB in all,
+// read and written, in 30 us by ncu), 0.8 of the copy peak.  ws: {U, moved}, hole [num_pages], high
 // [num_pages], rank_of [num_pages] (for pages at or above U: the place in
 // `high`, or -1).
 struct CompactWs {
