@@ -464,7 +464,8 @@ dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* caches, int layers, cons
 /* Bytes of workspace dsa_paged_index_topk is best given: 4.5 B per row and
  * pool of max_pages pages (rounded up to 32 pools: the scores, and the largest
  * of each eight), in passes of rows whose scores stay under 1 GiB (or of eight
- * rows, where those are more).  It accepts less, down to the bytes for min(rows, 8) rows, with the same result.
+ * rows, where those are more).  It accepts less, down to the bytes for
+ * min(rows, 8) rows, with the same result.
  * Returns 0 for invalid sizes (and for rows = 0, which needs none). */
 size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size);
 

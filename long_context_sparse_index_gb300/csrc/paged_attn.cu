@@ -27,12 +27,13 @@
 //                  copies begin when the row's table of keys is complete, and
 //                  two stages of a ring keep too few of them under way.
 //   256 rows       49 us: 269 MB at 5.5 TB/s.
-//   4096 rows      284 us (a chunk: its rows share keys, which come from L2): 15.2 TB/s of keys and values from L2, 0.75 of the
-//                  1 KB-gather rate, and half of the issue slots: the chains of
-//                  12 warps an SM (168 registers) bound it.  Fewer instructions
-//                  (precomputed addresses, no predicates: 283 us) changed
-//                  nothing; S a block ahead of the softmax took 334 us, for the
-//                  copies then have less time.
+//   4096 rows      284 us (a chunk: its rows share keys, which come from L2):
+//                  15.2 TB/s of keys and values, 0.75 of the 1 KB-gather rate,
+//                  and half of the issue slots: the chains of 12 warps an SM
+//                  (168 registers) bound it.  Fewer instructions (precomputed
+//                  addresses, no predicates: 283 us) changed nothing; S a block
+//                  ahead of the softmax took 334 us, for the copies then have
+//                  less time.
 #include "paged.cuh"
 
 namespace dsa {

@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, kMt <= 2 ? 3 : 2)
 //      set bits in order are the row, ascending, the first ties with them.
 // Latency bounds it: 10.6 us for one row or 64 of 32768 (1024 threads each), 65
 // us by ncu for 2048 rows (256 threads, five rows an SM at a time; six, at 40
-// registers, 80).  A threshold from a sample and one pass over the row took 118 us for those; a
-// warp per row 270.
+// registers, 80).  A threshold from a sample and one pass over the row took 118
+// us for those; a warp per row 270.
 // Should the list run over (hundreds of ties or of neighbours alike), or the
 // maxima have no finite range, a long row goes the short rows' way: the same
 // result, more passes.
@@ -692,8 +692,9 @@ cudaError_t launch_paged_select(const BatchView& b, int shift, int64_t row0, int
   const bool few = nrows <= ctx.num_sms;
   // Short rows by the thousand: no list is ever made, and ten of 128 threads
   // share an SM.  (The host does not know the rows' lengths: the table's width
-  // decides, and short rows in a wide table go the longer rows' way.)  256 / 128 threads, 2048 pools: 4096 rows 51.5 / 38.2, 1000 rows 20.5
-  // / 16.6, 300 rows (one turn either way) 12.3 / 14.3; 4096 pools, 2000 rows 44.3 / 45.3.
+  // decides, and short rows in a wide table go the longer rows' way.)  256 / 128
+  // threads, 2048 pools: 4096 rows 51.5 / 38.2, 1000 rows 20.5 / 16.6, 300 rows (one
+  // turn either way) 12.3 / 14.3; 4096 pools, 2000 rows 44.3 / 45.3.
   const int64_t pools = static_cast<int64_t>(b.max_pages) << (shift - 2);
   if (nrows > 5 * static_cast<int64_t>(ctx.num_sms) && pools <= 2048 && pools <= 8 * topk)
     return launch_select<0, 128>(b, shift, row0, nrows, scores, tops, ld, topk, pool_idx, ctx);

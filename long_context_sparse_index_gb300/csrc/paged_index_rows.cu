@@ -19,8 +19,9 @@
 // Bound by latency up to a few tiles a CTA, then by the reads (537 MB in 97 us,
 // 5.5 TB/s).  With all 256 columns in use (64 x 7 rows: 3.5 TB/s, tensor pipe 32 %,
 // issue slots 44 %) by the chain load, wait, fold, shuffle of the epilogue's 32
-// thousand values a tile, no unit being full: 8 epilogue warps took 53 us for 7 rows, 16 that go row by row 45.  One TMA
-// warp issued a box every 25 ns, so that pages of 16 tokens (64 boxes a tile) took
+// thousand values a tile, no unit being full: 8 epilogue warps took 53 us for 7
+// rows, 16 that go row by row 45.  One TMA warp issued a box every 25 ns, so that
+// pages of 16 tokens (64 boxes a tile) took
 // 77 us; three warps take 45, and leave the epilogue its 94 registers (with four
 // it had 80 and took 2 to 4 us more).  Five stages were no faster than four.
 #include "paged.cuh"
