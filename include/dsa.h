@@ -501,6 +501,153 @@ dsa_status_t dsa_paged_sparse_attn_fwd(const dsa_paged_cache_t* cache, const dsa
                                        float* lse, void* stream);
 
 /*
+ * Rotated positions.  (The source pages' layer has no positional encoding; these
+ * calls serve layers that have one.)  A table cos_sin, fp32 [positions, dims]
+ * with rows `stride` elements apart (a multiple of 4; 16-byte aligned), holds
+ * for every position the cosines of its dims/2 angles and behind them the
+ * sines.  It turns the first `dims` dimensions of a head (a multiple of 16):
+ * pair j at position p, with c = cos_sin[p][j] and s = cos_sin[p][dims/2 + j],
+ * becomes
+ *   (a c - b s, b c + a s)
+ * Pairs are (j, j + dims/2), or (2j, 2j + 1) with `interleaved` nonzero.  Any
+ * table will do: base, scaling and a factor on the logits are the caller's.
+ * A position that the table does not have is not followed: the row is not
+ * written, and dsa_sync_status reports DSA_ERR_INTERNAL.
+ */
+typedef struct {
+  const float* cos_sin;
+  int64_t positions; /* 1 .. 2^31 - 1 */
+  int64_t stride;
+  int dims;
+  int interleaved;
+} dsa_rope_t;
+
+/*
+ * Turns x bf16 [rows, heads, D] (rows x_stride elements apart, within a row
+ * contiguous) into out (rows out_stride apart), for the training calls: row r by
+ * the table's row positions[r] (device int32 [rows]: a packed batch, a shard), or
+ * by q_begin + r where positions is NULL.  inverse nonzero turns back, by the
+ * transposed matrix: the gradient of the call with inverse = 0 (and, for a table
+ * of unit length, its inverse).  Sums in fp32, rounded once more to bf16.
+ * D is 64 or 128, heads 1..128, dims <= D; dimensions past `dims` are copied.
+ * out may be x, with the same stride; else the two must not overlap.
+ */
+dsa_status_t dsa_rope(const void* x, int64_t x_stride, int64_t rows, int heads, int D, const dsa_rope_t* rope,
+                      const int32_t* positions, int64_t q_begin, int inverse, void* out, int64_t out_stride,
+                      void* stream);
+
+/*
+ * Queries that an append turns along: q bf16 [rows, Hq, 128] by the rope of the
+ * keys, q_idx bf16 [rows, Hi, 64] by the rope of the indexer's keys, each row at
+ * its position.  Hq = 0 or Hi = 0: none.  Strides as in dsa_rope; q_out may be q,
+ * and q_idx_out q_idx.  Rows behind the last sequence are not written.
+ */
+typedef struct {
+  const void* q;
+  void* q_out;
+  int64_t q_stride;
+  int64_t q_out_stride;
+  const void* q_idx;
+  void* q_idx_out;
+  int64_t q_idx_stride;
+  int64_t q_idx_out_stride;
+  int Hq; /* 0..128 */
+  int Hi; /* 0..64 */
+} dsa_rope_queries_t;
+
+/*
+ * dsa_cache_append_reserved (reserved may be NULL) that turns the keys on the
+ * way: k by `rope` and k_idx by `rope_idx`, each at its row's position in its
+ * sequence, rounded to bf16 from a correctly rounded fp32 sum; v is not turned.
+ * The pooled keys are those of the turned indexer keys.  Either rope may be NULL
+ * (then those keys, and their queries, are not turned).  queries may be NULL;
+ * queries of a rope that is NULL are refused.  One launch.
+ */
+dsa_status_t dsa_cache_append_rope(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                                   int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                                   int64_t k_idx_stride, const dsa_rope_t* rope, const dsa_rope_t* rope_idx,
+                                   const dsa_rope_queries_t* queries, const int32_t* reserved, void* stream);
+
+/*
+ * A paged cache whose keys and values are held in 4 bits: 336 bytes a token
+ * instead of 704.
+ *   kv     uint8 [num_pages, page_size / 4, 576]  the pools' keys and values
+ *   k_idx  bf16  [num_pages, page_size, 64]       as in dsa_paged_cache_t
+ *   khat   bf16  [num_pages, page_size / 4, 128]  as in dsa_paged_cache_t
+ * Page strides: kv's in bytes, a multiple of 16; the others' in elements, a
+ * multiple of 8.  16-byte aligned.  D = 128, Di = 64.
+ *
+ * The 128 values of a key or a value lie in 8 groups of 16 neighbours.  A group
+ * has one scale of 8 bits, 5 of exponent and 3 of mantissa without a sign (those
+ * of an fp16 number, from its bit 7 up), and each value a code of 4 bits, e2m1: 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6, and bit 3 the sign.  It stands for code * scale / 16.
+ * Written: scale = the nearest to 16 max|x| / 6, at most 10240; code = the nearest
+ * to 16 x / scale; ties to even.  So values beyond 3840 saturate, and groups whose
+ * largest magnitude is below 2.3e-5 lose bits of their scale (below 1.5e-6 all of
+ * them).  A group with an infinity or a NaN stands for 16 NaN.  Everything that a
+ * group stands for is exact in bf16.
+ * A pool's 576 bytes, for its tokens t = 0..3:
+ *   0    keys' codes [t][64]: byte b has dimension 2b low and 2b + 1 high
+ *   256  values' codes [group][t][8], in the same order
+ *   512  keys' scales [group / 2][t % 2][t / 2][group % 2]
+ *   544  values' scales [group][t]
+ *
+ * Page tables, batches, reservations and dsa_cache_free are those of the bf16
+ * cache.
+ */
+typedef struct {
+  void* kv;
+  void* k_idx;
+  void* khat;
+  int64_t kv_stride;
+  int64_t k_idx_stride;
+  int64_t khat_stride;
+  int64_t num_pages;
+  int page_size;
+  int D;
+  int Di;
+} dsa_paged_cache4_t;
+
+/* dsa_cache_append_rope into a cache in 4 bits: k (turned, rounded to bf16) and v
+ * are held as their codes.  Without ropes, the plain append. */
+dsa_status_t dsa_cache4_append(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                               int64_t k_idx_stride, const dsa_rope_t* rope, const dsa_rope_t* rope_idx,
+                               const dsa_rope_queries_t* queries, const int32_t* reserved, void* stream);
+
+/* The keys and values of the batch's rows as the cache holds them: k, v bf16
+ * [rows, 128] (rows *_stride elements apart, multiples of 8), exactly what the
+ * codes stand for.  A batch whose cu_q counts all tokens reads whole sequences.
+ * Rows behind the last sequence are not written. */
+dsa_status_t dsa_cache4_read(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, void* k,
+                             int64_t k_stride, void* v, int64_t v_stride, void* stream);
+
+/* dsa_cache_copy_pages, dsa_cache_fork, dsa_cache_compact and
+ * dsa_paged_index_topk over caches in 4 bits: the same arguments and results. */
+dsa_status_t dsa_cache4_copy_pages(const dsa_paged_cache4_t* caches, int layers, const int32_t* src,
+                                   const int32_t* dst, int64_t n, void* stream);
+dsa_status_t dsa_cache4_fork(const dsa_paged_cache4_t* caches, int layers, const dsa_page_table_t* pages,
+                             const int32_t* src, const int32_t* dst, int64_t n, int32_t* result, void* workspace,
+                             size_t ws_bytes, void* stream);
+dsa_status_t dsa_cache4_compact(const dsa_paged_cache4_t* caches, int layers, const dsa_page_table_t* pages,
+                                int32_t* result, void* workspace, size_t ws_bytes, void* stream);
+dsa_status_t dsa_paged4_index_topk(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
+                                   const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/*
+ * dsa_paged_sparse_attn_fwd over a cache in 4 bits: the attention over the keys
+ * and values that the codes stand for, with the same arguments and outputs.
+ * Products in fp16 with fp32 sums: codes times scales are exact in fp16, a head's
+ * query is scaled into its range by a power of two of its own, and the weights
+ * are rounded to it for their product with the values.  Needs no workspace; the
+ * same bits on every run.
+ */
+dsa_status_t dsa_paged4_sparse_attn_fwd(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, const void* q,
+                                        const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o,
+                                        float* lse, void* stream);
+
+/*
  * Indexer + top-k for callers that cannot allocate device memory.  (The
  * source pages have no counterpart to this call; it exists for users of the
  * library.)

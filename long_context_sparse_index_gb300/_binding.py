@@ -35,7 +35,9 @@ EXPORTED = ("dsa_index_topk_workspace", "dsa_index_topk", "dsa_sparse_attn_fwd",
             "dsa_fwd_tc_profile", "dsa_measure_fold", "dsa_cache_append", "dsa_cache_append_reserved",
             "dsa_cache_copy_pages",
             "dsa_cache_workspace", "dsa_cache_reserve", "dsa_cache_fork", "dsa_cache_free", "dsa_cache_compact",
-            "dsa_paged_index_topk_workspace", "dsa_paged_index_topk", "dsa_paged_sparse_attn_fwd")
+            "dsa_paged_index_topk_workspace", "dsa_paged_index_topk", "dsa_paged_sparse_attn_fwd", "dsa_rope",
+            "dsa_cache_append_rope", "dsa_cache4_append", "dsa_cache4_read", "dsa_cache4_copy_pages",
+            "dsa_cache4_fork", "dsa_cache4_compact", "dsa_paged4_index_topk", "dsa_paged4_sparse_attn_fwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -116,6 +118,8 @@ def _configure(lib):
     lib.dsa_last_kernel_config.restype = ctypes.c_int
     from ._paged import _configure_paged
     _configure_paged(lib)
+    from ._rope import _configure_rope
+    _configure_rope(lib)
     return lib
 
 

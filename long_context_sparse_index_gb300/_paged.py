@@ -24,6 +24,11 @@ class _CacheStruct(ctypes.Structure):
                 ("Di", _i32)]
 
 
+class _Cache4Struct(ctypes.Structure):
+    _fields_ = [("kv", _vp), ("k_idx", _vp), ("khat", _vp), ("kv_stride", _i64), ("k_idx_stride", _i64),
+                ("khat_stride", _i64), ("num_pages", _i64), ("page_size", _i32), ("D", _i32), ("Di", _i32)]
+
+
 class _BatchStruct(ctypes.Structure):
     _fields_ = [("block_table", _vp), ("table_stride", _i64), ("seq_lens", _vp), ("cu_q", _vp), ("rows", _i64),
                 ("max_pages", _i32), ("batch", _i32)]
@@ -99,6 +104,9 @@ class PagedCache:
     in 64..127), all bf16.  Within a page everything is contiguous; the
     distance between pages is free (a multiple of 8 elements)."""
 
+    _four = False
+    _cstruct = _CacheStruct
+
     def __init__(self, k, v, k_idx, khat):
         for t, n, d in ((k, "k", 128), (v, "v", 128), (k_idx, "k_idx", 64), (khat, "khat", 128)):
             _on_device(t, n, torch.bfloat16, 3)
@@ -127,6 +135,56 @@ class PagedCache:
         def new(tokens, d):
             return torch.empty(num_pages, tokens, d, dtype=torch.bfloat16, device=device)
         return cls(new(page_size, 128), new(page_size, 128), new(page_size, 64), new(page_size // 4, 128))
+
+
+class PagedCache4:
+    """One layer's cache with keys and values in 4 bits, 336 bytes a token
+    instead of 704, in pages of ``page_size`` tokens (a power of two, 16..1024).
+
+    kv uint8 [pages, page_size / 4, 576] (the codes and scales of each pool of
+    four tokens; the format stands in dsa.h), k_idx [pages, page_size, 64] and
+    khat [pages, page_size / 4, 128] bf16 as in PagedCache.  Within a page
+    everything is contiguous; the distance between pages is free (a multiple of
+    16 bytes).  The page operators and the indexer take it as they take a
+    PagedCache; dsa_cache4_append writes it, dsa_paged4_sparse_attn_fwd attends
+    over it and dsa_cache4_read reads rows back."""
+
+    _four = True
+    _cstruct = _Cache4Struct
+
+    def __init__(self, kv, k_idx, khat):
+        for t, n, d, dtype in ((kv, "kv", 576, torch.uint8), (k_idx, "k_idx", 64, torch.bfloat16),
+                               (khat, "khat", 128, torch.bfloat16)):
+            _on_device(t, n, dtype, 3)
+            if t.shape[2] != d or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+                raise ValueError(f"{n} must be [pages, pools or tokens, {d}] with contiguous pages (got shape "
+                                 f"{tuple(t.shape)}, strides {t.stride()})")
+        pages, page_size = k_idx.shape[0], k_idx.shape[1]
+        _shape(kv, "kv", (pages, page_size // 4, 576))
+        _shape(khat, "khat", (pages, page_size // 4, 128))
+        self.kv, self.k_idx, self.khat = kv, k_idx, khat
+        self.num_pages, self.page_size = pages, page_size
+        self.device = kv.device
+        self.device_index = kv.device.index
+
+        def stride(t):
+            return t.stride(0) if pages > 1 else t.shape[1] * t.shape[2]
+
+        self._struct = _Cache4Struct(kv.data_ptr(), k_idx.data_ptr(), khat.data_ptr(), stride(kv), stride(k_idx),
+                                     stride(khat), pages, page_size, 128, 64)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, device="cuda"):
+        """A cache of uninitialised pages."""
+        def new(n, d, dtype=torch.bfloat16):
+            return torch.empty(num_pages, n, d, dtype=dtype, device=device)
+        return cls(new(page_size // 4, 576, torch.uint8), new(page_size, 64), new(page_size // 4, 128))
+
+
+def _is_cache(cache, four: bool):
+    if getattr(cache, "_four", None) is not four:
+        raise TypeError(f"cache must be a {'PagedCache4' if four else 'PagedCache'} (got {type(cache).__name__})")
 
 
 class PagedBatch:
@@ -216,6 +274,14 @@ def _configure_paged(lib):
     lib.dsa_paged_index_topk_workspace.restype = sz
     lib.dsa_paged_index_topk.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, sz, vp]
     lib.dsa_paged_sparse_attn_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp]
+    lib.dsa_cache4_copy_pages.argtypes = lib.dsa_cache_copy_pages.argtypes
+    lib.dsa_cache4_fork.argtypes = lib.dsa_cache_fork.argtypes
+    lib.dsa_cache4_compact.argtypes = lib.dsa_cache_compact.argtypes
+    lib.dsa_paged4_index_topk.argtypes = lib.dsa_paged_index_topk.argtypes
+    lib.dsa_paged4_sparse_attn_fwd.argtypes = lib.dsa_paged_sparse_attn_fwd.argtypes
+    for f in (lib.dsa_cache4_copy_pages, lib.dsa_cache4_fork, lib.dsa_cache4_compact, lib.dsa_paged4_index_topk,
+              lib.dsa_paged4_sparse_attn_fwd):
+        f.restype = ctypes.c_int
     for f in (lib.dsa_cache_append, lib.dsa_cache_append_reserved, lib.dsa_cache_copy_pages, lib.dsa_cache_reserve,
               lib.dsa_cache_fork, lib.dsa_cache_free, lib.dsa_cache_compact, lib.dsa_paged_index_topk,
               lib.dsa_paged_sparse_attn_fwd):
@@ -261,6 +327,7 @@ def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=N
     overwrite their last tokens; given it, the append then writes nothing and
     dsa_sync_status reports DSA_ERR_INTERNAL.  Without it, look at the word
     before appending."""
+    _is_cache(cache, False)
     dev = _device_of(cache, batch)
     ks = _rows_strided(k, "k", torch.bfloat16, 128, dev)
     vs = _rows_strided(v, "v", torch.bfloat16, 128, dev)
@@ -279,16 +346,18 @@ def dsa_cache_append(cache: PagedCache, batch: PagedBatch, k, v, k_idx, stream=N
 
 def _layers(cache):
     """(first cache, struct array, count) of one cache or of a sequence of the layers' caches."""
-    if isinstance(cache, PagedCache):
+    if isinstance(cache, (PagedCache, PagedCache4)):
         return cache, cache._ref, 1
     caches = list(cache)
-    if not caches or not all(isinstance(c, PagedCache) for c in caches):
-        raise TypeError("cache must be a PagedCache or a sequence of the layers' PagedCaches")
+    if not caches or not (all(isinstance(c, PagedCache) for c in caches) or
+                          all(isinstance(c, PagedCache4) for c in caches)):
+        raise TypeError("cache must be a PagedCache (or PagedCache4) or a sequence of the layers' PagedCaches (or "
+                        "PagedCache4s)")
     first = caches[0]
     for c in caches:
         if c.device_index != first.device_index:
             raise ValueError("the layers' caches must be on one device")
-    return first, (_CacheStruct * len(caches))(*[c._struct for c in caches]), len(caches)
+    return first, (first._cstruct * len(caches))(*[c._struct for c in caches]), len(caches)
 
 
 def dsa_cache_copy_pages(cache, src, dst, stream=None):
@@ -299,7 +368,9 @@ def dsa_cache_copy_pages(cache, src, dst, stream=None):
     n = _ids(src, "src", dev)
     _ids(dst, "dst", dev)
     _shape(dst, "dst", (n,))
-    _check(load().dsa_cache_copy_pages(ref, layers, src.data_ptr(), dst.data_ptr(), n, _handle(stream, dev)))
+    lib = load()
+    call = lib.dsa_cache4_copy_pages if first._four else lib.dsa_cache_copy_pages
+    _check(call(ref, layers, src.data_ptr(), dst.data_ptr(), n, _handle(stream, dev)))
 
 
 def cache_workspace_size(num_pages: int, max_seqs: int, n: int = 0) -> int:
@@ -342,8 +413,9 @@ def dsa_cache_fork(cache, pages: PageTable, src, dst, result=None, workspace=Non
     _shape(dst, "dst", (n,))
     result = _result(result, "result", (1,), torch.int32, cache.device, stream)
     ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, n), workspace, cache.device, stream)
-    _check(lib.dsa_cache_fork(ref, layers, pages._with_page(cache.page_size), src.data_ptr(), dst.data_ptr(), n,
-                              result.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
+    call = lib.dsa_cache4_fork if cache._four else lib.dsa_cache_fork
+    _check(call(ref, layers, pages._with_page(cache.page_size), src.data_ptr(), dst.data_ptr(), n, result.data_ptr(),
+                ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
 
 
@@ -364,8 +436,9 @@ def dsa_cache_compact(cache, pages: PageTable, result=None, workspace=None, stre
     dev, lib = _of_cache(cache, pages), load()
     result = _result(result, "result", (2,), torch.int32, cache.device, stream)
     ws = _scratch(lib.dsa_cache_workspace(pages.num_pages, pages.max_seqs, 0), workspace, cache.device, stream)
-    _check(lib.dsa_cache_compact(ref, layers, pages._with_page(cache.page_size), result.data_ptr(), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), _handle(stream, dev)))
+    call = lib.dsa_cache4_compact if cache._four else lib.dsa_cache_compact
+    _check(call(ref, layers, pages._with_page(cache.page_size), result.data_ptr(), ws.data_ptr(),
+                ws.numel() * ws.element_size(), _handle(stream, dev)))
     return result
 
 
@@ -385,9 +458,9 @@ def dsa_paged_index_topk(cache: PagedCache, batch: PagedBatch, q_idx, w, topk: i
         _shape(w, "w", (rows, Hi))
     pool_idx = _result(pool_idx, "pool_idx", (rows, max(topk, 0)), torch.int32, cache.device, stream)
     ws = _scratch(batch._index_workspace(rows, cache.page_size), workspace, cache.device, stream)
-    _check(lib.dsa_paged_index_topk(cache._ref, batch._with_rows(rows), q_idx.data_ptr(), w.data_ptr(), Hi, Di, topk,
-                                    pool_idx.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                    _handle(stream, dev)))
+    call = lib.dsa_paged4_index_topk if cache._four else lib.dsa_paged_index_topk
+    _check(call(cache._ref, batch._with_rows(rows), q_idx.data_ptr(), w.data_ptr(), Hi, Di, topk, pool_idx.data_ptr(),
+                ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, dev)))
     return pool_idx
 
 
@@ -395,6 +468,19 @@ def dsa_paged_sparse_attn_fwd(cache: PagedCache, batch: PagedBatch, q, pool_idx,
                               stream=None):
     """(o [rows, 16, 128] bf16, lse [rows, 16] fp32) of the new tokens' attention
     over their selected pools and their own partial pool."""
+    _is_cache(cache, False)
+    return _attention(load().dsa_paged_sparse_attn_fwd, cache, batch, q, pool_idx, scale, o, lse, stream)
+
+
+def dsa_paged4_sparse_attn_fwd(cache: PagedCache4, batch: PagedBatch, q, pool_idx, scale: float = 0.0, o=None,
+                               lse=None, stream=None):
+    """dsa_paged_sparse_attn_fwd over a cache in 4 bits: the attention over the
+    keys and values that its codes stand for."""
+    _is_cache(cache, True)
+    return _attention(load().dsa_paged4_sparse_attn_fwd, cache, batch, q, pool_idx, scale, o, lse, stream)
+
+
+def _attention(call, cache, batch, q, pool_idx, scale, o, lse, stream):
     dev = _device_of(cache, batch)
     _full(q, "q", torch.bfloat16, 3, dev)
     _full(pool_idx, "pool_idx", torch.int32, 2, dev)
@@ -404,6 +490,6 @@ def dsa_paged_sparse_attn_fwd(cache: PagedCache, batch: PagedBatch, q, pool_idx,
         raise ValueError(f"pool_idx must have {rows} rows (got {sel_rows})")
     o = _result(o, "o", (rows, Hq, D), torch.bfloat16, cache.device, stream)
     lse = _result(lse, "lse", (rows, Hq), torch.float32, cache.device, stream)
-    _check(load().dsa_paged_sparse_attn_fwd(cache._ref, batch._with_rows(rows), q.data_ptr(), pool_idx.data_ptr(), Hq,
-                                            D, topk, scale, o.data_ptr(), lse.data_ptr(), _handle(stream, dev)))
+    _check(call(cache._ref, batch._with_rows(rows), q.data_ptr(), pool_idx.data_ptr(), Hq, D, topk, scale,
+                o.data_ptr(), lse.data_ptr(), _handle(stream, dev)))
     return o, lse

@@ -27,6 +27,8 @@
 #include "dsa_device.cuh"
 #include "dsa_kernels.h"
 #include "paged_kernels.h"
+#include "paged_rope_kernels.h"
+#include "rope_kernels.h"
 
 namespace dsa {
 // Unique id of the calling thread's current CUDA context, or 0 when there is
@@ -1212,6 +1214,8 @@ int64_t dsa_launch_count(void) { return g_launches.load(); }
 
 void dsa_launch_count_reset(void) { g_launches.store(0); }
 
+}  // extern "C"
+
 // ---------------------------------------------------------------- paged cache
 namespace {
 
@@ -1221,6 +1225,7 @@ constexpr int64_t kIntMax = 0x7FFFFFFFLL;
 constexpr int64_t kPagedScratch = int64_t{1} << 28;  // scores of a pass in the recommended workspace (1 GiB)
 constexpr int64_t kPagedPassMax = int64_t{1} << 31;  // scores of a pass however large the workspace
 constexpr int kPagedMinRows = 8;
+constexpr int kMaxRopeHeads = 128;
 // Three kernels make the scores; all give a sequence's rows the same work, with
 // different waste.  Measured at 32 heads where nothing else is said, the
 // score kernels alone, in us.
@@ -1256,32 +1261,65 @@ int log2_of(int x) {
   return s;
 }
 
+dsa_status_t cache_shape(const char* fn, int D, int Di, int page_size, int64_t num_pages) {
+  if (D != kD || Di != kDi)
+    return fail(DSA_ERR_UNSUPPORTED, "%s: D=%d, Di=%d unsupported (kernels implement D=128, Di=64)", fn, D, Di);
+  if (!page_size_ok(page_size))
+    return fail(DSA_ERR_UNSUPPORTED, "%s: page_size=%d unsupported (a power of two, 16..1024)", fn, page_size);
+  if (num_pages < 1 || num_pages > kIntMax / page_size)
+    return fail(DSA_ERR_INVALID_ARG, "%s: num_pages=%lld out of range (num_pages * page_size <= 2^31 - 1)", fn,
+                (long long)num_pages);
+  return DSA_OK;
+}
+dsa_status_t page_stride(const char* fn, const char* name, int64_t stride, int64_t least) {
+  if (stride < least || (stride & 7) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: %s page stride of %lld elements (a multiple of 8, at least %lld)", fn, name,
+                (long long)stride, (long long)least);
+  return DSA_OK;
+}
+
 dsa_status_t cache_view(const char* fn, const dsa_paged_cache_t* c, dsa::CacheView* out) {
   if (!c) return fail(DSA_ERR_INVALID_ARG, "%s: null cache", fn);
   if (!c->k || !c->v || !c->k_idx || !c->khat) return fail(DSA_ERR_INVALID_ARG, "%s: null cache pointer", fn);
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_idx) || !aligned16(c->khat))
     return fail(DSA_ERR_INVALID_ARG, "%s: cache buffers must be 16-byte aligned", fn);
-  if (c->D != kD || c->Di != kDi)
-    return fail(DSA_ERR_UNSUPPORTED, "%s: D=%d, Di=%d unsupported (kernels implement D=128, Di=64)", fn, c->D, c->Di);
-  if (!page_size_ok(c->page_size))
-    return fail(DSA_ERR_UNSUPPORTED, "%s: page_size=%d unsupported (a power of two, 16..1024)", fn, c->page_size);
-  if (c->num_pages < 1 || c->num_pages > kIntMax / c->page_size)
-    return fail(DSA_ERR_INVALID_ARG, "%s: num_pages=%lld out of range (num_pages * page_size <= 2^31 - 1)", fn,
-                (long long)c->num_pages);
+  dsa_status_t st = cache_shape(fn, c->D, c->Di, c->page_size, c->num_pages);
+  if (st != DSA_OK) return st;
   const int64_t page = c->page_size;
-  const struct { int64_t stride, least; const char* name; } strides[4] = {
-      {c->k_stride, page * kD, "k"}, {c->v_stride, page * kD, "v"}, {c->k_idx_stride, page * kDi, "k_idx"},
-      {c->khat_stride, page / 4 * 2 * kDi, "khat"}};
-  for (const auto& st : strides)
-    if (st.stride < st.least || (st.stride & 7) != 0)
-      return fail(DSA_ERR_INVALID_ARG, "%s: %s page stride of %lld elements (a multiple of 8, at least %lld)", fn,
-                  st.name, (long long)st.stride, (long long)st.least);
+  st = page_stride(fn, "k", c->k_stride, page * kD);
+  if (st == DSA_OK) st = page_stride(fn, "v", c->v_stride, page * kD);
+  if (st == DSA_OK) st = page_stride(fn, "k_idx", c->k_idx_stride, page * kDi);
+  if (st == DSA_OK) st = page_stride(fn, "khat", c->khat_stride, page / 4 * 2 * kDi);
+  if (st != DSA_OK) return st;
   *out = dsa::CacheView{static_cast<__nv_bfloat16*>(c->k), static_cast<__nv_bfloat16*>(c->v),
                         static_cast<__nv_bfloat16*>(c->k_idx), static_cast<__nv_bfloat16*>(c->khat), c->k_stride,
                         c->v_stride, c->k_idx_stride, c->khat_stride, static_cast<int>(c->num_pages),
                         log2_of(c->page_size)};
   return DSA_OK;
 }
+
+// A cache in 4 bits: `k` is its kv buffer, in units of two bytes.
+dsa_status_t cache_view(const char* fn, const dsa_paged_cache4_t* c, dsa::CacheView* out) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "%s: null cache", fn);
+  if (!c->kv || !c->k_idx || !c->khat) return fail(DSA_ERR_INVALID_ARG, "%s: null cache pointer", fn);
+  if (!aligned16(c->kv) || !aligned16(c->k_idx) || !aligned16(c->khat))
+    return fail(DSA_ERR_INVALID_ARG, "%s: cache buffers must be 16-byte aligned", fn);
+  dsa_status_t st = cache_shape(fn, c->D, c->Di, c->page_size, c->num_pages);
+  if (st != DSA_OK) return st;
+  const int64_t page = c->page_size;
+  if (c->kv_stride < page / 4 * dsa::kPool4 || (c->kv_stride & 15) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: kv page stride of %lld bytes (a multiple of 16, at least %lld)", fn,
+                (long long)c->kv_stride, (long long)(page / 4 * dsa::kPool4));
+  st = page_stride(fn, "k_idx", c->k_idx_stride, page * kDi);
+  if (st == DSA_OK) st = page_stride(fn, "khat", c->khat_stride, page / 4 * 2 * kDi);
+  if (st != DSA_OK) return st;
+  *out = dsa::CacheView{static_cast<__nv_bfloat16*>(c->kv), nullptr, static_cast<__nv_bfloat16*>(c->k_idx),
+                        static_cast<__nv_bfloat16*>(c->khat), c->kv_stride / 2, 0, c->k_idx_stride, c->khat_stride,
+                        static_cast<int>(c->num_pages), log2_of(c->page_size)};
+  return DSA_OK;
+}
+constexpr bool in_four(const dsa_paged_cache_t*) { return false; }
+constexpr bool in_four(const dsa_paged_cache4_t*) { return true; }
 
 dsa_status_t batch_view(const char* fn, const dsa_paged_batch_t* b, int page_size, dsa::BatchView* out) {
   if (!b) return fail(DSA_ERR_INVALID_ARG, "%s: null batch", fn);
@@ -1327,7 +1365,8 @@ dsa_status_t table_view(const char* fn, const dsa_page_table_t* t, dsa::PageTabl
 }
 
 // The caches of the layers that move pages together: the same pages of the same size.
-dsa_status_t cache_views(const char* fn, const dsa_paged_cache_t* caches, int layers, std::vector<dsa::CacheView>* out) {
+template <typename Cache>
+dsa_status_t cache_views(const char* fn, const Cache* caches, int layers, std::vector<dsa::CacheView>* out) {
   if (!caches) return fail(DSA_ERR_INVALID_ARG, "%s: null cache", fn);
   if (layers < 1) return fail(DSA_ERR_INVALID_ARG, "%s: layers=%d must be >= 1", fn, layers);
   out->resize(layers);
@@ -1384,6 +1423,18 @@ int64_t paged_score_ld(int max_pages, int page_size) {
 }
 size_t paged_scratch_bytes(int64_t rows, int64_t ld) { return static_cast<size_t>(rows) * (ld + ld / 8) * 4; }
 
+// The rows that an append is given; `reserved` may be null.
+dsa_status_t check_rows(const char* fn, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                        const void* k_idx, int64_t k_idx_stride, const int32_t* reserved) {
+  if (!k || !v || !k_idx) return fail(DSA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_idx))
+    return fail(DSA_ERR_INVALID_ARG, "%s: k, v and k_idx must be 16-byte aligned", fn);
+  if (k_stride < kD || v_stride < kD || k_idx_stride < kDi || ((k_stride | v_stride | k_idx_stride) & 7) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: row strides must be multiples of 8 elements, at least a row", fn);
+  if (!aligned4(reserved)) return fail(DSA_ERR_INVALID_ARG, "%s: reserved must be a 4-byte aligned device word", fn);
+  return DSA_OK;
+}
+
 // Both appends; `reserved` may be null.
 dsa_status_t append(const char* fn, const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
                     int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx, int64_t k_idx_stride,
@@ -1395,12 +1446,8 @@ dsa_status_t append(const char* fn, const dsa_paged_cache_t* cache, const dsa_pa
   if (st == DSA_OK) st = batch_view(fn, batch, cache->page_size, &b);
   if (st != DSA_OK) return st;
   if (b.rows == 0) return DSA_OK;
-  if (!k || !v || !k_idx) return fail(DSA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
-  if (!aligned16(k) || !aligned16(v) || !aligned16(k_idx))
-    return fail(DSA_ERR_INVALID_ARG, "%s: k, v and k_idx must be 16-byte aligned", fn);
-  if (k_stride < kD || v_stride < kD || k_idx_stride < kDi || ((k_stride | v_stride | k_idx_stride) & 7) != 0)
-    return fail(DSA_ERR_INVALID_ARG, "%s: row strides must be multiples of 8 elements, at least a row", fn);
-  if (!aligned4(reserved)) return fail(DSA_ERR_INVALID_ARG, "%s: reserved must be a 4-byte aligned device word", fn);
+  st = check_rows(fn, k, k_stride, v, v_stride, k_idx, k_idx_stride, reserved);
+  if (st != DSA_OK) return st;
   dsa::LaunchCtx ctx;
   st = make_ctx(stream, &ctx);
   if (st != DSA_OK) return st;
@@ -1416,24 +1463,15 @@ dsa_status_t append(const char* fn, const dsa_paged_cache_t* cache, const dsa_pa
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-}  // namespace
+// What follows serves both kinds of cache.
 
-dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
-                              int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
-                              int64_t k_idx_stride, void* stream) {
-  return append("dsa_cache_append", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, nullptr, stream);
+dsa_status_t launch_fail(const char* fn, cudaError_t e) {
+  return fail(DSA_ERR_CUDA, "%s: launch: %s", fn, cudaGetErrorString(e));
 }
 
-dsa_status_t dsa_cache_append_reserved(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
-                                       int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
-                                       int64_t k_idx_stride, const int32_t* reserved, void* stream) {
-  return append("dsa_cache_append_reserved", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, reserved,
-                stream);
-}
-
-dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* caches, int layers, const int32_t* src, const int32_t* dst,
-                                  int64_t n, void* stream) try {
-  const char* fn = "dsa_cache_copy_pages";
+template <typename Cache>
+dsa_status_t copy_pages(const char* fn, const Cache* caches, int layers, const int32_t* src, const int32_t* dst,
+                        int64_t n, void* stream) try {
   const dsa::CallScope scope(fn);
   std::vector<dsa::CacheView> views;
   dsa_status_t st = cache_views(fn, caches, layers, &views);
@@ -1449,57 +1487,20 @@ dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* caches, int layers, c
   dsa::call_param("layers", layers);
   dsa::call_variant("a block per slice of a page");
   cudaError_t e = timed_launch("copy_pages", ctx.stream, [&] {
-    return by_layers(views, [&](const dsa::CacheSet& set, bool) { return dsa::launch_copy_pages(set, src, dst, n, ctx); });
+    return by_layers(views, [&](const dsa::CacheSet& set, bool) {
+      return dsa::launch_copy_pages(set, in_four(caches), src, dst, n, ctx);
+    });
   }, layer_launches(views));
-  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_copy_pages: launch");
+  if (e != cudaSuccess) return launch_fail(fn, e);
   return DSA_OK;
 } catch (...) {
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-size_t dsa_cache_workspace(int64_t num_pages, int max_seqs, int64_t n) {
-  if (num_pages < 1 || num_pages > kIntMax || max_seqs < 1 || max_seqs > kMaxTableSeqs || n < 0 || n > kIntMax) return 0;
-  // the fork's list holds one page per child
-  int64_t w = dsa::fork_ws_words(n, max_seqs);
-  const int64_t r = dsa::reserve_ws_words(max_seqs, static_cast<int>(num_pages));
-  const int64_t z = dsa::compact_ws_words(static_cast<int>(num_pages));
-  w = w > r ? w : r;
-  w = w > z ? w : z;
-  return round_up(static_cast<size_t>(w) * 4, 256);
-}
-
-dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add, int32_t* result, void* workspace,
-                               size_t ws_bytes, void* stream) try {
-  const char* fn = "dsa_cache_reserve";
-  const dsa::CallScope scope(fn);
-  dsa::PageTableView t;
-  dsa_status_t st = table_view(fn, pages, &t);
-  if (st != DSA_OK) return st;
-  if (!add || !result || !aligned4(add) || !aligned4(result))
-    return fail(DSA_ERR_INVALID_ARG, "%s: add and result must be 4-byte aligned device arrays", fn);
-  const int np = static_cast<int>(pages->num_pages);
-  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(dsa::reserve_ws_words(t.max_seqs, np)) * 4);
-  if (st != DSA_OK) return st;
-  dsa::LaunchCtx ctx;
-  st = make_ctx(stream, &ctx);
-  if (st != DSA_OK) return st;
-  dsa::call_param("max_seqs", t.max_seqs);
-  dsa::call_param("num_pages", np);
-  dsa::call_variant("plan and take in one launch");
-  cudaError_t e = timed_launch("cache_reserve", ctx.stream, [&] {
-    return dsa::launch_cache_reserve(t, log2_of(pages->page_size), np, add, result, static_cast<int32_t*>(workspace),
-                                     ctx);
-  });
-  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_reserve: launch");
-  return DSA_OK;
-} catch (...) {
-  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
-}
-
-dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
+template <typename Cache>
+dsa_status_t fork_sequences(const char* fn, const Cache* caches, int layers, const dsa_page_table_t* pages,
                             const int32_t* src, const int32_t* dst, int64_t n, int32_t* result, void* workspace,
                             size_t ws_bytes, void* stream) try {
-  const char* fn = "dsa_cache_fork";
   const dsa::CallScope scope(fn);
   std::vector<dsa::CacheView> views;
   dsa::PageTableView t;
@@ -1529,42 +1530,18 @@ dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* caches, int layers, const d
   if (e == cudaSuccess && n > 0)
     e = timed_launch("fork_apply", ctx.stream, [&] {
       return by_layers(views, [&](const dsa::CacheSet& set, bool first) {
-        return dsa::launch_fork_apply(set, first, t, src, dst, static_cast<int>(n), ws, ctx);
+        return dsa::launch_fork_apply(set, in_four(caches), first, t, src, dst, static_cast<int>(n), ws, ctx);
       });
     }, layer_launches(views));
-  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_fork: launch");
+  if (e != cudaSuccess) return launch_fail(fn, e);
   return DSA_OK;
 } catch (...) {
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-dsa_status_t dsa_cache_free(const dsa_page_table_t* pages, const int32_t* seqs, int64_t n, void* stream) try {
-  const char* fn = "dsa_cache_free";
-  const dsa::CallScope scope(fn);
-  dsa::PageTableView t;
-  dsa_status_t st = table_view(fn, pages, &t);
-  if (st != DSA_OK) return st;
-  if (n < 0 || n > kIntMax) return fail(DSA_ERR_INVALID_ARG, "%s: n=%lld out of range", fn, (long long)n);
-  if (n == 0) return DSA_OK;
-  if (!seqs || !aligned4(seqs)) return fail(DSA_ERR_INVALID_ARG, "%s: seqs must be a 4-byte aligned device array", fn);
-  dsa::LaunchCtx ctx;
-  st = make_ctx(stream, &ctx);
-  if (st != DSA_OK) return st;
-  dsa::call_param("n", n);
-  dsa::call_variant("a block per sequence");
-  cudaError_t e = timed_launch("cache_free", ctx.stream, [&] {
-    return dsa::launch_cache_free(t, log2_of(pages->page_size), static_cast<int>(pages->num_pages), seqs,
-                                  static_cast<int>(n), ctx);
-  });
-  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_free: launch");
-  return DSA_OK;
-} catch (...) {
-  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
-}
-
-dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
-                               int32_t* result, void* workspace, size_t ws_bytes, void* stream) try {
-  const char* fn = "dsa_cache_compact";
+template <typename Cache>
+dsa_status_t compact_pages(const char* fn, const Cache* caches, int layers, const dsa_page_table_t* pages,
+                           int32_t* result, void* workspace, size_t ws_bytes, void* stream) try {
   const dsa::CallScope scope(fn);
   std::vector<dsa::CacheView> views;
   dsa::PageTableView t;
@@ -1590,28 +1567,19 @@ dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* caches, int layers, cons
   if (e == cudaSuccess)
     e = timed_launch("compact_apply", ctx.stream, [&] {
       return by_layers(views, [&](const dsa::CacheSet& set, bool first) {
-        return dsa::launch_compact_apply(set, first, t, ws, ctx);
+        return dsa::launch_compact_apply(set, in_four(caches), first, t, ws, ctx);
       });
     }, layer_launches(views));
-  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_compact: launch");
+  if (e != cudaSuccess) return launch_fail(fn, e);
   return DSA_OK;
 } catch (...) {
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size) {
-  if (rows < 1 || max_pages < 1 || !page_size_ok(page_size) || max_pages > kIntMax / page_size) return 0;
-  const int64_t ld = paged_score_ld(max_pages, page_size);
-  int64_t r = kPagedScratch / ld;
-  r = r < kPagedMinRows ? kPagedMinRows : r;
-  r = r < rows ? r : rows;
-  return round_up(paged_scratch_bytes(r, ld), 256);
-}
-
-dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
-                                  const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,
-                                  size_t ws_bytes, void* stream) try {
-  const char* fn = "dsa_paged_index_topk";
+template <typename Cache>
+dsa_status_t paged_index(const char* fn, const Cache* cache, const dsa_paged_batch_t* batch, const void* q_idx,
+                         const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,
+                         size_t ws_bytes, void* stream) try {
   const dsa::CallScope scope(fn);
   dsa::CacheView c;
   dsa::BatchView b;
@@ -1687,21 +1655,21 @@ dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_page
       e = timed_launch("paged_scores", ctx.stream, [&] {
         return dsa::launch_paged_scores(c, b, q_idx, w, Hi, r, n, rule, scores, tops, ld, tc, ctx);
       });
-    if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: scores launch");
+    if (e != cudaSuccess) return launch_fail(fn, e);
     e = timed_launch("paged_select", ctx.stream, [&] {
       return dsa::launch_paged_select(b, c.shift, r, n, scores, tops, ld, topk, pool_idx, ctx);
     });
-    if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_index_topk: selection launch");
+    if (e != cudaSuccess) return launch_fail(fn, e);
   }
   return DSA_OK;
 } catch (...) {
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
 }
 
-dsa_status_t dsa_paged_sparse_attn_fwd(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q,
-                                       const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o,
-                                       float* lse, void* stream) try {
-  const char* fn = "dsa_paged_sparse_attn_fwd";
+template <typename Cache>
+dsa_status_t paged_attn(const char* fn, const Cache* cache, const dsa_paged_batch_t* batch, const void* q,
+                        const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o, float* lse,
+                        void* stream) try {
   const dsa::CallScope scope(fn);
   dsa::CacheView c;
   dsa::BatchView b;
@@ -1720,11 +1688,319 @@ dsa_status_t dsa_paged_sparse_attn_fwd(const dsa_paged_cache_t* cache, const dsa
   dsa::call_param("rows", b.rows);
   dsa::call_param("batch", b.batch);
   dsa::call_param("topk", topk);
-  dsa::call_variant("a cluster per row: cp.async gather through the block table, mma.sync, online softmax");
-  cudaError_t e = timed_launch("paged_attn", ctx.stream, [&] {
-    return dsa::launch_paged_attn(c, b, q, pool_idx, topk, scale, o, lse, ctx);
+  constexpr bool kFour = in_four(static_cast<const Cache*>(nullptr));
+  dsa::call_variant(kFour ? "a cluster per row: cp.async gather of 4-bit pools through the block table, codes to fp16 in "
+                            "registers, mma.sync, online softmax"
+                          : "a cluster per row: cp.async gather through the block table, mma.sync, online softmax");
+  cudaError_t e = timed_launch(kFour ? "paged4_attn" : "paged_attn", ctx.stream, [&] {
+    return kFour ? dsa::launch_paged4_attn(c, b, q, pool_idx, topk, scale, o, lse, ctx)
+                 : dsa::launch_paged_attn(c, b, q, pool_idx, topk, scale, o, lse, ctx);
   });
-  if (e != cudaSuccess) return cuda_fail(e, "dsa_paged_sparse_attn_fwd: launch");
+  if (e != cudaSuccess) return launch_fail(fn, e);
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+// A rotation that a call was given (null: none).
+dsa_status_t rope_view(const char* fn, const dsa_rope_t* r, int D, dsa::RopeView* out) {
+  *out = dsa::RopeView{nullptr, 0, 0, 0, 0};
+  if (!r) return DSA_OK;
+  if (!r->cos_sin || !aligned16(r->cos_sin))
+    return fail(DSA_ERR_INVALID_ARG, "%s: cos_sin must be a 16-byte aligned device array", fn);
+  if (r->dims < 16 || r->dims > D || (r->dims & 15) != 0)
+    return fail(DSA_ERR_UNSUPPORTED, "%s: rotation of %d dimensions unsupported (a multiple of 16, at most %d)", fn,
+                r->dims, D);
+  if (r->positions < 1 || r->positions > kIntMax)
+    return fail(DSA_ERR_INVALID_ARG, "%s: %lld positions out of range (1..2^31 - 1)", fn, (long long)r->positions);
+  if (r->stride < r->dims || (r->stride & 3) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: cos_sin row stride of %lld elements (a multiple of 4, at least %d)", fn,
+                (long long)r->stride, r->dims);
+  *out = dsa::RopeView{r->cos_sin, r->positions, r->stride, r->dims, r->interleaved != 0};
+  return DSA_OK;
+}
+
+// Heads that are turned: null pointers, alignment, strides and the number of heads.
+dsa_status_t rope_heads(const char* fn, const char* name, const void* in, int64_t in_stride, const void* out,
+                        int64_t out_stride, int heads, int most, int D) {
+  if (heads < 0 || heads > most)
+    return fail(DSA_ERR_UNSUPPORTED, "%s: %d heads of %s unsupported (max %d)", fn, heads, name, most);
+  if (heads == 0) return DSA_OK;
+  if (!in || !out) return fail(DSA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!aligned16(in) || !aligned16(out))
+    return fail(DSA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  const int64_t least = static_cast<int64_t>(heads) * D;
+  if (in_stride < least || out_stride < least || ((in_stride | out_stride) & 7) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: row strides of %s must be multiples of 8 elements, at least a row", fn, name);
+  if (in == out && in_stride != out_stride)
+    return fail(DSA_ERR_INVALID_ARG, "%s: %s is turned in place with another stride", fn, name);
+  return DSA_OK;
+}
+
+template <typename Cache>
+dsa_status_t append_rope(const char* fn, const Cache* cache, const dsa_paged_batch_t* batch, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx, int64_t k_idx_stride,
+                         const dsa_rope_t* rope, const dsa_rope_t* rope_idx, const dsa_rope_queries_t* queries,
+                         const int32_t* reserved, void* stream) try {
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa::BatchView b;
+  dsa::RopeAppendArgs x;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st == DSA_OK) st = batch_view(fn, batch, cache->page_size, &b);
+  if (st == DSA_OK) st = rope_view(fn, rope, kD, &x.rope);
+  if (st == DSA_OK) st = rope_view(fn, rope_idx, kDi, &x.rope_idx);
+  if (st != DSA_OK) return st;
+  const dsa_rope_queries_t none = {};
+  const dsa_rope_queries_t& q = queries ? *queries : none;
+  if ((q.Hq != 0 && !rope) || (q.Hi != 0 && !rope_idx))
+    return fail(DSA_ERR_INVALID_ARG, "%s: queries without the rope that turns them", fn);
+  if (b.rows == 0) return DSA_OK;
+  st = check_rows(fn, k, k_stride, v, v_stride, k_idx, k_idx_stride, reserved);
+  if (st == DSA_OK) st = rope_heads(fn, "q", q.q, q.q_stride, q.q_out, q.q_out_stride, q.Hq, kMaxRopeHeads, kD);
+  if (st == DSA_OK)
+    st = rope_heads(fn, "q_idx", q.q_idx, q.q_idx_stride, q.q_idx_out, q.q_idx_out_stride, q.Hi, kMaxHi, kDi);
+  if (st != DSA_OK) return st;
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  x.a = dsa::AppendArgs{static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+                        static_cast<const __nv_bfloat16*>(k_idx), k_stride, v_stride, k_idx_stride, reserved};
+  x.q = dsa::QueryRows{static_cast<const __nv_bfloat16*>(q.q), static_cast<__nv_bfloat16*>(q.q_out), q.q_stride,
+                       q.q_out_stride, q.Hq};
+  x.qi = dsa::QueryRows{static_cast<const __nv_bfloat16*>(q.q_idx), static_cast<__nv_bfloat16*>(q.q_idx_out),
+                        q.q_idx_stride, q.q_idx_out_stride, q.Hi};
+  dsa::call_param("rows", b.rows);
+  dsa::call_param("batch", b.batch);
+  dsa::call_param("Hq", q.Hq);
+  dsa::call_param("Hi", q.Hi);
+  dsa::call_variant("warps of rows, and warps of a row's queries, in one launch");
+  const bool four = in_four(cache);
+  const cudaError_t e = timed_launch(four ? "cache4_append" : "cache_append_rope", ctx.stream,
+                                     [&] { return dsa::launch_append_rope(c, four, b, x, ctx); });
+  if (e != cudaSuccess) return launch_fail(fn, e);
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status_t dsa_cache_append(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                              int64_t k_idx_stride, void* stream) {
+  return append("dsa_cache_append", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, nullptr, stream);
+}
+
+dsa_status_t dsa_cache_append_reserved(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                                       int64_t k_idx_stride, const int32_t* reserved, void* stream) {
+  return append("dsa_cache_append_reserved", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, reserved,
+                stream);
+}
+
+size_t dsa_cache_workspace(int64_t num_pages, int max_seqs, int64_t n) {
+  if (num_pages < 1 || num_pages > kIntMax || max_seqs < 1 || max_seqs > kMaxTableSeqs || n < 0 || n > kIntMax) return 0;
+  // the fork's list holds one page per child
+  int64_t w = dsa::fork_ws_words(n, max_seqs);
+  const int64_t r = dsa::reserve_ws_words(max_seqs, static_cast<int>(num_pages));
+  const int64_t z = dsa::compact_ws_words(static_cast<int>(num_pages));
+  w = w > r ? w : r;
+  w = w > z ? w : z;
+  return round_up(static_cast<size_t>(w) * 4, 256);
+}
+
+dsa_status_t dsa_cache_reserve(const dsa_page_table_t* pages, const int32_t* add, int32_t* result, void* workspace,
+                               size_t ws_bytes, void* stream) try {
+  const char* fn = "dsa_cache_reserve";
+  const dsa::CallScope scope(fn);
+  dsa::PageTableView t;
+  dsa_status_t st = table_view(fn, pages, &t);
+  if (st != DSA_OK) return st;
+  if (!add || !result || !aligned4(add) || !aligned4(result))
+    return fail(DSA_ERR_INVALID_ARG, "%s: add and result must be 4-byte aligned device arrays", fn);
+  const int np = static_cast<int>(pages->num_pages);
+  st = check_ws(fn, workspace, ws_bytes, static_cast<size_t>(dsa::reserve_ws_words(t.max_seqs, np)) * 4);
+  if (st != DSA_OK) return st;
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("max_seqs", t.max_seqs);
+  dsa::call_param("num_pages", np);
+  dsa::call_variant("plan and take in one launch");
+  cudaError_t e = timed_launch("cache_reserve", ctx.stream, [&] {
+    return dsa::launch_cache_reserve(t, log2_of(pages->page_size), np, add, result, static_cast<int32_t*>(workspace),
+                                     ctx);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_reserve: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+dsa_status_t dsa_cache_free(const dsa_page_table_t* pages, const int32_t* seqs, int64_t n, void* stream) try {
+  const char* fn = "dsa_cache_free";
+  const dsa::CallScope scope(fn);
+  dsa::PageTableView t;
+  dsa_status_t st = table_view(fn, pages, &t);
+  if (st != DSA_OK) return st;
+  if (n < 0 || n > kIntMax) return fail(DSA_ERR_INVALID_ARG, "%s: n=%lld out of range", fn, (long long)n);
+  if (n == 0) return DSA_OK;
+  if (!seqs || !aligned4(seqs)) return fail(DSA_ERR_INVALID_ARG, "%s: seqs must be a 4-byte aligned device array", fn);
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("n", n);
+  dsa::call_variant("a block per sequence");
+  cudaError_t e = timed_launch("cache_free", ctx.stream, [&] {
+    return dsa::launch_cache_free(t, log2_of(pages->page_size), static_cast<int>(pages->num_pages), seqs,
+                                  static_cast<int>(n), ctx);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "dsa_cache_free: launch");
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+size_t dsa_paged_index_topk_workspace(int64_t rows, int max_pages, int page_size) {
+  if (rows < 1 || max_pages < 1 || !page_size_ok(page_size) || max_pages > kIntMax / page_size) return 0;
+  const int64_t ld = paged_score_ld(max_pages, page_size);
+  int64_t r = kPagedScratch / ld;
+  r = r < kPagedMinRows ? kPagedMinRows : r;
+  r = r < rows ? r : rows;
+  return round_up(paged_scratch_bytes(r, ld), 256);
+}
+
+dsa_status_t dsa_cache_copy_pages(const dsa_paged_cache_t* caches, int layers, const int32_t* src, const int32_t* dst,
+                                  int64_t n, void* stream) {
+  return copy_pages("dsa_cache_copy_pages", caches, layers, src, dst, n, stream);
+}
+dsa_status_t dsa_cache4_copy_pages(const dsa_paged_cache4_t* caches, int layers, const int32_t* src,
+                                   const int32_t* dst, int64_t n, void* stream) {
+  return copy_pages("dsa_cache4_copy_pages", caches, layers, src, dst, n, stream);
+}
+
+dsa_status_t dsa_cache_fork(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
+                            const int32_t* src, const int32_t* dst, int64_t n, int32_t* result, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  return fork_sequences("dsa_cache_fork", caches, layers, pages, src, dst, n, result, workspace, ws_bytes, stream);
+}
+dsa_status_t dsa_cache4_fork(const dsa_paged_cache4_t* caches, int layers, const dsa_page_table_t* pages,
+                             const int32_t* src, const int32_t* dst, int64_t n, int32_t* result, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  return fork_sequences("dsa_cache4_fork", caches, layers, pages, src, dst, n, result, workspace, ws_bytes, stream);
+}
+
+dsa_status_t dsa_cache_compact(const dsa_paged_cache_t* caches, int layers, const dsa_page_table_t* pages,
+                               int32_t* result, void* workspace, size_t ws_bytes, void* stream) {
+  return compact_pages("dsa_cache_compact", caches, layers, pages, result, workspace, ws_bytes, stream);
+}
+dsa_status_t dsa_cache4_compact(const dsa_paged_cache4_t* caches, int layers, const dsa_page_table_t* pages,
+                                int32_t* result, void* workspace, size_t ws_bytes, void* stream) {
+  return compact_pages("dsa_cache4_compact", caches, layers, pages, result, workspace, ws_bytes, stream);
+}
+
+dsa_status_t dsa_paged_index_topk(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
+                                  const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  return paged_index("dsa_paged_index_topk", cache, batch, q_idx, w, Hi, Di, topk, pool_idx, workspace, ws_bytes,
+                     stream);
+}
+dsa_status_t dsa_paged4_index_topk(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, const void* q_idx,
+                                   const float* w, int Hi, int Di, int topk, int32_t* pool_idx, void* workspace,
+                                   size_t ws_bytes, void* stream) {
+  return paged_index("dsa_paged4_index_topk", cache, batch, q_idx, w, Hi, Di, topk, pool_idx, workspace, ws_bytes,
+                     stream);
+}
+
+dsa_status_t dsa_paged_sparse_attn_fwd(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* q,
+                                       const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o,
+                                       float* lse, void* stream) {
+  return paged_attn("dsa_paged_sparse_attn_fwd", cache, batch, q, pool_idx, Hq, D, topk, scale, o, lse, stream);
+}
+dsa_status_t dsa_paged4_sparse_attn_fwd(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, const void* q,
+                                        const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o,
+                                        float* lse, void* stream) {
+  return paged_attn("dsa_paged4_sparse_attn_fwd", cache, batch, q, pool_idx, Hq, D, topk, scale, o, lse, stream);
+}
+
+dsa_status_t dsa_cache_append_rope(const dsa_paged_cache_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                                   int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                                   int64_t k_idx_stride, const dsa_rope_t* rope, const dsa_rope_t* rope_idx,
+                                   const dsa_rope_queries_t* queries, const int32_t* reserved, void* stream) {
+  return append_rope("dsa_cache_append_rope", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, rope,
+                     rope_idx, queries, reserved, stream);
+}
+dsa_status_t dsa_cache4_append(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                               int64_t k_idx_stride, const dsa_rope_t* rope, const dsa_rope_t* rope_idx,
+                               const dsa_rope_queries_t* queries, const int32_t* reserved, void* stream) {
+  return append_rope("dsa_cache4_append", cache, batch, k, k_stride, v, v_stride, k_idx, k_idx_stride, rope, rope_idx,
+                     queries, reserved, stream);
+}
+
+dsa_status_t dsa_cache4_read(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, void* k,
+                             int64_t k_stride, void* v, int64_t v_stride, void* stream) try {
+  const char* fn = "dsa_cache4_read";
+  const dsa::CallScope scope(fn);
+  dsa::CacheView c;
+  dsa::BatchView b;
+  dsa_status_t st = cache_view(fn, cache, &c);
+  if (st == DSA_OK) st = batch_view(fn, batch, cache->page_size, &b);
+  if (st != DSA_OK) return st;
+  if (b.rows == 0) return DSA_OK;
+  if (!k || !v) return fail(DSA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+  if (!aligned16(k) || !aligned16(v)) return fail(DSA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned", fn);
+  if (k_stride < kD || v_stride < kD || ((k_stride | v_stride) & 7) != 0)
+    return fail(DSA_ERR_INVALID_ARG, "%s: row strides must be multiples of 8 elements, at least a row", fn);
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("rows", b.rows);
+  dsa::call_param("batch", b.batch);
+  dsa::call_variant("a warp per row");
+  const cudaError_t e = timed_launch("cache4_read", ctx.stream, [&] {
+    return dsa::launch_cache4_read(c, b, k, k_stride, v, v_stride, ctx);
+  });
+  if (e != cudaSuccess) return launch_fail(fn, e);
+  return DSA_OK;
+} catch (...) {
+  return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary
+}
+
+dsa_status_t dsa_rope(const void* x, int64_t x_stride, int64_t rows, int heads, int D, const dsa_rope_t* rope,
+                      const int32_t* positions, int64_t q_begin, int inverse, void* out, int64_t out_stride,
+                      void* stream) try {
+  const char* fn = "dsa_rope";
+  const dsa::CallScope scope(fn);
+  if (!rope) return fail(DSA_ERR_INVALID_ARG, "%s: null rope", fn);
+  if (D != kD && D != kDi)
+    return fail(DSA_ERR_UNSUPPORTED, "%s: D=%d unsupported (kernels implement D=64 and D=128)", fn, D);
+  dsa::RopeView r;
+  dsa_status_t st = rope_view(fn, rope, D, &r);
+  if (st != DSA_OK) return st;
+  if (rows < 0 || rows > kIntMax) return fail(DSA_ERR_INVALID_ARG, "%s: rows=%lld out of range", fn, (long long)rows);
+  if (heads < 1) return fail(DSA_ERR_INVALID_ARG, "%s: heads=%d must be >= 1", fn, heads);
+  if (!positions && (q_begin < 0 || q_begin > r.positions - rows))
+    return fail(DSA_ERR_INVALID_ARG, "%s: positions %lld .. %lld are not the table's (it has %lld)", fn,
+                (long long)q_begin, (long long)(q_begin + rows - 1), (long long)r.positions);
+  if (!aligned4(positions)) return fail(DSA_ERR_INVALID_ARG, "%s: positions must be 4-byte aligned", fn);
+  if (rows == 0) return DSA_OK;
+  st = rope_heads(fn, "x", x, x_stride, out, out_stride, heads, kMaxRopeHeads, D);
+  if (st != DSA_OK) return st;
+  dsa::LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != DSA_OK) return st;
+  dsa::call_param("rows", rows);
+  dsa::call_param("heads", heads);
+  dsa::call_param("D", D);
+  dsa::call_variant(inverse ? "a warp per row, turned back" : "a warp per row");
+  const dsa::RopeArgs a{static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(out), x_stride, out_stride,
+                        rows, heads, D, positions, q_begin, inverse ? -1.f : 1.f};
+  const cudaError_t e = timed_launch("rope", ctx.stream, [&] { return dsa::launch_rope(r, a, ctx); });
+  if (e != cudaSuccess) return launch_fail(fn, e);
   return DSA_OK;
 } catch (...) {
   return DSA_ERR_INTERNAL;  // no exception (out of host memory) crosses the C boundary

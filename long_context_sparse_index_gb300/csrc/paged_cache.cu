@@ -4,7 +4,7 @@
 // A page holds `page` tokens of one layer: keys and values (256 B each),
 // indexer keys (128 B) and, for every complete pool of four tokens, the pooled
 // indexer key as a bf16 hi/lo pair (256 B): 704 B a token.  Pools never cross
-// a page.
+// a page.  With keys and values in 4 bits (kv4.cuh) it is 336 B a token.
 //
 // The pooled key is the one of the contiguous indexer:
 //   Khat_p = ((k0 + k1) + (k2 + k3)) * 0.25 in fp32, hi = bf16(Khat),
@@ -145,32 +145,45 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 11;
 constexpr int kCopyVecs = kCopyThreads * kCopyUnroll;
 
-__device__ __forceinline__ int page_vecs(const CacheView& c) { return 44 << c.shift; }  // 704 B a token
-__device__ __forceinline__ int page_slices(const CacheView& c) { return (page_vecs(c) + kCopyVecs - 1) / kCopyVecs; }
+// 16-byte vectors of a token: 704 B, or 336 B with keys and values in 4 bits
+__host__ __device__ constexpr int token_vecs(bool four) { return four ? 21 : 44; }
+template <bool kFour>
+__device__ __forceinline__ int page_vecs(const CacheView& c) { return token_vecs(kFour) << c.shift; }
+template <bool kFour>
+__device__ __forceinline__ int page_slices(const CacheView& c) { return (page_vecs<kFour>(c) + kCopyVecs - 1) / kCopyVecs; }
 
-// Vector x (0 .. 44 * page) of a page: keys, values, indexer keys, pooled keys.
+// Vector x of a page: keys, values (in 4 bits both at once, 144 B a token), indexer keys, pooled keys.
+template <bool kFour>
 __device__ __forceinline__ uint4* page_vec(const CacheView& c, int64_t page, int x) {
   const int n = 16 << c.shift;
-  if (x < n) return reinterpret_cast<uint4*>(c.k + page * c.k_stride) + x;
-  x -= n;
-  if (x < n) return reinterpret_cast<uint4*>(c.v + page * c.v_stride) + x;
-  x -= n;
+  if (kFour) {
+    const int m = 9 << c.shift;
+    if (x < m) return reinterpret_cast<uint4*>(c.k + page * c.k_stride) + x;
+    x -= m;
+  } else {
+    if (x < n) return reinterpret_cast<uint4*>(c.k + page * c.k_stride) + x;
+    x -= n;
+    if (x < n) return reinterpret_cast<uint4*>(c.v + page * c.v_stride) + x;
+    x -= n;
+  }
   if (x < n / 2) return reinterpret_cast<uint4*>(c.k_idx + page * c.kidx_stride) + x;
   return reinterpret_cast<uint4*>(c.khat + page * c.khat_stride) + (x - n / 2);
 }
 
 // Slice `sl` of page src to page dst, by a whole block; all loads first.
+template <bool kFour>
 __device__ __forceinline__ void copy_slice(const CacheView& c, int64_t src, int64_t dst, int sl) {
-  const int n = page_vecs(c), x0 = sl * kCopyVecs + threadIdx.x;
+  const int n = page_vecs<kFour>(c), x0 = sl * kCopyVecs + threadIdx.x;
   uint4 t[kCopyUnroll];
 #pragma unroll
   for (int u = 0; u < kCopyUnroll; ++u)
-    if (x0 + u * kCopyThreads < n) t[u] = *page_vec(c, src, x0 + u * kCopyThreads);
+    if (x0 + u * kCopyThreads < n) t[u] = *page_vec<kFour>(c, src, x0 + u * kCopyThreads);
 #pragma unroll
   for (int u = 0; u < kCopyUnroll; ++u)
-    if (x0 + u * kCopyThreads < n) *page_vec(c, dst, x0 + u * kCopyThreads) = t[u];
+    if (x0 + u * kCopyThreads < n) *page_vec<kFour>(c, dst, x0 + u * kCopyThreads) = t[u];
 }
 
+template <bool kFour>
 __global__ void __launch_bounds__(kCopyThreads)
     copy_pages_kernel(const __grid_constant__ CacheSet set, const int32_t* __restrict__ src,
                       const int32_t* __restrict__ dst, unsigned* status) {
@@ -181,7 +194,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (threadIdx.x == 0) record_status(status, kStatusInternal);
     return;
   }
-  copy_slice(c, s, d, blockIdx.y);
+  copy_slice<kFour>(c, s, d, blockIdx.y);
 }
 
 // ================================================================= planning
@@ -451,6 +464,7 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
 // slice of the last page; all parts of the first layer share the row and the
 // counts.  (No layer reads a row that the first one writes: a child's row was
 // free, and what has no tokens has no pages.)
+template <bool kFour>
 __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(const __grid_constant__ CacheSet set, bool first, const PageTableView t,
                       const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, int32_t* ws_,
@@ -480,9 +494,9 @@ __global__ void __launch_bounds__(kCopyThreads)
     to[x] = p;
   }
   if (first && blockIdx.y == 0 && threadIdx.x == 0) t.lens[d] = len;
-  if (part && static_cast<int>(blockIdx.y) < page_slices(c)) {
+  if (part && static_cast<int>(blockIdx.y) < page_slices<kFour>(c)) {
     const int old = from[full];
-    if (static_cast<unsigned>(old) < static_cast<unsigned>(c.num_pages)) copy_slice(c, old, fresh, blockIdx.y);
+    if (static_cast<unsigned>(old) < static_cast<unsigned>(c.num_pages)) copy_slice<kFour>(c, old, fresh, blockIdx.y);
     else if (threadIdx.x == 0) record_status(status, kStatusInternal);
   }
 }
@@ -578,6 +592,7 @@ __global__ void __cluster_dims__(kC, 1, 1) __launch_bounds__(kPlanThreads)
   plan_sync<kC>();  // no CTA leaves while another reads its shared memory
 }
 
+template <bool kFour>
 __global__ void __launch_bounds__(kCopyThreads)
     compact_apply_kernel(const __grid_constant__ CacheSet set, bool first, const PageTableView t, int32_t* ws_) {
   const CacheView& c = set.v[blockIdx.z];
@@ -586,11 +601,11 @@ __global__ void __launch_bounds__(kCopyThreads)
   pdl_wait();  // the plan is written
   const int used = ws.head[0], moved = ws.head[1];
   if (moved == 0) return;
-  const int slices = page_slices(c);
+  const int slices = page_slices<kFour>(c);
   for (int64_t x = blockIdx.x; x < static_cast<int64_t>(moved) * slices; x += gridDim.x) {
     const int m = static_cast<int>(x / slices), sl = static_cast<int>(x % slices);
     const int from = ws.high[m], to = ws.hole[m];
-    copy_slice(c, from, to, sl);
+    copy_slice<kFour>(c, from, to, sl);
     if (first && sl == 0 && threadIdx.x == 0) {
       t.count[to] = t.count[from];
       t.count[from] = 0;
@@ -610,7 +625,7 @@ __global__ void __launch_bounds__(kCopyThreads)
   }
 }
 
-int host_slices(int shift) { return ((44 << shift) + kCopyVecs - 1) / kCopyVecs; }
+int host_slices(bool four, int shift) { return ((token_vecs(four) << shift) + kCopyVecs - 1) / kCopyVecs; }
 
 }  // namespace
 
@@ -621,10 +636,11 @@ cudaError_t launch_cache_append(const CacheView& c, const BatchView& b, const Ap
   return cudaGetLastError();
 }
 
-cudaError_t launch_copy_pages(const CacheSet& set, const int32_t* src, const int32_t* dst, int64_t n,
+cudaError_t launch_copy_pages(const CacheSet& set, bool four, const int32_t* src, const int32_t* dst, int64_t n,
                               const LaunchCtx& ctx) {
-  copy_pages_kernel<<<dim3(static_cast<unsigned>(n), host_slices(set.v[0].shift), set.n), kCopyThreads, 0,
-                      ctx.stream>>>(set, src, dst, ctx.status);
+  const dim3 grid(static_cast<unsigned>(n), host_slices(four, set.v[0].shift), set.n);
+  if (four) copy_pages_kernel<true><<<grid, kCopyThreads, 0, ctx.stream>>>(set, src, dst, ctx.status);
+  else copy_pages_kernel<false><<<grid, kCopyThreads, 0, ctx.stream>>>(set, src, dst, ctx.status);
   return cudaGetLastError();
 }
 
@@ -652,16 +668,16 @@ cudaError_t launch_fork_plan(const PageTableView& t, int shift, int num_pages, c
   return cudaGetLastError();
 }
 
-cudaError_t launch_fork_apply(const CacheSet& set, bool first, const PageTableView& t, const int32_t* src,
+cudaError_t launch_fork_apply(const CacheSet& set, bool four, bool first, const PageTableView& t, const int32_t* src,
                               const int32_t* dst, int n, int32_t* ws, const LaunchCtx& ctx) {
   // parts of a child: one per slice of its last page, and enough that a thread
   // copies at most 4 entries of the row (8 parts at the most for long rows)
-  const int slices = host_slices(set.v[0].shift);
+  const int slices = host_slices(four, set.v[0].shift);
   const int by_row = first ? (t.max_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads) : 1;
   const int parts = slices > by_row ? slices : by_row < 8 ? by_row : 8;
   LaunchCtx early = ctx;
   early.pdl = first;  // (only the plan stands right before the first)
-  return launch_ex(early, fork_apply_kernel, dim3(n, parts, set.n), dim3(kCopyThreads), 0, set, first, t, src, dst, n,
+  return launch_ex(early, four ? fork_apply_kernel<true> : fork_apply_kernel<false>, dim3(n, parts, set.n), dim3(kCopyThreads), 0, set, first, t, src, dst, n,
                    ws, ctx.status);
 }
 
@@ -680,12 +696,12 @@ cudaError_t launch_compact_plan(const PageTableView& t, int num_pages, int32_t* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_compact_apply(const CacheSet& set, bool first, const PageTableView& t, int32_t* ws,
+cudaError_t launch_compact_apply(const CacheSet& set, bool four, bool first, const PageTableView& t, int32_t* ws,
                                  const LaunchCtx& ctx) {
   LaunchCtx early = ctx;
   early.pdl = first;  // (only the plan stands right before the first)
-  return launch_ex(early, compact_apply_kernel, dim3((ctx.num_sms * 16 + set.n - 1) / set.n, 1, set.n), dim3(kCopyThreads),
-                   0, set, first, t, ws);
+  return launch_ex(early, four ? compact_apply_kernel<true> : compact_apply_kernel<false>,
+                   dim3((ctx.num_sms * 16 + set.n - 1) / set.n, 1, set.n), dim3(kCopyThreads), 0, set, first, t, ws);
 }
 
 }  // namespace dsa

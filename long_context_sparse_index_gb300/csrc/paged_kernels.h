@@ -58,7 +58,8 @@ struct CacheSet {
 };
 
 cudaError_t launch_cache_append(const CacheView& c, const BatchView& b, const AppendArgs& a, const LaunchCtx& ctx);
-cudaError_t launch_copy_pages(const CacheSet& set, const int32_t* src, const int32_t* dst, int64_t n,
+// (four: caches whose keys and values are in 4 bits)
+cudaError_t launch_copy_pages(const CacheSet& set, bool four, const int32_t* src, const int32_t* dst, int64_t n,
                               const LaunchCtx& ctx);
 // Scratch words (int32) of the page operators below.
 int64_t fork_ws_words(int64_t n, int max_seqs);
@@ -70,13 +71,13 @@ cudaError_t launch_cache_reserve(const PageTableView& t, int shift, int num_page
 // also changes the table and the counts.
 cudaError_t launch_fork_plan(const PageTableView& t, int shift, int num_pages, const int32_t* src, const int32_t* dst,
                              int n, int32_t* result, int32_t* ws, const LaunchCtx& ctx);
-cudaError_t launch_fork_apply(const CacheSet& set, bool first, const PageTableView& t, const int32_t* src,
+cudaError_t launch_fork_apply(const CacheSet& set, bool four, bool first, const PageTableView& t, const int32_t* src,
                               const int32_t* dst, int n, int32_t* ws, const LaunchCtx& ctx);
 cudaError_t launch_cache_free(const PageTableView& t, int shift, int num_pages, const int32_t* seqs, int n,
                               const LaunchCtx& ctx);
 cudaError_t launch_compact_plan(const PageTableView& t, int num_pages, int32_t* result, int32_t* ws,
                                 const LaunchCtx& ctx);
-cudaError_t launch_compact_apply(const CacheSet& set, bool first, const PageTableView& t, int32_t* ws,
+cudaError_t launch_compact_apply(const CacheSet& set, bool four, bool first, const PageTableView& t, int32_t* ws,
                                  const LaunchCtx& ctx);
 
 // Which sequences' scores the kernel of 128-row tiles makes: those of at least

@@ -1,0 +1,289 @@
+// paged_rope.cu -- new tokens into a paged cache with their keys turned by their
+// positions on the way, into bf16 pages or into pages of 4 bits, and the step's
+// queries turned with them; and the rows of a 4-bit cache read back.
+//
+// What the cache holds is what would be appended had the caller turned the keys
+// before: k and k_idx turned in fp32 (correctly rounded, rope.cuh) and rounded to
+// bf16; the pooled key is the mean of the four turned bf16 keys; the 4-bit codes
+// are those of the turned bf16 key (kv4.cuh).
+//
+// One launch.  Warps of the first blocks append kRows rows each: 16 lanes hold
+// a row's key and 16 its value, 16 B a lane; 8 lanes hold an indexer key.  The
+// others turn a row's heads each, 4 KB for 16 heads of 128 or 32 of 64, all
+// loads before the first store.
+#include "kv4.cuh"
+#include "paged.cuh"
+#include "paged_rope_kernels.h"
+#include "rope.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kDi = 64;
+constexpr int kWarps = 4;
+
+// The pooled key's chunk of eight dimensions from the four tokens' chunks: hi
+// and lo of the fp32 mean.
+__device__ __forceinline__ void pooled(const uint4 (&four)[4], uint4* hi, uint4* lo) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float kh[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      float y[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) y[t] = z ? bf_hi((&four[t].x)[e]) : bf_lo((&four[t].x)[e]);
+      kh[z] = __fmul_rn(__fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3])), 0.25f);
+    }
+    const uint32_t h = pack_bf16(kh[0], kh[1]);
+    (&hi->x)[e] = h;
+    (&lo->x)[e] = pack_bf16(__fsub_rn(kh[0], bf_lo(h)), __fsub_rn(kh[1], bf_hi(h)));
+  }
+}
+
+// One row's key (lanes 0..15) and value (16..31), eight dimensions a lane, to
+// the places of token t of the pool at `pool`.  Neighbouring lanes hold a group.
+__device__ __forceinline__ void store4(uint8_t* pool, int t, const uint4& x, int lane, bool on) {
+  const int ch = lane & 15;
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = bf_lo((&x.x)[e]);
+    f[2 * e + 1] = bf_hi((&x.x)[e]);
+  }
+  float top = 0.f;
+  bool odd = false;  // an infinity or a NaN
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    odd |= !(fabsf(f[e]) < INFINITY);
+    top = fmaxf(top, fabsf(f[e]));
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const unsigned any = __ballot_sync(0xffffffffu, odd);
+  odd = (any >> (lane & 30)) & 3u;
+  const uint32_t bits = odd ? kScaleNan : scale4_of(top);
+  const uint32_t w = codes4(f, odd ? 0.f : scale4(bits));
+  if (!on) return;
+  const bool key = lane < 16;
+  *reinterpret_cast<uint32_t*>(pool + (key ? k4_code_at(t, 8 * ch) : v4_code_at(t, 8 * ch))) = w;
+  if ((ch & 1) == 0) pool[key ? k4_scale_at(t, ch / 2) : v4_scale_at(t, ch / 2)] = static_cast<uint8_t>(bits);
+}
+
+// Rows r0 .. r0 + kRows - 1 (of one warp).
+template <int kRows, bool kFour>
+__device__ __forceinline__ void append_rows(const CacheView& c, const BatchView& b, const RopeAppendArgs& x, int64_t r0,
+                                            int lane, unsigned* status) {
+  const AppendArgs& a = x.a;
+  // the rows' sequences: one walk over the offsets; lanes 8u .. 8u + 7 work out
+  // row r0 + u (of a single row: every lane)
+  const int mine = kRows == 4 ? lane >> 3 : 0;
+  const int64_t row = r0 + mine;
+  int page = -1, older = 0;  // older: how many of the pool's tokens come before the call's rows
+  int64_t pos = 0;
+  bool astray = a.reserved != nullptr && __ldg(a.reserved) < 0;
+  for (int j0 = 0; j0 < b.batch; j0 += 32) {
+    const int j = j0 + lane;
+    int c0 = 0, c1 = 0, len = 0;
+    if (j < b.batch) {
+      c0 = __ldg(b.cu + j);
+      c1 = __ldg(b.cu + j + 1);
+      len = __ldg(b.lens + j);
+      astray |= c0 < 0 || c1 < c0 || c1 > b.rows;
+    }
+    int src = -1;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const unsigned hit =
+          __ballot_sync(0xffffffffu, j < b.batch && c0 <= r0 + u && r0 + u < c1 && r0 + u < b.rows);
+      if (mine == u && hit != 0u) src = __ffs(hit) - 1;
+    }
+    const int64_t first = __shfl_sync(0xffffffffu, c0, src & 31), last = __shfl_sync(0xffffffffu, c1, src & 31);
+    const int64_t n = __shfl_sync(0xffffffffu, len, src & 31);
+    if (src >= 0) {
+      const int64_t before = row - first;
+      pos = n - last + row;
+      if (pos < before || n > (static_cast<int64_t>(b.max_pages) << c.shift) ||
+          (x.rope.dims != 0 && pos >= x.rope.positions) || (x.rope_idx.dims != 0 && pos >= x.rope_idx.positions)) {
+        record_status(status, kStatusInternal);
+      } else {
+        page = page_of(b, c.num_pages, j0 + src, static_cast<int>(pos >> c.shift), status);
+        older = static_cast<int>(before < 3 ? 3 - before : 0);
+      }
+    }
+  }
+  // Then no row's position is sure, and what it would overwrite may be a live
+  // token: nothing is written.  (Every warp has seen all offsets.)
+  if (__any_sync(0xffffffffu, astray)) {
+    if (lane == 0) record_status(status, kStatusInternal);
+    return;
+  }
+  const int off = static_cast<int>(pos & ((1 << c.shift) - 1));
+  // keys and values
+  const int half = lane >> 4, ch = lane & 15;
+  uint4 kv[kRows];
+  int pg[kRows];
+  int64_t ps[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    pg[u] = __shfl_sync(0xffffffffu, page, 8 * u);
+    ps[u] = __shfl_sync(0xffffffffu, pos, 8 * u);
+    kv[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (pg[u] >= 0) kv[u] = ld_row((half ? a.v + (r0 + u) * a.v_stride : a.k + (r0 + u) * a.k_stride) + 8 * ch);
+  }
+  // indexer keys: lanes 8u .. 8u + 7 row r0 + u.  Of a single row: token u of its
+  // pool, if the row completes it.
+  const int g = lane & 7, tok = lane >> 3;
+  const bool ends = page >= 0 && (off & 3) == 3;
+  const __nv_bfloat16* const idx = a.k_idx + 8 * g;
+  __nv_bfloat16* const pidx = c.k_idx + static_cast<int64_t>(page < 0 ? 0 : page) * c.kidx_stride + 8 * g;
+  const float* const ci = x.rope_idx.cs;
+  const int64_t si = x.rope_idx.stride;
+  uint4 hi, lo;
+  if (kRows == 4) {
+    uint4 own = make_uint4(0u, 0u, 0u, 0u);
+    if (page >= 0) own = ld_row(idx + row * a.kidx_stride);
+    own = turn_chunk(x.rope_idx, own, ci + pos * si, g, lane, page >= 0);
+    uint4 four[4];
+    four[3] = own;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {  // token t of the pool is this row less 3 - t
+      four[t] = make_uint4(0u, 0u, 0u, 0u);
+      const bool call = ends && t >= older;
+      if (call) four[t] = ld_row(idx + (row - 3 + t) * a.kidx_stride);
+      four[t] = turn_chunk(x.rope_idx, four[t], ci + (pos - 3 + t) * si, g, lane, call);
+      if (ends && t < older) four[t] = *reinterpret_cast<const uint4*>(pidx + (off - 3 + t) * kDi);
+    }
+    if (page >= 0) *reinterpret_cast<uint4*>(pidx + off * kDi) = own;
+    pooled(four, &hi, &lo);
+  } else {
+    const int t0 = off & 3;  // the row's place in its pool
+    const bool me = page >= 0 && tok == t0, call = me || (ends && tok >= older);
+    uint4 own = make_uint4(0u, 0u, 0u, 0u);
+    if (call) own = ld_row(idx + (row - t0 + tok) * a.kidx_stride);
+    own = turn_chunk(x.rope_idx, own, ci + (pos - t0 + tok) * si, g, lane, call);
+    if (ends && !call) own = *reinterpret_cast<const uint4*>(pidx + (off - 3 + tok) * kDi);
+    if (me) *reinterpret_cast<uint4*>(pidx + off * kDi) = own;
+    uint4 four[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (&four[t].x)[e] = __shfl_sync(0xffffffffu, (&own.x)[e], 8 * t + g);
+    pooled(four, &hi, &lo);
+  }
+  if (ends && (kRows == 4 || tok == 0)) {
+    uint4* to = reinterpret_cast<uint4*>(c.khat + static_cast<int64_t>(page) * c.khat_stride + (off >> 2) * (2 * kDi));
+    to[g] = hi;
+    to[8 + g] = lo;
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const uint4 y = turn_chunk(x.rope, kv[u], x.rope.cs + ps[u] * x.rope.stride, ch, lane, pg[u] >= 0 && half == 0);
+    if (half == 0) kv[u] = y;
+    const int of = static_cast<int>(ps[u] & ((1 << c.shift) - 1));
+    if (kFour) {
+      uint8_t* const pool =
+          reinterpret_cast<uint8_t*>(c.k + static_cast<int64_t>(pg[u] < 0 ? 0 : pg[u]) * c.k_stride) + (of >> 2) * kPool4Bytes;
+      store4(pool, of & 3, kv[u], lane, pg[u] >= 0);
+    } else if (pg[u] >= 0) {
+      __nv_bfloat16* dst = half ? c.v + pg[u] * c.v_stride : c.k + pg[u] * c.k_stride;
+      reinterpret_cast<uint4*>(dst + of * kD)[ch] = kv[u];
+    }
+  }
+}
+
+// Row r of the queries (or of the indexer's), a warp's work.
+__device__ __forceinline__ void turn_queries(const BatchView& b, int shift, const RopeView& r, const QueryRows& q, int D,
+                                             int64_t row, const int32_t* reserved, int lane, unsigned* status) {
+  // (the append records a reservation that found too few pages)
+  if (reserved != nullptr && __ldg(reserved) < 0) return;
+  const RowAt at = warp_locate(b, shift, row, lane, status);
+  if (at.seq < 0 || at.pos < 0) return;
+  if (at.pos >= r.positions) {
+    if (lane == 0) record_status(status, kStatusInternal);
+    return;
+  }
+  const __nv_bfloat16* in = q.in + row * q.in_stride;
+  __nv_bfloat16* out = q.out + row * q.out_stride;
+  const float* cs = r.cs + at.pos * r.stride;
+  if (r.inter) turn_heads<true>(in, out, q.heads, D, r.dims, cs, 1.f, lane, 32);
+  else turn_heads<false>(in, out, q.heads, D, r.dims, cs, 1.f, lane, 32);
+}
+
+template <int kRows, bool kFour>
+__global__ void __launch_bounds__(32 * kWarps)
+    append_rope_kernel(const CacheView c, const BatchView b, const RopeAppendArgs x, unsigned append_blocks,
+                       unsigned* status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x < append_blocks) {
+    const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows;
+    if (r0 < b.rows) append_rows<kRows, kFour>(c, b, x, r0, lane, status);
+    return;
+  }
+  int64_t w = static_cast<int64_t>(blockIdx.x - append_blocks) * kWarps + warp;
+  if (x.q.heads > 0) {
+    if (w < b.rows) return turn_queries(b, c.shift, x.rope, x.q, kD, w, x.a.reserved, lane, status);
+    w -= b.rows;
+  }
+  if (x.qi.heads > 0 && w < b.rows)
+    turn_queries(b, c.shift, x.rope_idx, x.qi, kDi, w, x.a.reserved, lane, status);
+}
+
+// ----------------------------------------------------------------- reading back
+// A warp per row: 16 lanes its key and 16 its value, a word of codes each.
+__global__ void __launch_bounds__(32 * kWarps)
+    cache4_read_kernel(const CacheView c, const BatchView b, __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v,
+                       int64_t k_stride, int64_t v_stride, unsigned* status) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (row >= b.rows) return;
+  const RowAt at = warp_locate(b, c.shift, row, lane, status);
+  if (at.seq < 0 || at.pos < 0) return;
+  const int page = page_of(b, c.num_pages, at.seq, static_cast<int>(at.pos >> c.shift), lane == 0 ? status : nullptr);
+  if (page < 0) return;
+  const int off = static_cast<int>(at.pos & ((1 << c.shift) - 1)), t = off & 3, ch = lane & 15;
+  const uint8_t* pool = reinterpret_cast<const uint8_t*>(c.k + page * c.k_stride) + (off >> 2) * kPool4Bytes;
+  const bool key = lane < 16;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(pool + (key ? k4_code_at(t, 8 * ch) : v4_code_at(t, 8 * ch)));
+  const uint32_t bits = pool[key ? k4_scale_at(t, ch / 2) : v4_scale_at(t, ch / 2)];
+  const uint32_t s2 = bits * 0x00800080u;  // the scale twice, as fp16
+  const uint32_t y[4] = {mul_f16x2(f16_of_codes<0>(w), s2), mul_f16x2(f16_of_codes<1>(w), s2),
+                         mul_f16x2(f16_of_codes<2>(w), s2), mul_f16x2(f16_of_codes<3>(w), s2)};
+  uint4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
+    (&o.x)[e] = pack_bf16(f.x * 0.0625f, f.y * 0.0625f);
+  }
+  __nv_bfloat16* to = key ? k + row * k_stride : v + row * v_stride;
+  reinterpret_cast<uint4*>(to)[ch] = o;
+}
+
+template <int kRows, bool kFour>
+cudaError_t launch_append(const CacheView& c, const BatchView& b, const RopeAppendArgs& x, const LaunchCtx& ctx) {
+  const int64_t per = static_cast<int64_t>(kRows) * kWarps;
+  const int64_t ab = (b.rows + per - 1) / per;
+  const int64_t turns = b.rows * ((x.q.heads > 0) + (x.qi.heads > 0));
+  const int64_t blocks = ab + (turns + kWarps - 1) / kWarps;
+  append_rope_kernel<kRows, kFour><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(
+      c, b, x, static_cast<unsigned>(ab), ctx.status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_rope(const CacheView& c, bool four, const BatchView& b, const RopeAppendArgs& x,
+                               const LaunchCtx& ctx) {
+  if (b.rows <= 1024)
+    return four ? launch_append<1, true>(c, b, x, ctx) : launch_append<1, false>(c, b, x, ctx);
+  return four ? launch_append<4, true>(c, b, x, ctx) : launch_append<4, false>(c, b, x, ctx);
+}
+
+cudaError_t launch_cache4_read(const CacheView& c, const BatchView& b, void* k, int64_t k_stride, void* v,
+                               int64_t v_stride, const LaunchCtx& ctx) {
+  cache4_read_kernel<<<static_cast<unsigned>((b.rows + kWarps - 1) / kWarps), 32 * kWarps, 0, ctx.stream>>>(
+      c, b, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_stride, v_stride, ctx.status);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

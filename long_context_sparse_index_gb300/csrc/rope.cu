@@ -1,0 +1,48 @@
+// rope.cu -- heads turned by their position, on contiguous sequences: the
+// rotation before the layer's training calls, and its gradient (the rotation
+// back, for the matrix of a pair is orthogonal up to the table's scale: the
+// gradient multiplies by the transpose, which turns by -s).
+//
+// The arithmetic is in fp32 (products of a bf16 and an fp32 number, one FMA),
+// rounded once more to bf16.  Bound by memory: every element is read and
+// written once, and a row of the table serves all heads of its row.
+#include "rope.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kWarps = 8;
+
+// A warp takes `per` rows (one, or as many as have heads enough for its lanes).
+template <bool kInter>
+__global__ void __launch_bounds__(32 * kWarps)
+    rope_kernel(const RopeView r, const RopeArgs a, int per, int lanes, unsigned* status) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t row = w * per + lane / lanes;
+  if (row >= a.rows) return;
+  const int64_t pos = a.positions ? static_cast<int64_t>(__ldg(a.positions + row)) : a.begin + row;
+  if (pos < 0 || pos >= r.positions) {  // a position without an angle: the row is not written
+    record_status(status, kStatusInternal);
+    return;
+  }
+  turn_heads<kInter>(a.x + row * a.x_stride, a.out + row * a.out_stride, a.heads, a.D, r.dims, r.cs + pos * r.stride,
+                     a.dir, lane & (lanes - 1), lanes);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeView& r, const RopeArgs& a, const LaunchCtx& ctx) {
+  // lanes of a row: all of a warp, or fewer if its heads have less for them
+  int lanes = a.D / 8;
+  while (lanes < 32 && lanes < a.heads * (a.D / 8)) lanes *= 2;
+  const int per = 32 / lanes;
+  const int64_t blocks = (a.rows + static_cast<int64_t>(per) * kWarps - 1) / (static_cast<int64_t>(per) * kWarps);
+  if (r.inter)
+    rope_kernel<true><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, per, lanes, ctx.status);
+  else
+    rope_kernel<false><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, per, lanes, ctx.status);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa
