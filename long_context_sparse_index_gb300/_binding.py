@@ -126,6 +126,8 @@ def _configure(lib):
 def load():
     """Loads libdsa.so (built by __graft_entry__.build()); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -53,7 +53,7 @@ def _configure_rope(lib):
 
 
 def _heads_strided(t, name: str, device: int):
-    """[rows, heads, D] whose rows are contiguous; returns the distance between rows, which is free."""
+    """[rows, heads, D] whose rows are contiguous; returns rows, heads, D and the distance between rows, which is free."""
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.get_device() == device):
         _on_device(t, name, torch.bfloat16, 3)
     n, h, d = t.shape
@@ -61,7 +61,7 @@ def _heads_strided(t, name: str, device: int):
     if n > 0 and (step != 1 or (h > 1 and head != d)):
         raise ValueError(f"{name} must have contiguous rows of heads (got shape {tuple(t.shape)}, strides "
                          f"{t.stride()})")
-    return apart if n > 1 else h * d
+    return n, h, d, apart if n > 1 else h * d
 
 
 def _turned_out(given, name: str, like, device: int, stream):
@@ -69,7 +69,7 @@ def _turned_out(given, name: str, like, device: int, stream):
     if given is None:
         given = _new(like.shape, torch.bfloat16, like.device, stream)
         return given, like.shape[1] * like.shape[2]
-    apart = _heads_strided(given, name, device)
+    apart = _heads_strided(given, name, device)[3]
     _shape(given, name, like.shape)
     return given, apart
 
@@ -85,14 +85,19 @@ def dsa_rope(x, rope: Rope, positions=None, q_begin: int = 0, inverse: bool = Fa
                         out.unsqueeze(1) if isinstance(out, torch.Tensor) and out.dim() == 2 else out, stream)
         return out if out is not None else back.squeeze(1)
     dev = _device_of(rope)
-    apart = _heads_strided(x, "x", dev)
-    S, H, D = x.shape
+    S, H, D, apart = _heads_strided(x, "x", dev)
+    at = None
     if positions is not None:
         _full(positions, "positions", torch.int32, 1, dev)
-        _shape(positions, "positions", (S,))
-    out, out_apart = _turned_out(out, "out", x, dev, stream)
-    _check(load().dsa_rope(x.data_ptr(), apart, S, H, D, rope._ref, None if positions is None else positions.data_ptr(),
-                           q_begin, inverse, out.data_ptr(), out_apart, _handle(stream, dev)))
+        if positions.shape[0] != S:
+            _shape(positions, "positions", (S,))
+        at = positions.data_ptr()
+    if out is None:
+        out, out_apart = _new((S, H, D), torch.bfloat16, rope.device, stream), H * D
+    else:
+        out, out_apart = _turned_out(out, "out", x, dev, stream)
+    _check(load().dsa_rope(x.data_ptr(), apart, S, H, D, rope._ref, at, q_begin, inverse, out.data_ptr(), out_apart,
+                           _handle(stream, dev)))
     return out
 
 
@@ -118,46 +123,56 @@ def dsa_cache4_append(cache: PagedCache4, batch: PagedBatch, k, v, k_idx, rope: 
                    reserved, stream)
 
 
+def _rope_ref(r, name: str, dev: int):
+    if r is None:
+        return None
+    if not isinstance(r, Rope):
+        raise TypeError(f"{name} must be a Rope or None (got {type(r).__name__})")
+    if r.device_index != dev:
+        _device_of(r)
+    return r._ref
+
+
+def _queries(t, out, name: str, rows: int, d: int, dev: int, device, stream):
+    """(output, heads, [pointers and distances]) of queries to be turned."""
+    n, h, last, apart = _heads_strided(t, name, dev)
+    if n != rows or last != d:
+        _shape(t, name, (rows, h, d))
+    if out is None:
+        out, to = _new((n, h, d), torch.bfloat16, device, stream), h * d
+    else:
+        out, to = _turned_out(out, name + "_out", t, dev, stream)
+    return out, h, (t.data_ptr(), out.data_ptr(), apart, to)
+
+
+_NO_QUERIES = (None, None, 0, 0)
+
+
 def _append(call, cache, batch, k, v, k_idx, rope, rope_idx, q, q_idx, q_out, q_idx_out, reserved, stream):
     dev = _device_of(cache, batch)
-    for r, name in ((rope, "rope"), (rope_idx, "rope_idx")):
-        if r is not None and not (isinstance(r, Rope) and r.device_index == dev):
-            if not isinstance(r, Rope):
-                raise TypeError(f"{name} must be a Rope or None")
-            _device_of(r)
+    r, ri = _rope_ref(rope, "rope", dev), _rope_ref(rope_idx, "rope_idx", dev)
     ks = _rows_strided(k, "k", torch.bfloat16, 128, dev)
     vs = _rows_strided(v, "v", torch.bfloat16, 128, dev)
     kis = _rows_strided(k_idx, "k_idx", torch.bfloat16, 64, dev)
     rows = k.shape[0]
     if v.shape[0] != rows or k_idx.shape[0] != rows:
         raise ValueError(f"k, v and k_idx must have the same rows (got {rows}, {v.shape[0]} and {k_idx.shape[0]})")
-    queries, hq, hi = None, 0, 0
-    if q is not None or q_idx is not None:
-        args = [None, None, 0, 0, None, None, 0, 0]
-        if q is not None:
-            apart = _heads_strided(q, "q", dev)
-            if q.shape[0] != rows or q.shape[2] != 128:
-                _shape(q, "q", (rows, q.shape[1], 128))
-            q_out, to = _turned_out(q_out, "q_out", q, dev, stream)
-            hq = q.shape[1]
-            args[:4] = q.data_ptr(), q_out.data_ptr(), apart, to
-        if q_idx is not None:
-            apart = _heads_strided(q_idx, "q_idx", dev)
-            if q_idx.shape[0] != rows or q_idx.shape[2] != 64:
-                _shape(q_idx, "q_idx", (rows, q_idx.shape[1], 64))
-            q_idx_out, to = _turned_out(q_idx_out, "q_idx_out", q_idx, dev, stream)
-            hi = q_idx.shape[1]
-            args[4:] = q_idx.data_ptr(), q_idx_out.data_ptr(), apart, to
-        queries = ctypes.byref(_QueriesStruct(*args, hq, hi))
     if (q is None and q_out is not None) or (q_idx is None and q_idx_out is not None):
         raise ValueError("q_out and q_idx_out need q and q_idx")
+    queries = None
+    if q is not None or q_idx is not None:
+        hq, hi, of_q, of_qi = 0, 0, _NO_QUERIES, _NO_QUERIES
+        if q is not None:
+            q_out, hq, of_q = _queries(q, q_out, "q", rows, 128, dev, cache.device, stream)
+        if q_idx is not None:
+            q_idx_out, hi, of_qi = _queries(q_idx, q_idx_out, "q_idx", rows, 64, dev, cache.device, stream)
+        queries = ctypes.byref(_QueriesStruct(*of_q, *of_qi, hq, hi))
     if reserved is not None:
         _full(reserved, "reserved", torch.int32, 1, dev)
         _shape(reserved, "reserved", (1,))
         reserved = reserved.data_ptr()
-    _check(call(cache._ref, batch._with_rows(rows), k.data_ptr(), ks, v.data_ptr(), vs, k_idx.data_ptr(), kis,
-                None if rope is None else rope._ref, None if rope_idx is None else rope_idx._ref, queries, reserved,
-                _handle(stream, dev)))
+    _check(call(cache._ref, batch._with_rows(rows), k.data_ptr(), ks, v.data_ptr(), vs, k_idx.data_ptr(), kis, r, ri,
+                queries, reserved, _handle(stream, dev)))
     return q_out, q_idx_out
 
 
@@ -169,13 +184,16 @@ def dsa_cache4_read(cache: PagedCache4, batch: PagedBatch, rows: int, k=None, v=
     dev = _device_of(cache, batch)
     if rows < 0:
         raise ValueError(f"rows must be >= 0 (got {rows})")
-    out, apart = [], []
-    for t, name in ((k, "k"), (v, "v")):
-        if t is None:
-            t = _new((rows, 128), torch.bfloat16, cache.device, stream)
-        apart.append(_rows_strided(t, name, torch.bfloat16, 128, dev))
-        _shape(t, name, (rows, 128))
-        out.append(t)
-    _check(load().dsa_cache4_read(cache._ref, batch._with_rows(rows), out[0].data_ptr(), apart[0], out[1].data_ptr(),
-                                  apart[1], _handle(stream, dev)))
-    return out[0], out[1]
+    k, ks = _row_out(k, "k", rows, dev, cache.device, stream)
+    v, vs = _row_out(v, "v", rows, dev, cache.device, stream)
+    _check(load().dsa_cache4_read(cache._ref, batch._with_rows(rows), k.data_ptr(), ks, v.data_ptr(), vs,
+                                  _handle(stream, dev)))
+    return k, v
+
+
+def _row_out(t, name: str, rows: int, dev: int, device, stream):
+    if t is None:
+        return _new((rows, 128), torch.bfloat16, device, stream), 128
+    apart = _rows_strided(t, name, torch.bfloat16, 128, dev)
+    _shape(t, name, (rows, 128))
+    return t, apart

@@ -42,9 +42,9 @@ __device__ __forceinline__ void pooled(const uint4 (&four)[4], uint4* hi, uint4*
   }
 }
 
-// One row's key (lanes 0..15) and value (16..31), eight dimensions a lane, to
-// the places of token t of the pool at `pool`.  Neighbouring lanes hold a group.
-__device__ __forceinline__ void store4(uint8_t* pool, int t, const uint4& x, int lane, bool on) {
+// A row's key or value, eight dimensions a lane (16 lanes), to the places of
+// token t of the pool at `pool`.  Neighbouring lanes hold a group.
+__device__ __forceinline__ void store4(uint8_t* pool, int t, const uint4& x, int lane, bool key, bool on) {
   const int ch = lane & 15;
   float f[8];
 #pragma unroll
@@ -65,12 +65,25 @@ __device__ __forceinline__ void store4(uint8_t* pool, int t, const uint4& x, int
   const uint32_t bits = odd ? kScaleNan : scale4_of(top);
   const uint32_t w = codes4(f, odd ? 0.f : scale4(bits));
   if (!on) return;
-  const bool key = lane < 16;
   *reinterpret_cast<uint32_t*>(pool + (key ? k4_code_at(t, 8 * ch) : v4_code_at(t, 8 * ch))) = w;
   if ((ch & 1) == 0) pool[key ? k4_scale_at(t, ch / 2) : v4_scale_at(t, ch / 2)] = static_cast<uint8_t>(bits);
 }
 
-// Rows r0 .. r0 + kRows - 1 (of one warp).
+// A row's key or value into the cache.
+template <bool kFour>
+__device__ __forceinline__ void store_row(const CacheView& c, int page, int off, const uint4& x, int lane, bool key) {
+  if (kFour) {
+    uint8_t* const pool =
+        reinterpret_cast<uint8_t*>(c.k + static_cast<int64_t>(page < 0 ? 0 : page) * c.k_stride) + (off >> 2) * kPool4Bytes;
+    store4(pool, off & 3, x, lane, key, page >= 0);
+  } else if (page >= 0) {
+    __nv_bfloat16* dst = key ? c.k + page * c.k_stride : c.v + page * c.v_stride;
+    reinterpret_cast<uint4*>(dst + off * kD)[lane & 15] = x;
+  }
+}
+
+// Rows r0 .. r0 + kRows - 1 (of one warp).  Keys and values take 16 lanes each: a
+// row's key and value side by side, or two rows' keys and then two rows' values.
 template <int kRows, bool kFour>
 __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView& b, const RopeAppendArgs& x, int64_t r0,
                                             int lane, unsigned* status) {
@@ -79,6 +92,19 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView&
   // row r0 + u (of a single row: every lane)
   const int mine = kRows == 4 ? lane >> 3 : 0;
   const int64_t row = r0 + mine;
+  // The rows are asked for before their places are known.
+  constexpr int kP = kRows == 4 ? 2 : 1;  // passes
+  const int half = lane >> 4, ch = lane & 15, g = lane & 7, tok = lane >> 3;
+  const __nv_bfloat16* const idx = a.k_idx + 8 * g;
+  uint4 kx[kP], vx[kP], own = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int p = 0; p < kP; ++p) {
+    kx[p] = vx[p] = make_uint4(0u, 0u, 0u, 0u);
+    const int64_t r = r0 + (kRows == 4 ? 2 * p + half : 0);
+    if (kRows == 4 && r < b.rows) vx[p] = ld_row(a.v + r * a.v_stride + 8 * ch);
+    if (r < b.rows) kx[p] = ld_row((kRows == 1 && half ? a.v + r * a.v_stride : a.k + r * a.k_stride) + 8 * ch);
+  }
+  if (row < b.rows) own = ld_row(idx + row * a.kidx_stride);
   int page = -1, older = 0;  // older: how many of the pool's tokens come before the call's rows
   int64_t pos = 0;
   bool astray = a.reserved != nullptr && __ldg(a.reserved) < 0;
@@ -118,100 +144,102 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView&
     if (lane == 0) record_status(status, kStatusInternal);
     return;
   }
-  const int off = static_cast<int>(pos & ((1 << c.shift) - 1));
-  // keys and values
-  const int half = lane >> 4, ch = lane & 15;
-  uint4 kv[kRows];
-  int pg[kRows];
-  int64_t ps[kRows];
+  const int mask = (1 << c.shift) - 1;
+  const int off = static_cast<int>(pos & mask);
+  int pg[kP], of[kP];
+  RopeChunk kt[kP];
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    pg[u] = __shfl_sync(0xffffffffu, page, 8 * u);
-    ps[u] = __shfl_sync(0xffffffffu, pos, 8 * u);
-    kv[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (pg[u] >= 0) kv[u] = ld_row((half ? a.v + (r0 + u) * a.v_stride : a.k + (r0 + u) * a.k_stride) + 8 * ch);
+  for (int p = 0; p < kP; ++p) {
+    const int from = kRows == 4 ? 8 * (2 * p + half) : 0;
+    pg[p] = __shfl_sync(0xffffffffu, page, from);
+    const int64_t at = __shfl_sync(0xffffffffu, pos, from);
+    of[p] = static_cast<int>(at & mask);
+    kt[p] = rope_chunk(x.rope, x.rope.cs + at * x.rope.stride, ch, pg[p] >= 0 && (kRows == 4 || half == 0));
   }
-  // indexer keys: lanes 8u .. 8u + 7 row r0 + u.  Of a single row: token u of its
-  // pool, if the row completes it.
-  const int g = lane & 7, tok = lane >> 3;
-  const bool ends = page >= 0 && (off & 3) == 3;
-  const __nv_bfloat16* const idx = a.k_idx + 8 * g;
-  __nv_bfloat16* const pidx = c.k_idx + static_cast<int64_t>(page < 0 ? 0 : page) * c.kidx_stride + 8 * g;
+  // Indexer keys: lanes 8u .. 8u + 7 row r0 + u, and then, for each row that
+  // completes a pool, lanes 8t .. 8t + 7 the pool's token t.  (A single row's own
+  // lanes are those of its token.)
   const float* const ci = x.rope_idx.cs;
   const int64_t si = x.rope_idx.stride;
-  uint4 hi, lo;
+  const bool ends = page >= 0 && (off & 3) == 3;
   if (kRows == 4) {
-    uint4 own = make_uint4(0u, 0u, 0u, 0u);
-    if (page >= 0) own = ld_row(idx + row * a.kidx_stride);
-    own = turn_chunk(x.rope_idx, own, ci + pos * si, g, lane, page >= 0);
-    uint4 four[4];
-    four[3] = own;
+    own = turn_chunk(x.rope_idx, own, rope_chunk(x.rope_idx, ci + pos * si, g, page >= 0), g, lane, page >= 0);
+    if (page >= 0) *reinterpret_cast<uint4*>(c.k_idx + page * c.kidx_stride + off * kDi + 8 * g) = own;
+  }
+  unsigned todo = kRows == 4 ? __ballot_sync(0xffffffffu, ends && g == 0) : 1u;
+  while (todo != 0u) {
+    const int src = __ffs(todo) - 1;  // a lane of the row
+    todo &= todo - 1;
+    const int e_page = __shfl_sync(0xffffffffu, page, src), e_off = __shfl_sync(0xffffffffu, off, src);
+    const int e_older = __shfl_sync(0xffffffffu, older, src);
+    const int64_t e_pos = __shfl_sync(0xffffffffu, pos, src), e_row = r0 + (kRows == 4 ? src >> 3 : 0);
+    const bool whole = kRows == 4 || ends;
+    const int t0 = e_off & 3;  // the row's place in its pool
+    const bool me = e_page >= 0 && tok == t0, call = me || (whole && tok >= e_older);
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    __nv_bfloat16* const pidx = c.k_idx + static_cast<int64_t>(e_page < 0 ? 0 : e_page) * c.kidx_stride + 8 * g;
+    bool here = false;  // the warp's own rows have been turned
+    if (kRows == 4) {
+      const int in = (src >> 3) - 3 + tok;
+      here = call && in >= 0;
 #pragma unroll
-    for (int t = 0; t < 3; ++t) {  // token t of the pool is this row less 3 - t
-      four[t] = make_uint4(0u, 0u, 0u, 0u);
-      const bool call = ends && t >= older;
-      if (call) four[t] = ld_row(idx + (row - 3 + t) * a.kidx_stride);
-      four[t] = turn_chunk(x.rope_idx, four[t], ci + (pos - 3 + t) * si, g, lane, call);
-      if (ends && t < older) four[t] = *reinterpret_cast<const uint4*>(pidx + (off - 3 + t) * kDi);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = __shfl_sync(0xffffffffu, (&own.x)[e], 8 * (in & 3) + g);
+        if (here) (&y.x)[e] = w;
+      }
+    } else if (me) {
+      y = own;
     }
-    if (page >= 0) *reinterpret_cast<uint4*>(pidx + off * kDi) = own;
-    pooled(four, &hi, &lo);
-  } else {
-    const int t0 = off & 3;  // the row's place in its pool
-    const bool me = page >= 0 && tok == t0, call = me || (ends && tok >= older);
-    uint4 own = make_uint4(0u, 0u, 0u, 0u);
-    if (call) own = ld_row(idx + (row - t0 + tok) * a.kidx_stride);
-    own = turn_chunk(x.rope_idx, own, ci + (pos - t0 + tok) * si, g, lane, call);
-    if (ends && !call) own = *reinterpret_cast<const uint4*>(pidx + (off - 3 + tok) * kDi);
-    if (me) *reinterpret_cast<uint4*>(pidx + off * kDi) = own;
-    uint4 four[4];
+    const bool load = call && !here;
+    if (load && (kRows == 4 || !me)) y = ld_row(idx + (e_row - t0 + tok) * a.kidx_stride);
+    if (whole && !call) y = *reinterpret_cast<const uint4*>(pidx + (e_off - 3 + tok) * kDi);
+    if (__any_sync(0xffffffffu, load)) {
+      const uint4 z = turn_chunk(x.rope_idx, y, rope_chunk(x.rope_idx, ci + (e_pos - t0 + tok) * si, g, load), g, lane, load);
+      if (load) y = z;
+    }
+    if (kRows == 1 && me) *reinterpret_cast<uint4*>(pidx + e_off * kDi) = y;
+    if (kRows == 1 && !__any_sync(0xffffffffu, whole)) break;
+    uint4 four[4], hi, lo;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) (&four[t].x)[e] = __shfl_sync(0xffffffffu, (&own.x)[e], 8 * t + g);
+      for (int e = 0; e < 4; ++e) (&four[t].x)[e] = __shfl_sync(0xffffffffu, (&y.x)[e], 8 * t + g);
     pooled(four, &hi, &lo);
-  }
-  if (ends && (kRows == 4 || tok == 0)) {
-    uint4* to = reinterpret_cast<uint4*>(c.khat + static_cast<int64_t>(page) * c.khat_stride + (off >> 2) * (2 * kDi));
-    to[g] = hi;
-    to[8 + g] = lo;
+    uint4* to =
+        reinterpret_cast<uint4*>(c.khat + static_cast<int64_t>(e_page) * c.khat_stride + (e_off >> 2) * (2 * kDi)) + g;
+    if (tok == 0) to[0] = hi;
+    if (tok == 1) to[8] = lo;
   }
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    const uint4 y = turn_chunk(x.rope, kv[u], x.rope.cs + ps[u] * x.rope.stride, ch, lane, pg[u] >= 0 && half == 0);
-    if (half == 0) kv[u] = y;
-    const int of = static_cast<int>(ps[u] & ((1 << c.shift) - 1));
-    if (kFour) {
-      uint8_t* const pool =
-          reinterpret_cast<uint8_t*>(c.k + static_cast<int64_t>(pg[u] < 0 ? 0 : pg[u]) * c.k_stride) + (of >> 2) * kPool4Bytes;
-      store4(pool, of & 3, kv[u], lane, pg[u] >= 0);
-    } else if (pg[u] >= 0) {
-      __nv_bfloat16* dst = half ? c.v + pg[u] * c.v_stride : c.k + pg[u] * c.k_stride;
-      reinterpret_cast<uint4*>(dst + of * kD)[ch] = kv[u];
-    }
+  for (int p = 0; p < kP; ++p) {
+    const uint4 y = turn_chunk(x.rope, kx[p], kt[p], ch, lane, pg[p] >= 0 && (kRows == 4 || half == 0));
+    if (kRows == 4 || half == 0) kx[p] = y;
+    store_row<kFour>(c, pg[p], of[p], kx[p], lane, kRows == 4 || half == 0);
+    if (kRows == 4) store_row<kFour>(c, pg[p], of[p], vx[p], lane, false);
   }
 }
 
 // Row r of the queries (or of the indexer's), a warp's work.
 __device__ __forceinline__ void turn_queries(const BatchView& b, int shift, const RopeView& r, const QueryRows& q, int D,
                                              int64_t row, const int32_t* reserved, int lane, unsigned* status) {
-  // (the append records a reservation that found too few pages)
-  if (reserved != nullptr && __ldg(reserved) < 0) return;
-  const RowAt at = warp_locate(b, shift, row, lane, status);
-  if (at.seq < 0 || at.pos < 0) return;
-  if (at.pos >= r.positions) {
+  const auto find = [&]() -> const float* {
+    // (the append records a reservation that found too few pages)
+    if (reserved != nullptr && __ldg(reserved) < 0) return nullptr;
+    const RowAt at = warp_locate(b, shift, row, lane, status);
+    if (at.seq < 0 || at.pos < 0) return nullptr;
+    if (at.pos < r.positions) return r.cs + at.pos * r.stride;
     if (lane == 0) record_status(status, kStatusInternal);
-    return;
-  }
+    return nullptr;
+  };
   const __nv_bfloat16* in = q.in + row * q.in_stride;
   __nv_bfloat16* out = q.out + row * q.out_stride;
-  const float* cs = r.cs + at.pos * r.stride;
-  if (r.inter) turn_heads<true>(in, out, q.heads, D, r.dims, cs, 1.f, lane, 32);
-  else turn_heads<false>(in, out, q.heads, D, r.dims, cs, 1.f, lane, 32);
+  const int n = rope_chunk_lanes(r.dims, r.inter);
+  if (r.inter) turn_heads<true>(in, out, q.heads, D, r.dims, n, 1.f, lane, 32, find);
+  else turn_heads<false>(in, out, q.heads, D, r.dims, n, 1.f, lane, 32, find);
 }
 
 template <int kRows, bool kFour>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, 7)
     append_rope_kernel(const CacheView c, const BatchView b, const RopeAppendArgs x, unsigned append_blocks,
                        unsigned* status) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

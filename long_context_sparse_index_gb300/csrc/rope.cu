@@ -15,33 +15,35 @@ constexpr int kWarps = 8;
 
 // A warp takes `per` rows (one, or as many as have heads enough for its lanes).
 template <bool kInter>
-__global__ void __launch_bounds__(32 * kWarps)
-    rope_kernel(const RopeView r, const RopeArgs a, int per, int lanes, unsigned* status) {
+__global__ void __launch_bounds__(32 * kWarps, 4)
+    rope_kernel(const RopeView r, const RopeArgs a, int n, int per, int lanes, unsigned* status) {
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t row = w * per + lane / lanes;
   if (row >= a.rows) return;
-  const int64_t pos = a.positions ? static_cast<int64_t>(__ldg(a.positions + row)) : a.begin + row;
-  if (pos < 0 || pos >= r.positions) {  // a position without an angle: the row is not written
-    record_status(status, kStatusInternal);
-    return;
-  }
-  turn_heads<kInter>(a.x + row * a.x_stride, a.out + row * a.out_stride, a.heads, a.D, r.dims, r.cs + pos * r.stride,
-                     a.dir, lane & (lanes - 1), lanes);
+  const auto find = [&]() -> const float* {
+    const int64_t pos = a.positions ? static_cast<int64_t>(__ldg(a.positions + row)) : a.begin + row;
+    if (pos >= 0 && pos < r.positions) return r.cs + pos * r.stride;
+    record_status(status, kStatusInternal);  // a position without an angle: the row is not written
+    return nullptr;
+  };
+  turn_heads<kInter>(a.x + row * a.x_stride, a.out + row * a.out_stride, a.heads, a.D, r.dims, n, a.dir,
+                     lane & (lanes - 1), lanes, find);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeView& r, const RopeArgs& a, const LaunchCtx& ctx) {
   // lanes of a row: all of a warp, or fewer if its heads have less for them
-  int lanes = a.D / 8;
-  while (lanes < 32 && lanes < a.heads * (a.D / 8)) lanes *= 2;
+  const int n = rope_chunk_lanes(r.dims, r.inter);
+  int lanes = n;
+  while (lanes < 32 && lanes < a.heads * n) lanes *= 2;
   const int per = 32 / lanes;
   const int64_t blocks = (a.rows + static_cast<int64_t>(per) * kWarps - 1) / (static_cast<int64_t>(per) * kWarps);
   if (r.inter)
-    rope_kernel<true><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, per, lanes, ctx.status);
+    rope_kernel<true><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, n, per, lanes, ctx.status);
   else
-    rope_kernel<false><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, per, lanes, ctx.status);
+    rope_kernel<false><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, n, per, lanes, ctx.status);
   return cudaGetLastError();
 }
 

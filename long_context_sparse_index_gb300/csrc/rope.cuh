@@ -62,46 +62,74 @@ __device__ __forceinline__ uint4 turn_half(const uint4& x, const uint4& y, const
   return z;
 }
 
-// A head held by neighbouring lanes, chunk g (8 dimensions) in each: the chunk
-// turned by the table's row `cs` (a shared 16-byte aligned row of cosines and
-// sines).  Every lane of the warp calls it; `on`: the lane holds something.
-__device__ __forceinline__ uint4 turn_chunk(const RopeView& r, const uint4& x, const float* cs, int g, int lane, bool on) {
-  if (r.dims == 0) return x;
-  const float* sn = cs + r.dims / 2;
-  if (r.inter) {
-    if (!on || 8 * g >= r.dims) return x;
-    return turn_pairs<true>(x, __ldg(reinterpret_cast<const float4*>(cs) + g),
-                            __ldg(reinterpret_cast<const float4*>(sn) + g));
+// A head held by neighbouring lanes, chunk g (8 dimensions) in each: the cosines
+// and sines that the chunk needs of the table's row `cs`.
+struct RopeChunk {
+  float4 c[2], s[2];
+};
+__device__ __forceinline__ RopeChunk rope_chunk(const RopeView& r, const float* cs, int g, bool on) {
+  RopeChunk x = {};
+  if (!on || 8 * g >= r.dims) return x;  // (also where there is no rotation)
+  const int m = r.dims / 16, j = r.inter ? g : 2 * (g < m ? g : g - m);
+  const float4* c = reinterpret_cast<const float4*>(cs) + j;
+  const float4* s = reinterpret_cast<const float4*>(cs + r.dims / 2) + j;
+  x.c[0] = __ldg(c);
+  x.s[0] = __ldg(s);
+  if (!r.inter) {
+    x.c[1] = __ldg(c + 1);
+    x.s[1] = __ldg(s + 1);
   }
+  return x;
+}
+// The chunk turned.  Every lane of the warp calls it; `on`: the lane holds
+// something.
+__device__ __forceinline__ uint4 turn_chunk(const RopeView& r, const uint4& x, const RopeChunk& t, int g, int lane, bool on) {
+  if (r.dims == 0) return x;
+  if (r.inter) return !on || 8 * g >= r.dims ? x : turn_pairs<true>(x, t.c[0], t.s[0]);
   const int m = r.dims / 16;  // chunks of a half
   const int from = g < m ? lane + m : g < 2 * m ? lane - m : lane;
   uint4 y;
 #pragma unroll
   for (int e = 0; e < 4; ++e) (&y.x)[e] = __shfl_sync(0xffffffffu, (&x.x)[e], from);
   if (!on || g >= 2 * m) return x;
-  const int j = g < m ? g : g - m;
-  float4 c[2], s[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    c[e] = __ldg(reinterpret_cast<const float4*>(cs) + 2 * j + e);
-    s[e] = __ldg(reinterpret_cast<const float4*>(sn) + 2 * j + e);
-  }
-  return turn_half<true>(x, y, c, s, g < m ? -1.f : 1.f);
+  return turn_half<true>(x, y, t.c, t.s, g < m ? -1.f : 1.f);
 }
 
-__device__ __forceinline__ int pow2_at_least(int x) { return x <= 1 ? 1 : 1 << (32 - __clz(x - 1)); }
+// Lanes that a head's chunks take: a power of two.
+__host__ __device__ inline int rope_chunk_lanes(int dims, bool inter) {
+  const int chunks = inter ? dims / 8 : dims / 16;
+  int n = 1;
+  while (n < chunks) n *= 2;
+  return n;
+}
 
 // `heads` heads of D dimensions turned by one row of the table, by a group of
-// lanes: lane `lane` of `lanes` (a power of two, at least D / 8).  `in` and
-// `out` may be the same heads.
-template <bool kInter>
-__device__ __forceinline__ void turn_heads(const __nv_bfloat16* in, __nv_bfloat16* out, int heads, int D, int dims,
-                                           const float* cs, float dir, int lane, int lanes) {
-  constexpr int kU = 4;
-  const float* sn = cs + dims / 2;
+// lanes: lane `lane` of `lanes` (a power of two, at least n = rope_chunk_lanes).
+// `row()` says which row (null: none, and nothing is written); it is asked after
+// the first heads have been asked for, so that looking up a position costs no time
+// of its own.  `in` and `out` may be the same heads.
+template <bool kInter, typename Row>
+__device__ __forceinline__ void turn_heads(const __nv_bfloat16* in, __nv_bfloat16* out, int heads, int D, int dims, int n,
+                                           float dir, int lane, int lanes, Row&& row) {
+  constexpr int kU = kInter ? 4 : 2;  // heads under way: four 16-byte loads a lane
   const int chunks = kInter ? dims / 8 : dims / 16;  // what a head has for a lane each
-  const int n = pow2_at_least(chunks);
   const int j = lane & (n - 1), step = lanes / n;
+  uint4 x[kU], y[kU];
+  const auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int h = h0 + u * step;
+      if (h < heads && j < chunks) {
+        x[u] = *reinterpret_cast<const uint4*>(in + h * D + 8 * j);
+        if (!kInter) y[u] = *reinterpret_cast<const uint4*>(in + h * D + dims / 2 + 8 * j);
+      }
+    }
+  };
+  int h0 = lane / n;
+  load(h0);
+  const float* cs = row();
+  if (cs == nullptr) return;
+  const float* sn = cs + dims / 2;
   if (j < chunks) {
     constexpr int kV = kInter ? 1 : 2;
     float4 c[kV], s[kV];
@@ -109,37 +137,39 @@ __device__ __forceinline__ void turn_heads(const __nv_bfloat16* in, __nv_bfloat1
     for (int e = 0; e < kV; ++e) {
       c[e] = __ldg(reinterpret_cast<const float4*>(cs) + kV * j + e);
       s[e] = __ldg(reinterpret_cast<const float4*>(sn) + kV * j + e);
-      s[e] = make_float4(dir * s[e].x, dir * s[e].y, dir * s[e].z, dir * s[e].w);
     }
-    for (int h0 = lane / n; h0 < heads; h0 += kU * step) {
-      uint4 x[kU], y[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int h = h0 + u * step;
-        if (h < heads) {
-          x[u] = *reinterpret_cast<const uint4*>(in + h * D + 8 * j);
-          if (!kInter) y[u] = *reinterpret_cast<const uint4*>(in + h * D + dims / 2 + 8 * j);
-        }
-      }
+    while (h0 < heads) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int h = h0 + u * step;
         if (h >= heads) continue;
-        if (kInter) {
-          *reinterpret_cast<uint4*>(out + h * D + 8 * j) = turn_pairs<false>(x[u], c[0], s[0]);
-        } else if constexpr (!kInter) {
-          *reinterpret_cast<uint4*>(out + h * D + 8 * j) = turn_half<false>(x[u], y[u], c, s, -1.f);
-          *reinterpret_cast<uint4*>(out + h * D + dims / 2 + 8 * j) = turn_half<false>(y[u], x[u], c, s, 1.f);
+        if constexpr (kInter) {
+          const float4 t = make_float4(dir * s[0].x, dir * s[0].y, dir * s[0].z, dir * s[0].w);
+          *reinterpret_cast<uint4*>(out + h * D + 8 * j) = turn_pairs<false>(x[u], c[0], t);
+        } else {
+          *reinterpret_cast<uint4*>(out + h * D + 8 * j) = turn_half<false>(x[u], y[u], c, s, -dir);
+          *reinterpret_cast<uint4*>(out + h * D + dims / 2 + 8 * j) = turn_half<false>(y[u], x[u], c, s, dir);
         }
       }
+      h0 += kU * step;
+      load(h0);
     }
   }
   // the dimensions that are not turned
-  const int rest = (D - dims) / 8;
-  if (rest > 0 && in != out)
-    for (int e = lane; e < heads * rest; e += lanes) {
-      const int at = e / rest * D + dims + e % rest * 8;
-      *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(in + at);
+  const int rest = (D - dims) / 8, all = heads * rest;
+  if (all > 0 && in != out)
+    for (int e0 = lane; e0 < all; e0 += 4 * lanes) {
+      uint4 x[4];
+      int at[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + u * lanes;
+        at[u] = e / rest * D + dims + e % rest * 8;
+        if (e < all) x[u] = *reinterpret_cast<const uint4*>(in + at[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (e0 + u * lanes < all) *reinterpret_cast<uint4*>(out + at[u]) = x[u];
     }
 }
 
