@@ -123,6 +123,41 @@ def _configure(lib):
     return lib
 
 
+# The extension module that takes a call's common form (csrc/marshal.cpp): it
+# checks the tensors, allocates the outputs and calls the library, and declines
+# (None) whatever is out of the ordinary, which the Python code then does or refuses.
+marshal = None
+
+
+def _bind_marshal(lib):
+    global marshal
+    try:
+        from . import _marshal as module
+    except ImportError as e:
+        raise DsaError(DSA_ERR_CUDA, f"the extension module _marshal.so is not built ({e}); run "
+                                     "__graft_entry__.build()") from e
+    if module.torch_version != torch.__version__:
+        raise DsaError(DSA_ERR_CUDA, f"_marshal.so was built for torch {module.torch_version}, this is "
+                                     f"{torch.__version__}; run __graft_entry__.build()")
+    module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.dsa_rope, lib.dsa_cache_append_rope, lib.dsa_cache4_append, lib.dsa_cache4_read,
+        lib.dsa_paged4_sparse_attn_fwd)])
+    marshal = module
+
+
+def load_marshal():
+    """The extension module, bound to the library."""
+    load()
+    return marshal
+
+
+def outputs(done):
+    """What the extension module returned: the outputs, or the status of a call that failed."""
+    if done.__class__ is int:
+        _check(done)
+    return done
+
+
 def load():
     """Loads libdsa.so (built by __graft_entry__.build()); raises if it is missing."""
     global _lib
@@ -132,7 +167,9 @@ def load():
         if _lib is None:
             if not os.path.exists(LIB_PATH):
                 raise DsaError(DSA_ERR_CUDA, f"{LIB_PATH} is not built; run __graft_entry__.build()")
-            _lib = _configure(ctypes.CDLL(LIB_PATH))
+            lib = _configure(ctypes.CDLL(LIB_PATH))
+            _bind_marshal(lib)
+            _lib = lib
     return _lib
 
 

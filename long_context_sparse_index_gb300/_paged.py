@@ -13,6 +13,7 @@ import ctypes
 
 import torch
 
+from . import _binding
 from ._binding import _check, _need, _out, _shape, load
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -127,7 +128,7 @@ class PagedCache:
 
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_idx.data_ptr(), khat.data_ptr(), stride(k),
                                     stride(v), stride(k_idx), stride(khat), pages, page_size, 128, 64)
-        self._ref = ctypes.byref(self._struct)
+        self._ref, self._addr = ctypes.byref(self._struct), ctypes.addressof(self._struct)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, device="cuda"):
@@ -172,7 +173,7 @@ class PagedCache4:
 
         self._struct = _Cache4Struct(kv.data_ptr(), k_idx.data_ptr(), khat.data_ptr(), stride(kv), stride(k_idx),
                                      stride(khat), pages, page_size, 128, 64)
-        self._ref = ctypes.byref(self._struct)
+        self._ref, self._addr = ctypes.byref(self._struct), ctypes.addressof(self._struct)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, device="cuda"):
@@ -205,6 +206,8 @@ class PagedBatch:
         self._fields = (block_table.data_ptr(), block_table.stride(0) if block_table.shape[0] > 1 else self.max_pages,
                         seq_lens.data_ptr(), cu_q.data_ptr())
         self._last = (-1, None)
+        self._base = _BatchStruct(*self._fields, 0, self.max_pages, self.batch)  # of no rows; never written again
+        self._addr = ctypes.addressof(self._base)
         self._index_ws = (None, 0)
 
     def _index_workspace(self, rows: int, page_size: int) -> int:
@@ -477,6 +480,11 @@ def dsa_paged4_sparse_attn_fwd(cache: PagedCache4, batch: PagedBatch, q, pool_id
     """dsa_paged_sparse_attn_fwd over a cache in 4 bits: the attention over the
     keys and values that its codes stand for."""
     _is_cache(cache, True)
+    if o is None and lse is None and stream is None and batch.device_index == cache.device_index:
+        done = (_binding.marshal or _binding.load_marshal()).attention4(cache._addr, batch._addr, cache.device_index, q,
+                                                                        pool_idx, scale)
+        if done is not None:
+            return _binding.outputs(done)
     return _attention(load().dsa_paged4_sparse_attn_fwd, cache, batch, q, pool_idx, scale, o, lse, stream)
 
 

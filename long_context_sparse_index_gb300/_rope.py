@@ -7,9 +7,10 @@ import ctypes
 
 import torch
 
+from . import _binding
 from ._binding import _check, _shape, load
-from ._paged import (PagedBatch, PagedCache, PagedCache4, _device_of, _full, _handle, _is_cache, _new,
-                     _on_device, _rows_strided)
+from ._paged import (PagedBatch, PagedCache, PagedCache4, _device_of, _full, _handle, _is_cache, _new, _on_device,
+                     _rows_strided)
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 
@@ -40,7 +41,7 @@ class Rope:
         self.device, self.device_index = cos_sin.device, cos_sin.device.index
         self._struct = _RopeStruct(cos_sin.data_ptr(), self.positions,
                                    cos_sin.stride(0) if self.positions > 1 else self.dims, self.dims, self.interleaved)
-        self._ref = ctypes.byref(self._struct)
+        self._ref, self._addr = ctypes.byref(self._struct), ctypes.addressof(self._struct)
 
 
 def _configure_rope(lib):
@@ -84,6 +85,10 @@ def dsa_rope(x, rope: Rope, positions=None, q_begin: int = 0, inverse: bool = Fa
         back = dsa_rope(x.unsqueeze(1), rope, positions, q_begin, inverse,
                         out.unsqueeze(1) if isinstance(out, torch.Tensor) and out.dim() == 2 else out, stream)
         return out if out is not None else back.squeeze(1)
+    if out is None and stream is None and isinstance(rope, Rope):
+        done = (_binding.marshal or _binding.load_marshal()).rope(x, positions, rope._addr, rope.device_index, q_begin, inverse)
+        if done is not None:
+            return _binding.outputs(done)
     dev = _device_of(rope)
     S, H, D, apart = _heads_strided(x, "x", dev)
     at = None
@@ -149,6 +154,16 @@ _NO_QUERIES = (None, None, 0, 0)
 
 
 def _append(call, cache, batch, k, v, k_idx, rope, rope_idx, q, q_idx, q_out, q_idx_out, reserved, stream):
+    if q_out is None and q_idx_out is None and stream is None:
+        at = cache.device_index
+        r = 0 if rope is None else rope._addr if isinstance(rope, Rope) and rope.device_index == at else None
+        ri = 0 if rope_idx is None else \
+            rope_idx._addr if isinstance(rope_idx, Rope) and rope_idx.device_index == at else None
+        if r is not None and ri is not None and batch.device_index == at:
+            done = (_binding.marshal or _binding.load_marshal()).append(cache._four, cache._addr, batch._addr, at, k,
+                                                                        v, k_idx, r, ri, q, q_idx, reserved)
+            if done is not None:
+                return _binding.outputs(done)
     dev = _device_of(cache, batch)
     r, ri = _rope_ref(rope, "rope", dev), _rope_ref(rope_idx, "rope_idx", dev)
     ks = _rows_strided(k, "k", torch.bfloat16, 128, dev)
@@ -181,6 +196,10 @@ def dsa_cache4_read(cache: PagedCache4, batch: PagedBatch, rows: int, k=None, v=
     exactly what the codes stand for.  A batch whose cu_q counts all tokens reads
     whole sequences."""
     _is_cache(cache, True)
+    if k is None and v is None and stream is None and batch.device_index == cache.device_index:
+        done = (_binding.marshal or _binding.load_marshal()).read(cache._addr, batch._addr, cache.device_index, rows)
+        if done is not None:
+            return _binding.outputs(done)
     dev = _device_of(cache, batch)
     if rows < 0:
         raise ValueError(f"rows must be >= 0 (got {rows})")

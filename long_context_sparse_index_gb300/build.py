@@ -1,8 +1,10 @@
-"""Builds libdsa.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libdsa.so in-tree with nvcc for sm_103a (GB300), and the Python
+binding's extension module _marshal.so with the host compiler.
 
 Each CUDA translation unit under csrc/ is compiled in parallel to an object
 in _build/, then linked (static CUDA runtime) into libdsa.so next to this
-file.  Rebuilds only when a source or header is newer than the library.
+file.  Rebuilds only when a source or header is newer than the library (the
+extension module also when torch has changed).
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -32,6 +35,9 @@ LIB_STAMPS = os.path.join(HERE, "libdsa_stamps.so")
 # (DSA_DEBUG); the arithmetic and results are the default build's
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libdsa_debug.so")
+# the binding's short way into the library (csrc/marshal.cpp), for the torch it was built with
+MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE] + ARCH
@@ -57,6 +63,35 @@ def _stale(lib: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's extension module; returns its path."""
+    import torch
+    stamp = os.path.join(BUILD, "marshal.torch")
+    deps = [MARSHAL_SOURCE, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(MARSHAL) and os.path.exists(stamp):
+        with open(stamp) as f:
+            same = f.read() == torch.__version__
+        if same and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
+            return MARSHAL
+    os.makedirs(BUILD, exist_ok=True)
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f'-DDSA_TORCH_VERSION="{torch.__version__}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           "-I", sysconfig.get_paths()["include"], MARSHAL_SOURCE, "-o", tmp, "-L", os.path.join(root, "lib"),
+           *[f"-l{n}" for n in ("c10", "c10_cuda", "torch_cpu", "torch_cuda", "torch", "torch_python")]]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"marshal.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, trace: bool = False, debug: bool = False,
           stamps: bool = False) -> str:
     """Compile and link libdsa.so (or, with trace=True, the measurement
@@ -65,9 +100,12 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False, debug
     libdsa_debug.so); returns its path."""
     if trace + debug + stamps > 1:
         raise ValueError("build: the trace, stamps and debug variants are separate builds")
+    default = not (trace or stamps or debug)
     lib, bdir = (LIB_TRACE, BUILD_TRACE) if trace else (LIB_STAMPS, BUILD_STAMPS) if stamps else \
         (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
     if not force and not _stale(lib):
+        if default:
+            build_marshal()
         return lib
     os.makedirs(bdir, exist_ok=True)
     nvcc = _nvcc()
@@ -87,8 +125,11 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False, debug
         return obj
 
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        marshal = ex.submit(build_marshal, force) if default else None
         objs = list(ex.map(compile_one, srcs))
+        if marshal is not None:
+            marshal.result()
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs],
                        capture_output=True, text=True)

@@ -419,3 +419,59 @@ def test_calls_record_what_they_ran():
     assert c["entry"] == "dsa_paged4_sparse_attn_fwd" and c["kernels"] == [["paged4_attn", 1]]
     dsa.dsa_rope(bf16(2, HQ, D).to(DEV), dsa.Rope(f4.table(2, 64).to(DEV)))
     assert dsa.last_kernel_config()["kernels"] == [["rope", 1]]
+
+
+def test_short_and_long_way_of_a_call_agree():
+    """The extension module's way (outputs to allocate, the current stream) and the Python code's (a stream given): the
+    same bits for what the first takes, and for what it leaves to the second."""
+    here = torch.cuda.current_stream()
+    S, wide = 20, bf16(20, 4, 256, seed=1).to(DEV)
+    rope = dsa.Rope(f4.table(64, 64).to(DEV))
+    pos = i32(range(3, 23))
+    shapes = (wide[:, :, :128].contiguous(), wide[:, 1:2, 64:128], wide.view(20, 8, 128)[:, 2:5], wide[::2, 0, 128:],
+              wide[:, 0, ::2])
+    for x in shapes[:4]:
+        at = pos[:x.shape[0]].contiguous()
+        for kw in (dict(), dict(q_begin=9), dict(positions=at), dict(positions=at, inverse=True)):
+            a, b = dsa.dsa_rope(x, rope, **kw), dsa.dsa_rope(x, rope, stream=here, **kw)
+            assert same_bits(a, b) and a.shape == x.shape
+    with pytest.raises(ValueError):  # a row whose elements lie apart
+        dsa.dsa_rope(shapes[4], rope)
+    m = f4.Model4([1, 2, 5], [7, 30, 0], 16, seed=10)
+    new = gpu(m.fill(m.T, D), m.fill(m.T, D), m.fill(m.T, DI))
+    q, qi = bf16(m.T, HQ, D).to(DEV), bf16(m.T, 3, DI).to(DEV)
+    idx = dsa.Rope(f4.table(64, 32).to(DEV), interleaved=True)
+    sel = torch.full((m.T, 4), -1, dtype=torch.int32, device=DEV)
+    for four, call in ((False, dsa.dsa_cache_append_rope), (True, dsa.dsa_cache4_append)):
+        for args in ((rope, idx, q, qi), (None, idx, None, qi), (rope, None, q, None), (None, None, None, None)):
+            got = []
+            for kw in (dict(), dict(stream=here), dict(reserved=i32([1])), dict(reserved=i32([1]), stream=here)):
+                cache, batch = m.to_gpu4(dsa) if four else m.to_gpu(dsa)
+                out = call(cache, batch, *new, *args, **kw)
+                got.append([t for t in out if t is not None] + ([cache.kv] if four else [cache.k, cache.v])
+                           + [cache.k_idx, cache.khat])
+                assert [t is None for t in out] == [t is None for t in args[2:]]
+                if four:
+                    got[-1] += dsa.dsa_cache4_read(cache, batch, m.T, stream=kw.get("stream"))
+                    got[-1] += dsa.dsa_paged4_sparse_attn_fwd(cache, batch, q, sel, 0.25, stream=kw.get("stream"))
+            for other in got[1:]:
+                for a, b in zip(got[0], other):
+                    assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    dsa.dsa_sync_status()
+
+
+def test_short_way_raises_what_the_library_refuses():
+    rope = dsa.Rope(f4.table(8, 64).to(DEV))
+    x = bf16(9, 2, 64).to(DEV)
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_rope(x, rope)  # nine positions of eight
+    assert e.value.status == dsa.DSA_ERR_INVALID_ARG and "dsa_rope" in str(e.value)
+    m = f4.Model4([2], [30], 16, seed=11)
+    cache, batch = m.to_gpu4(dsa)
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_paged4_sparse_attn_fwd(cache, batch, bf16(2, 8, 128).to(DEV), i32([0, 0]).view(2, 1))
+    assert e.value.status == dsa.DSA_ERR_UNSUPPORTED
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_rope(bf16(9, 2, 64).to(DEV), rope, q_begin=1)
+    assert torch.cuda.memory_allocated() == before  # the outputs of a refused call are given back
