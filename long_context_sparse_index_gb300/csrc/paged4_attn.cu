@@ -15,18 +15,37 @@
 // P is rounded to fp16 for its product with V (2^-12 of each weight; the
 // normaliser sums the unrounded weights), and o once at the end.
 //
-// Layout of the work: a cluster of C CTAs (1 to 6) of four warps per row.  CTA c
-// takes the row's blocks of 16 pools c, c + C, ...; each warp gathers the 576
-// bytes of its own 4 pools of a block by 16-byte cp.async copies into its quarter
-// of a ring of kStages blocks, and waits only for its own copies.  Nothing is
-// unpacked in shared memory: a lane's codes of a fragment are neighbours (32
-// dimensions of a key, 16 dimensions of two tokens' values), so it reads 16 bytes
-// at a time and converts in registers.  The order of dimensions in a sum is free,
-// so Q's fragments take the keys' order; tokens 0, 1 and 2, 3 of the upper two
-// pools change places, which keeps the reads of V free of bank conflicts.  The
-// warps' partial softmax states (m, l, O) are merged through shared memory, the
-// CTAs' through distributed shared memory, always in the same order: no atomics,
-// no workspace, one launch, the same bits on every run.
+// Layout of the work: a cluster of C CTAs (1 to 8) of four warps per row.  CTA c
+// takes the row's blocks of 16 pools c, c + C, ..., and each warp its own slice of
+// four pools of each; it gathers their 576 bytes each by 16-byte cp.async copies
+// into its part of a ring of kStages blocks, waits only for its own copies, and
+// takes two slices (32 keys) a step.  Nothing is unpacked in shared memory: a lane's
+// codes of a fragment are neighbours (32 dimensions of a key, 16 dimensions of two
+// tokens' values), so it reads 16 bytes at a time and converts in registers.  The
+// order of dimensions in a sum is free, so Q's fragments take the keys' order;
+// tokens 0, 1 and 2, 3 of the upper two pools change places, which keeps the reads
+// of V free of bank conflicts.  A head's reference is looked at by a vote and moves
+// only when a product is above it by 2^8, so most steps rescale nothing.  The warps'
+// partial softmax states (m, l, O) are merged through shared memory; the CTAs hand
+// theirs to the one that finishes a part of the row, so nothing is read from
+// another CTA.  Always in the same order: no atomics, no workspace, one launch, the
+// same bits on every run.
+//
+// Measured with 512 pools a row, launches in a graph, keys and values from HBM:
+//   1 row       7.2 us, latency: selection, page, pool (three dependent reads,
+//               0.8 us each), 16 keys a warp at about 0.45 us, the merge.
+//   64 rows     14.0 us: 19 MB, 1.4 TB/s.
+//   512 rows    46 us.
+//   4096 rows   262 us: 262 TFLOP/s, and 4.6 TB/s of pools from L2.  A slice of 16
+//               keys takes 146 clocks of an SM, of which the 32 products have the
+//               tensor pipe for 65; the conversions (64), the scales' products (64)
+//               and the pairing of tokens (16) go to pipes that take an instruction
+//               every two clocks, and the product's issue and theirs overlap by
+//               half only (measured: products' clocks + half of the others').
+//               More warps an SM (12 or 16), more registers, one or two slices a
+//               step or another order of the instructions moved it by 1 % at most.
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "paged.cuh"
 #include "paged_rope_kernels.h"
@@ -42,7 +61,8 @@ constexpr int kBlkPools = 16;
 constexpr int kWarpPools = kBlkPools / kWarps;             // 4 pools of each block per warp
 constexpr uint32_t kWarpStage = kWarpPools * kPool4Bytes;  // 2304 B
 constexpr uint32_t kStageBytes = kWarps * kWarpStage;      // 9 KB: one block
-constexpr int kMaxSplit = 6;  // CTAs of a row's cluster
+constexpr int kMaxSplit = 8;  // CTAs of a row's cluster
+constexpr int kVecs = kHq * kD / 4;  // a row's output in vectors of four
 // The merge slabs, a row of 16 per head: four runs of 32 columns, 36 floats apart,
 // so that a quarter warp's 16-byte stores reach all banks.
 constexpr int kRunLd = 36;
@@ -67,6 +87,17 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_st_f32(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_st_f32x4(uint32_t a, const float4& v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -119,12 +150,11 @@ __device__ __forceinline__ void key_frag(uint32_t w, uint32_t s, uint32_t& b0, u
   b1 = mul_f16x2(f16_of_codes<2 * kHalf + 1>(w), s);
 }
 
-// Gathers the 4 pools of warp w into `st`.  `at`: the block's pools as byte
-// offsets (-1: nothing there, zero-filled).  Eight lanes a pool.
-__device__ __forceinline__ void gather_warp(uint32_t st, const uint8_t* kv, const int64_t* at, int w, int lane,
-                                            bool any_hole) {
+// Gathers the four pools of a slice into `st`.  `at`: the pools as byte offsets
+// (-1: nothing there, zero-filled).  Eight lanes a pool.
+__device__ __forceinline__ void gather_slice(uint32_t st, const uint8_t* kv, const int64_t* at, int lane, bool any_hole) {
   const int p = lane >> 3, c8 = lane & 7;
-  const int64_t off = at[w * kWarpPools + p];
+  const int64_t off = at[p];
   const uint8_t* src = kv + off + c8 * 16;
   const uint32_t dst = st + p * kPool4Bytes + c8 * 16;
   if (!any_hole) {
@@ -174,7 +204,9 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
   int64_t* pools = reinterpret_cast<int64_t*>(gbase + kStages * kStageBytes);
   __shared__ int s_nsel;
   __shared__ float s_m[kWarps][kHq], s_l[kWarps][kHq];
-  __shared__ float s_cm[kHq], s_cl[kHq];  // this CTA's merged reference and normaliser
+  // what the cluster's CTAs hand to this one: references, normalisers, partial O
+  __shared__ float s_pm[kSplit ? kMaxSplit : 1][kHq], s_pl[kSplit ? kMaxSplit : 1][kHq];
+  __shared__ float4 s_po[kSplit ? kVecs + kMaxSplit : 1];
   __shared__ uint4 s_q[8 * 32];           // Q's fragments, a step's for each lane
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -183,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
   const int rank = kSplit ? static_cast<int>(cluster_rank()) : 0;
   const int64_t r = kSplit ? blockIdx.x / static_cast<unsigned>(split) : blockIdx.x;
 
+  if (kSplit) cluster_arrive();  // (this CTA runs: the others may write to its shared memory)
   pdl_wait();  // launched early: what stands before in the stream has ended
   // ---- everything that depends on the row's number alone is asked for at
   // once: Q, the selection, the offsets and lengths
@@ -205,7 +238,10 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
   const RowAt at = warp_locate(b, c.shift, r, lane, warp == 0 ? status : nullptr);
   // padding behind the last sequence, or a row without a position: every CTA of
   // the cluster leaves here
-  if (at.seq < 0 || at.pos < 0) return;
+  if (at.seq < 0 || at.pos < 0) {
+    if (kSplit) cluster_wait();
+    return;
+  }
   const int64_t i = at.pos;
   const int64_t n_elig = i >> 2;
   // selected pools: the leading non-negative entries
@@ -232,51 +268,73 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
   // is none, are recorded; nothing is read for them.
   bool bad = false;
   const int pshift = c.shift - 2;  // log2(pools per page)
-  for (int e = tid; e < nblk * kBlkPools; e += kThreads) {
+  const auto pool_of = [&](int e) -> int64_t {  // -1: none
     const int slot = (rank + e / kBlkPools * kC) * kBlkPools + e % kBlkPools;
-    int64_t pool = -1, off = slot <= nsel ? -1 : 0;  // (what an empty slot reads is masked)
-    if (slot < nsel) {
-      const int p = __ldg(prow + slot);
-      if (p < n_elig) pool = p;
-      else bad = true;
-      if (slot > 0 && p <= __ldg(prow + slot - 1)) bad = true;
-    } else if (slot == nsel) {
-      pool = n_elig;
-    }
+    if (slot >= nsel) return slot == nsel ? n_elig : -1;
+    const int p = __ldg(prow + slot);
+    if (slot > 0 && p <= __ldg(prow + slot - 1)) bad = true;
+    if (p < n_elig) return p;
+    bad = true;
+    return -1;
+  };
+  const auto page_at = [&](int64_t pool) { return pool < 0 ? 0 : __ldg(b.table + at.seq * b.table_stride + (pool >> pshift)); };
+  const auto put = [&](int e, int64_t pool, int page) {
+    const bool empty = (rank + e / kBlkPools * kC) * kBlkPools + e % kBlkPools > nsel;
+    int64_t off = empty ? 0 : -1;  // (what an empty slot reads is masked)
     if (pool >= 0) {
-      const int page = __ldg(b.table + at.seq * b.table_stride + (pool >> pshift));
       if (static_cast<unsigned>(page) < static_cast<unsigned>(c.num_pages))
         off = page * (2 * c.k_stride) + (pool & ((1 << pshift) - 1)) * kPool4Bytes;
       else bad = true;
     }
     pools[e] = off;
-  }
-  if (bad) record_status(status, kStatusInternal);
-
-  // ---- the gather pipeline's prologue
-  // the pools are visible; without holes only the row's last block (its own pool
-  // and the empty slots after it) needs a mask
-  const bool any_hole = __syncthreads_or(bad) != 0;
-  const uint8_t* kv = reinterpret_cast<const uint8_t*>(c.k);
-#pragma unroll
-  for (int s = 0; s < kStages - 2; ++s) {
-    if (s < mine) gather_warp(sKV + s * kStageBytes + warp * kWarpStage, kv, pools + s * kBlkPools, warp, lane, any_hole);
-    cp_async_commit();
-  }
-
+  };
   // Q's fragments in the keys' order: step kk takes, of each lane's 32 dimensions,
   // 4 kk .. 4 kk + 3.  All warps have the same ones; each stores two steps'.
-  float f0, f1;  // what a head's products are to be multiplied by (log2 units)
+  float f0 = 0.f, f1 = 0.f;  // what a head's products are to be multiplied by (log2 units)
   const uint32_t sQ = smem_u32(s_q) + 16 * lane;
-  {
+  const auto ready_q = [&] {
     uint32_t x0[16], x1[16];
     f0 = fmaxf(scale_log2 * kUnit * query_f16(q0, x0), 1.17549435e-38f);
     f1 = fmaxf(scale_log2 * kUnit * query_f16(q1, x1), 1.17549435e-38f);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
       if (kk >> 1 == warp) st_shared_v4(sQ + 512 * kk, x0[2 * kk], x1[2 * kk], x0[2 * kk + 1], x1[2 * kk + 1]);
+  };
+  const int entries = nblk * kBlkPools;
+  int e0 = tid;
+  if (kSplit) {  // few entries: Q is made ready while a thread's first page number comes
+    const int64_t pool = tid < entries ? pool_of(tid) : -1;
+    const int page = page_at(pool);
+    ready_q();
+    if (tid < entries) put(tid, pool, page);
+    e0 += kThreads;
   }
-  __syncthreads();
+#pragma unroll 4
+  for (int e = e0; e < entries; e += kThreads) {
+    const int64_t pool = pool_of(e);
+    put(e, pool, page_at(pool));
+  }
+  if (bad) record_status(status, kStatusInternal);
+
+  // ---- the gather pipeline's prologue
+  // the pools are visible; without holes only the row's last block (its own
+  // pool and the empty slots after it) needs a mask
+  const bool any_hole = __syncthreads_or(bad) != 0;
+  const uint8_t* kv = reinterpret_cast<const uint8_t*>(c.k);
+  const int64_t* const my_pools = pools + warp * kWarpPools;
+  const uint32_t ring = sKV + warp * kWarpStage;
+  // (a split row has few slices, and all of them under way at once; a whole row
+  // keeps the pace of its refills: 4096 rows 265 us with a full ring, 261 so)
+  constexpr int kFirst = kSplit ? kStages : kStages - 2;
+#pragma unroll
+  for (int u = 0; u < kFirst; ++u) {
+    if (u < mine) gather_slice(ring + u * kStageBytes, kv, my_pools + u * kBlkPools, lane, any_hole);
+    cp_async_commit();
+  }
+  if (!kSplit) {  // many: while the first slices come
+    ready_q();
+    __syncthreads();
+  }
 
   float o_acc[16][4];
 #pragma unroll
@@ -297,27 +355,16 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
   const uint32_t k_up = 128u * up, v_up = 16u * (t4 >> 1);
   const int k_rot = 16 * up, v_rot = 16 * (t4 >> 1);
 
-  int stage = 0;
-  for (int l = 0; l < mine; l += 2) {
-    cp_async_wait<kStages - 4>();  // this lane's copies of slices l and l + 1
-    __syncwarp();                  // ... and the other lanes'; slices l - 2 and l - 1 have been read
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int ahead = l + u + kStages - 2;
-      const int st = stage + u < 2 ? stage + u + kStages - 2 : stage + u - 2;
-      if (ahead < mine) gather_warp(sKV + st * kStageBytes + warp * kWarpStage, kv, pools + ahead * kBlkPools, warp, lane, any_hole);
-      cp_async_commit();
-    }
-    const uint32_t sW = sKV + stage * kStageBytes + warp * kWarpStage;
-    stage = stage + 2 == kStages ? 0 : stage + 2;
-
-    // S = Q K^T for the 32 keys of two slices (four n-tiles of 8)
-    float s[4][4];
+  // One step: slices l .. l + kN - 1 of this warp, at sW.
+  const auto step = [&](auto count, int l, uint32_t sW) {
+    constexpr int kN = decltype(count)::value;
+    // S = Q K^T for 16 keys of each slice (two n-tiles of 8)
+    float s[2 * kN][4];
     {
-      uint4 kw[4];
-      uint32_t sc[4][2];
+      uint4 kw[2 * kN];
+      uint32_t sc[2 * kN][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kN; ++u) {
         const uint32_t at = sW + u * kStageBytes;
         kw[2 * u] = lds128(at + k_at + k_up);
         kw[2 * u + 1] = lds128(at + k_at + (128u - k_up));
@@ -334,32 +381,32 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t qa[4] = {qv[e].x, qv[e].y, qv[e].z, qv[e].w};
-          uint32_t b[4][2];
+          uint32_t b[2 * kN][2];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
+          for (int n = 0; n < 2 * kN; ++n) {
             if (e == 0) key_frag<0>((&kw[n].x)[h], sc[n][h >> 1], b[n][0], b[n][1]);
             else key_frag<1>((&kw[n].x)[h], sc[n][h >> 1], b[n][0], b[n][1]);
           }
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
+          for (int n = 0; n < 2 * kN; ++n) {
             if (h + e == 0) mma_f16_16816_first(s[n], qa, b[n][0], b[n][1]);
             else mma_f16_16816(s[n], qa, b[n][0], b[n][1]);
           }
         }
       }
     }
-    uint32_t vs[2];  // scales of the first n-tile's two tokens, then the second's
+    uint32_t vs[kN];  // scales of the first n-tile's two tokens, then the second's
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kN; ++u) {
       vs[u] = lds32(sW + u * kStageBytes + vs_at);
       vs[u] = __funnelshift_r(vs[u], vs[u], v_rot);
     }
-    if (l + 2 >= mine || any_hole) {  // the own pool, or a slice that is not there
+    if (l + kN >= mine || any_hole) {  // the own pool, or a slice that is not there
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kN; ++u) {
         const int in = warp * kWarpPools + t4;
         const int slot = (rank + (l + u) * kC) * kBlkPools + in;
-        const int have = l + u >= mine || slot > nsel || pools[(l + u) * kBlkPools + in] < 0 ? 0
+        const int have = slot > nsel || pools[(l + u) * kBlkPools + in] < 0 ? 0
                          : slot == nsel ? static_cast<int>(i & 3) + 1
                                         : 4;
         const int ta = 2 * (t4 >> 1);
@@ -380,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
     for (int hh = 0; hh < 2; ++hh) {
       mx[hh] = fmaxf(s[0][2 * hh], s[0][2 * hh + 1]);
 #pragma unroll
-      for (int n = 1; n < 4; ++n) mx[hh] = fmaxf(mx[hh], fmaxf(s[n][2 * hh], s[n][2 * hh + 1]));
+      for (int n = 1; n < 2 * kN; ++n) mx[hh] = fmaxf(mx[hh], fmaxf(s[n][2 * hh], s[n][2 * hh + 1]));
     }
     if (__any_sync(0xffffffffu, mx[0] > rise[0] || mx[1] > rise[1])) {
       float al[2];
@@ -408,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
         o_acc[j][3] *= al[1];
       }
     }
-    uint32_t pa[2][4];
+    uint32_t pa[kN][4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 2 * kN; ++n)
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         float2 p = fma2(s[n][2 * hh], s[n][2 * hh + 1], hh ? f1 : f0, minus_m[hh]);
@@ -423,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
     // pairs the pool's tokens.  Two tokens' codes of a dimension become
     // neighbours, four dimensions at a time.
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kN; ++u) {
       const uint32_t at = sW + u * kStageBytes;
       const uint4 va = lds128(at + v_at + v_up), vb = lds128(at + v_at + (16u - v_up));
       const uint32_t sa = __byte_perm(vs[u], 0u, 0x4140) << 7, sb = __byte_perm(vs[u], 0u, 0x4342) << 7;
@@ -443,12 +490,32 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
         mma_f16_16816(o_acc[8 * w + 7], pa[u], mul_f16x2(f16_of_codes<3>(oa), sa), mul_f16x2(f16_of_codes<3>(ob), sb));
       }
     }
+  };
+  int stage = 0;
+  for (int l = 0; l < mine; l += 2) {
+    if (l == 0) cp_async_wait<kFirst - 2>();  // this lane's copies of slices l and l + 1
+    else cp_async_wait<kStages - 4>();
+    __syncwarp();  // ... and the other lanes'; slices l - 2 and l - 1 have been read
+    if (!kSplit || l != 0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int ahead = l + u + kStages - 2;
+        const int st = stage + u < 2 ? stage + u + kStages - 2 : stage + u - 2;
+        if (ahead < mine) gather_slice(ring + st * kStageBytes, kv, my_pools + ahead * kBlkPools, lane, any_hole);
+        cp_async_commit();
+      }
+    }
+    const uint32_t sW = ring + stage * kStageBytes;
+    stage = stage + 2 == kStages ? 0 : stage + 2;
+    if (!kSplit || l + 1 < mine) step(std::integral_constant<int, 2>{}, l, sW);
+    else step(std::integral_constant<int, 1>{}, l, sW);  // (a whole row masks its last odd slice)
   }
   cp_async_wait<0>();
   const float m_run[2] = {rise[0] == -INFINITY ? -INFINITY : -minus_m[0], rise[1] == -INFINITY ? -INFINITY : -minus_m[1]};
 
-  // ---- merge the four warps' partial states into the CTA's (unnormalised,
-  // at the CTA's reference M)
+  // ---- merge the four warps' partial states into the CTA's (unnormalised, at
+  // the CTA's reference M)
+  if (kSplit) cluster_wait();  // every CTA of the cluster runs
   float l_sum[2] = {l_run[0].x + l_run[0].y, l_run[1].x + l_run[1].y};
 #pragma unroll
   for (int off = 1; off <= 2; off <<= 1) {
@@ -475,16 +542,13 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
     for (int w = 0; w < kWarps; ++w) L += s_l[w][h] * exp2f(s_m[w][h] - Mu);
     fac[hh] = exp2f(m_run[hh] - Mu);
     if (!kSplit) fac[hh] *= kUnit / L;
-    if (warp == 0 && t4 == 0) {
-      if (!kSplit) {
-        lse[r * kHq + h] = (M + log2f(L)) * kLn2;
-      } else {
-        s_cm[h] = M;
-        s_cl[h] = L;
-      }
+    if (!kSplit && warp == 0 && t4 == 0) lse[r * kHq + h] = (M + log2f(L)) * kLn2;
+    if (kSplit && warp + kWarps * t4 < kC) {  // a lane tells a CTA
+      cluster_st_f32(cluster_map(smem_u32(&s_pm[rank][h]), warp + kWarps * t4), M);
+      cluster_st_f32(cluster_map(smem_u32(&s_pl[rank][h]), warp + kWarps * t4), L);
     }
   }
-  float* red = reinterpret_cast<float*>(gbase);  // four slabs over the ring
+  float* red = reinterpret_cast<float*>(gbase);  // the warps' slabs over the ring
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -496,10 +560,12 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
     }
   __syncthreads();
   __nv_bfloat16* orow = o + r * (kHq * kD);
-  // the CTA's O, four columns a thread at a time
+  // the CTA's O, four columns a thread at a time: written, or handed to the CTA of
+  // the cluster that finishes this part of the row
+  const int per = kSplit ? (kVecs + kC - 1) / kC : kVecs;
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int e = 4 * (tid + kThreads * m);
+  for (int m = 0; m < kVecs / kThreads; ++m) {
+    const int v = tid + kThreads * m, e = 4 * v;
     const int from = (e / kD) * kRedLd + slab_col(e % kD);
     float4 y = *reinterpret_cast<const float4*>(red + from);
 #pragma unroll
@@ -510,48 +576,36 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
       y.z += z.z;
       y.w += z.w;
     }
-    if (kSplit) *reinterpret_cast<float4*>(red + from) = y;
+    if (kSplit) cluster_st_f32x4(cluster_map(smem_u32(&s_po[rank * per + v % per]), v / per), y);
     else *reinterpret_cast<uint2*>(orow + e) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
   }
   if (kSplit) {
-    // then every CTA of the cluster finishes its share of the 2048 outputs from
-    // the C slabs
-    cluster_sync();
-    for (int u4 = rank * kThreads + tid; u4 < kHq * kD / 4; u4 += kC * kThreads) {
-      const int e = 4 * u4, h = e / kD, col = e % kD;
-      float cm[kMaxSplit], cl[kMaxSplit];
-      float4 y[kMaxSplit];
-#pragma unroll
-      for (int u = 0; u < kMaxSplit; ++u) {
-        cm[u] = -INFINITY;
-        cl[u] = 0.f;
-        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (u < kC) {
-          cm[u] = cluster_ld_f32(cluster_map(smem_u32(&s_cm[h]), u));
-          cl[u] = cluster_ld_f32(cluster_map(smem_u32(&s_cl[h]), u));
-          y[u] = cluster_ld_f32x4(cluster_map(smem_u32(red + h * kRedLd + slab_col(col)), u));
-        }
-      }
-      float M = cm[0];
-#pragma unroll
-      for (int u = 1; u < kMaxSplit; ++u) M = fmaxf(M, cm[u]);
-      float L = 0.f;
+    cluster_sync();  // everything has been handed over; nothing is read from another CTA
+    for (int x = tid; x < per && rank * per + x < kVecs; x += kThreads) {
+      const int e = 4 * (rank * per + x), h = e / kD, col = e % kD;
+      float cm[kMaxSplit], M = -INFINITY, L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < kMaxSplit; ++u) {
+        cm[u] = u < kC ? s_pm[u][h] : -INFINITY;
+        M = fmaxf(M, cm[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kMaxSplit; ++u) {
+        if (u >= kC) continue;
         const float f = exp2f(cm[u] - M);  // every row has a key of its own: M is finite
-        L += cl[u] * f;
-        acc.x += y[u].x * f;
-        acc.y += y[u].y * f;
-        acc.z += y[u].z * f;
-        acc.w += y[u].w * f;
+        const float4 y = s_po[u * per + x];
+        L += s_pl[u][h] * f;
+        acc.x += y.x * f;
+        acc.y += y.y * f;
+        acc.z += y.z * f;
+        acc.w += y.w * f;
       }
       const float inv = kUnit / L;
       *reinterpret_cast<uint2*>(orow + e) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
       if (col == 0) lse[r * kHq + h] = (M + log2f(L)) * kLn2;
     }
-    cluster_sync();  // no CTA leaves while another reads its shared memory
   }
 }
 
@@ -567,8 +621,6 @@ template <int kStages, bool kSplit>
 cudaError_t allow_smem() {
   constexpr size_t kMost =
       128 + static_cast<size_t>(kStages) * kStageBytes + static_cast<size_t>(kBlocksOf[1]) * kBlkPools * sizeof(int64_t);
-  // (4800: the static part; 1024: the system's)
-  static_assert(kMost + 4800 + 1024 <= 228 * 1024 / 3, "three CTAs an SM at the longest rows");
   static std::atomic<bool> attr_done[kAttrDevices];
   return set_smem_limit_once(paged4_attn_kernel<kStages, kSplit>, static_cast<int>(kMost), attr_done);
 }
@@ -624,19 +676,22 @@ cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q
 // The CTAs of a row.  A split shortens a row's chain of slices (76 ns each, four
 // warps side by side) and costs a merge across the cluster; CTAs that share an SM
 // slow one another down, and the rows' clusters have to be on the device at once
-// (the runtime says how many are: 74 of 6).  Measured, in us with 1 / 2 / 4 / 6 / 8
-// CTAs a row, keys and values from HBM:
-//   512 pools   1 row 17.6 / 13.3 / 9.5 / 8.2 / 8.1    20 rows 17.9 / 13.4 / 9.9 / 8.9 / 9.8
-//               40 rows 19.6 / 14.7 / 12.7 / 11.5 / 12.8    64 rows 19.8 / 15.1 / 13.9 / 15.1 / 22.1
-//               100 rows 19.9 / 18.6 / 17.5 / 24.8    114 rows 20.0 / 18.9 / 25.5    228 rows 26.4 / 25.4
-//   255 pools   4 rows 10.0 / 9.0 / 7.3 / 7.4 / 6.8    40 rows 10.5 / 9.5 / 8.7 / 9.3 / 9.4
-//               64 rows 11.6 / 10.4 / 9.9 / 11.5    130 rows 11.1 / 11.8
-//   128 pools   4 rows 7.5 / 7.9 / 7.0 / 6.5 / 6.6    28 rows 7.6 / 8.2 / 7.7 / 7.8    90 rows 7.8 / 9.8 / 9.7
+// (the runtime says how many are: 51 of 8, 74 of 6).  Measured, in us with 1 / 2 / 4 /
+// 6 / 8 CTAs a row, keys and values from HBM:
+//   512 pools   1 row 17.9 / 12.8 / 9.0 / 7.7 / 7.1    16 rows 18.0 / 13.1 / 9.3 / 8.0 / 8.8
+//               32 rows 19.7 / 14.4 / 10.5 / 10.5 / 9.7    40 rows 20.5 / 14.8 / 12.7 / 11.3 / 11.7
+//               64 rows 20.2 / 15.4 / 14.0 / 14.9    100 rows 20.3 / 18.9 / 17.3    228 rows 26.4 / 25.4
+//   255 pools   1 row 10.3 / 9.0 / 7.0 / 6.7 / 6.2    32 rows 10.8 / 9.2 / 7.4 / 8.0 / 7.5
+//               64 rows 11.7 / 10.2 / 9.5 / 9.9    130 rows 11.1 / 11.4
+//   128 pools   1 row 7.8 / 7.6 / 6.3 / 6.0 / 5.8    40 rows 8.0 / 7.9 / 7.7 / 7.4 / 7.7    90 rows 7.8 / 9.8 / 9.7
 int split_wanted(int64_t rows, int blocks, int num_sms) {
   const int64_t sms = num_sms;
-  if (blocks >= 6 && 6 * rows <= (blocks > 20 ? 2 * sms : sms)) return 6;
-  if (blocks >= 16 || (blocks >= 6 && 4 * rows <= sms)) return 4;
-  return 1;
+  if (blocks < 6) return 1;
+  if (12 * rows <= sms) return 8;
+  if (6 * rows <= sms) return 6;
+  if (blocks >= 16 && 8 * rows <= 2 * sms) return 8;
+  if (blocks > 20 && 6 * rows <= 2 * sms) return 6;
+  return blocks >= 16 || 4 * rows <= sms ? 4 : 1;
 }
 
 }  // namespace
