@@ -242,6 +242,7 @@ template <int kRows, bool kFour>
 __global__ void __launch_bounds__(32 * kWarps, 7)
     append_rope_kernel(const CacheView c, const BatchView b, const RopeAppendArgs x, unsigned append_blocks,
                        unsigned* status) {
+  pdl_wait();  // launched early: what stands before in the stream has ended
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x < append_blocks) {
     const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows;
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(32 * kWarps, 7)
 __global__ void __launch_bounds__(32 * kWarps)
     cache4_read_kernel(const CacheView c, const BatchView b, __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v,
                        int64_t k_stride, int64_t v_stride, unsigned* status) {
+  pdl_wait();  // launched early: what stands before in the stream has ended
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (row >= b.rows) return;
@@ -293,9 +295,10 @@ cudaError_t launch_append(const CacheView& c, const BatchView& b, const RopeAppe
   const int64_t ab = (b.rows + per - 1) / per;
   const int64_t turns = b.rows * ((x.q.heads > 0) + (x.qi.heads > 0));
   const int64_t blocks = ab + (turns + kWarps - 1) / kWarps;
-  append_rope_kernel<kRows, kFour><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(
-      c, b, x, static_cast<unsigned>(ab), ctx.status);
-  return cudaGetLastError();
+  LaunchCtx early = ctx;
+  early.pdl = 1;
+  return launch_ex(early, append_rope_kernel<kRows, kFour>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0, c,
+                   b, x, static_cast<unsigned>(ab), ctx.status);
 }
 
 }  // namespace
@@ -309,9 +312,11 @@ cudaError_t launch_append_rope(const CacheView& c, bool four, const BatchView& b
 
 cudaError_t launch_cache4_read(const CacheView& c, const BatchView& b, void* k, int64_t k_stride, void* v,
                                int64_t v_stride, const LaunchCtx& ctx) {
-  cache4_read_kernel<<<static_cast<unsigned>((b.rows + kWarps - 1) / kWarps), 32 * kWarps, 0, ctx.stream>>>(
-      c, b, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_stride, v_stride, ctx.status);
-  return cudaGetLastError();
+  LaunchCtx early = ctx;
+  early.pdl = 1;
+  return launch_ex(early, cache4_read_kernel, dim3(static_cast<unsigned>((b.rows + kWarps - 1) / kWarps)),
+                   dim3(32 * kWarps), 0, c, b, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_stride,
+                   v_stride, ctx.status);
 }
 
 }  // namespace dsa

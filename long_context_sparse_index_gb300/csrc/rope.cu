@@ -17,6 +17,7 @@ constexpr int kWarps = 8;
 template <bool kInter>
 __global__ void __launch_bounds__(32 * kWarps, 4)
     rope_kernel(const RopeView r, const RopeArgs a, int n, int per, int lanes, unsigned* status) {
+  pdl_wait();  // launched early: what stands before in the stream has ended
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t row = w * per + lane / lanes;
@@ -40,11 +41,10 @@ cudaError_t launch_rope(const RopeView& r, const RopeArgs& a, const LaunchCtx& c
   while (lanes < 32 && lanes < a.heads * n) lanes *= 2;
   const int per = 32 / lanes;
   const int64_t blocks = (a.rows + static_cast<int64_t>(per) * kWarps - 1) / (static_cast<int64_t>(per) * kWarps);
-  if (r.inter)
-    rope_kernel<true><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, n, per, lanes, ctx.status);
-  else
-    rope_kernel<false><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, ctx.stream>>>(r, a, n, per, lanes, ctx.status);
-  return cudaGetLastError();
+  LaunchCtx early = ctx;
+  early.pdl = 1;
+  return launch_ex(early, r.inter ? rope_kernel<true> : rope_kernel<false>, dim3(static_cast<unsigned>(blocks)),
+                   dim3(32 * kWarps), 0, r, a, n, per, lanes, ctx.status);
 }
 
 }  // namespace dsa
