@@ -81,11 +81,13 @@ def dsa_rope(x, rope: Rope, positions=None, q_begin: int = 0, inverse: bool = Fa
     shard).  Rows may lie any multiple of 8 elements apart.  inverse: turned
     back, which is the rotation's gradient (dx from dy, at the same positions).
     out may be x."""
+    if not isinstance(rope, Rope):
+        raise TypeError(f"rope must be a Rope (got {type(rope).__name__})")
     if isinstance(x, torch.Tensor) and x.dim() == 2:
         back = dsa_rope(x.unsqueeze(1), rope, positions, q_begin, inverse,
                         out.unsqueeze(1) if isinstance(out, torch.Tensor) and out.dim() == 2 else out, stream)
         return out if out is not None else back.squeeze(1)
-    if out is None and stream is None and isinstance(rope, Rope):
+    if out is None and stream is None:
         done = (_binding.marshal or _binding.load_marshal()).rope(x, positions, rope._addr, rope.device_index, q_begin, inverse)
         if done is not None:
             return _binding.outputs(done)

@@ -239,8 +239,9 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // attention4(cache, batch, device, q, pool_idx, scale): (o, lse)
 PyObject* attention4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    const long device = n == 6 ? PyLong_AsLong(a[2]) : -1;
-    const double scale = n == 6 ? PyFloat_AsDouble(a[5]) : 0.0;
+    if (n != 6 || !(PyFloat_Check(a[5]) || PyLong_Check(a[5]))) return declined();
+    const long device = PyLong_AsLong(a[2]);
+    const double scale = PyFloat_AsDouble(a[5]);
     if (PyErr_Occurred()) {
       PyErr_Clear();
       return declined();
