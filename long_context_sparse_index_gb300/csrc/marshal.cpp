@@ -109,7 +109,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return declined();
     }
     int64_t apart = 0;
-    if (!on_current(device)) return declined();
+    if (!on_current(device) || !PyBool_Check(a[5])) return declined();
     const int d = static_cast<int>(device);
     const at::Tensor* x = heads_of(a[0], d, &apart);
     const at::Tensor* at = nullptr;
@@ -123,7 +123,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out = fresh({rows, heads, dim}, at::kBFloat16, d);
     const dsa_rope_t* r = address<dsa_rope_t>(a[2]);
     void* stream = stream_of(d);
-    const int back = PyObject_IsTrue(a[5]);
+    const int back = a[5] == Py_True;
     dsa_status_t st;
     Py_BEGIN_ALLOW_THREADS;
     st = g_lib.rope(x->const_data_ptr(), apart, rows, static_cast<int>(heads), static_cast<int>(dim), r,

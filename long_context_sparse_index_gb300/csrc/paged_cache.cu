@@ -677,8 +677,8 @@ cudaError_t launch_fork_apply(const CacheSet& set, bool four, bool first, const 
   const int parts = slices > by_row ? slices : by_row < 8 ? by_row : 8;
   LaunchCtx early = ctx;
   early.pdl = first;  // (only the plan stands right before the first)
-  return launch_ex(early, four ? fork_apply_kernel<true> : fork_apply_kernel<false>, dim3(n, parts, set.n), dim3(kCopyThreads), 0, set, first, t, src, dst, n,
-                   ws, ctx.status);
+  return launch_ex(early, four ? fork_apply_kernel<true> : fork_apply_kernel<false>, dim3(n, parts, set.n),
+                   dim3(kCopyThreads), 0, set, first, t, src, dst, n, ws, ctx.status);
 }
 
 cudaError_t launch_cache_free(const PageTableView& t, int shift, int num_pages, const int32_t* seqs, int n,

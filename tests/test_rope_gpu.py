@@ -1,5 +1,6 @@
 """Rotated positions on the GPU, against plain 64-bit models: heads turned and turned back, appends that turn keys and
 queries, and the layer trained with them."""
+import ctypes
 import gc
 import math
 
@@ -488,6 +489,15 @@ def test_short_and_long_way_of_a_call_agree():
                 for a, b in zip(got[0], other):
                     assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
     dsa.dsa_sync_status()
+
+
+def test_a_direction_that_is_no_truth_value_is_refused():
+    """The call's own error, whatever asking the object for its truth would raise."""
+    rope, x = dsa.Rope(f4.table(8, 64).to(DEV)), bf16(8, 2, 64).to(DEV)
+    for inverse in (torch.tensor([1, 2]), "back", None):
+        with pytest.raises(ctypes.ArgumentError):
+            dsa.dsa_rope(x, rope, inverse=inverse)
+    assert same_bits(dsa.dsa_rope(x, rope, inverse=1), dsa.dsa_rope(x, rope, inverse=True))
 
 
 def test_short_way_raises_what_the_library_refuses():
