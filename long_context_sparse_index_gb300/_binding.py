@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 import torch
 
@@ -129,16 +130,32 @@ def _configure(lib):
 marshal = None
 
 
+class _Declines:
+    """Stands in for an extension module that does not fit: the Python code does every call."""
+
+    @staticmethod
+    def rope(*args):
+        return None
+
+    append = read = attention4 = rope
+
+
 def _bind_marshal(lib):
+    """Binds the module to the library.  The kernels are the library's either way: without the module, or with one of
+    another torch, calls cost the host more, and a warning says so."""
     global marshal
+    wrong = None
     try:
         from . import _marshal as module
+        if module.torch_version != torch.__version__:
+            wrong = f"was built for torch {module.torch_version}, this is {torch.__version__}"
     except ImportError as e:
-        raise DsaError(DSA_ERR_CUDA, f"the extension module _marshal.so is not built ({e}); run "
-                                     "__graft_entry__.build()") from e
-    if module.torch_version != torch.__version__:
-        raise DsaError(DSA_ERR_CUDA, f"_marshal.so was built for torch {module.torch_version}, this is "
-                                     f"{torch.__version__}; run __graft_entry__.build()")
+        wrong = f"cannot be loaded ({e})"
+    if wrong is not None:
+        warnings.warn(f"the extension module _marshal.so {wrong}: calls take more of the host's time until "
+                      "__graft_entry__.build() has run", RuntimeWarning, stacklevel=3)
+        marshal = _Declines
+        return
     module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.dsa_rope, lib.dsa_cache_append_rope, lib.dsa_cache4_append, lib.dsa_cache4_read,
         lib.dsa_paged4_sparse_attn_fwd)])
@@ -146,7 +163,7 @@ def _bind_marshal(lib):
 
 
 def load_marshal():
-    """The extension module, bound to the library."""
+    """The extension module, bound to the library (or what stands in for it)."""
     load()
     return marshal
 

@@ -143,6 +143,26 @@ def test_binding_refuses_what_is_no_rope_and_cpu_tensors():
         dsa.dsa_paged4_sparse_attn_fwd(None, None, None, None)
 
 
+def test_library_loads_without_a_fitting_extension_module(lib, monkeypatch):
+    """A module that is missing, or of another torch: a warning, and every call is left to the Python code."""
+    import sys
+    import types
+
+    from long_context_sparse_index_gb300 import _binding
+    monkeypatch.setattr(_binding, "marshal", None)
+    pkg = sys.modules["long_context_sparse_index_gb300"]
+    for module in (None, types.SimpleNamespace(torch_version="0.0", bind=lambda *a: pytest.fail("bound"))):
+        monkeypatch.setitem(sys.modules, "long_context_sparse_index_gb300._marshal", module)
+        if module is None:
+            monkeypatch.delattr(pkg, "_marshal", raising=False)
+        else:
+            monkeypatch.setattr(pkg, "_marshal", module, raising=False)
+        with pytest.warns(RuntimeWarning, match="_marshal.so"):
+            _binding._bind_marshal(lib)
+        m = _binding.load_marshal()
+        assert [f() for f in (m.rope, m.append, m.read, m.attention4)] == [None] * 4
+
+
 # --------------------------------------------------------------------------- the plain models
 
 def test_scales_and_codes_are_exact_in_16_bits():
