@@ -7,10 +7,16 @@
 // bf16; the pooled key is the mean of the four turned bf16 keys; the 4-bit codes
 // are those of the turned bf16 key (kv4.cuh).
 //
-// One launch.  Warps of the first blocks append kRows rows each: 16 lanes hold
-// a row's key and 16 its value, 16 B a lane; 8 lanes hold an indexer key.  The
-// others turn a row's heads each, 4 KB for 16 heads of 128 or 32 of 64, all
-// loads before the first store.
+// One launch.  Warps of some blocks append kRows rows each, keys and values in
+// one block, indexer keys in the next: 16 lanes hold a row's key and 16 its value,
+// 16 B a lane; 8 lanes hold an indexer key.  The other blocks' warps turn a row's
+// heads each, 4 KB for 16 heads of 128 or 32 of 64, all loads before the first
+// store.
+// Few rows are bound by the chain offsets -> page and the table's row -> store;
+// many by memory (9815 rows with 48 query heads: 30.0 us, 6.05 TB/s).  A warp for
+// keys, values and indexer keys together needs more registers and twice the
+// chain: 64 rows 2.8 us instead of 2.5 (in 4 bits 3.2 instead of 2.5), 9815 rows
+// 31.8 us.
 #include "kv4.cuh"
 #include "paged.cuh"
 #include "paged_rope_kernels.h"
@@ -82,11 +88,13 @@ __device__ __forceinline__ void store_row(const CacheView& c, int page, int off,
   }
 }
 
-// Rows r0 .. r0 + kRows - 1 (of one warp).  Keys and values take 16 lanes each: a
-// row's key and value side by side, or two rows' keys and then two rows' values.
-template <int kRows, bool kFour>
+// Rows r0 .. r0 + kRows - 1 (of one warp): their keys and values, or their indexer
+// keys.  Keys and values take 16 lanes each: a row's key and value side by side, or
+// two rows' keys and then two rows' values.
+template <int kRows, bool kFour, bool kKv>
 __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView& b, const RopeAppendArgs& x, int64_t r0,
                                             int lane, unsigned* status) {
+  constexpr bool kIdx = !kKv;
   const AppendArgs& a = x.a;
   // the rows' sequences: one walk over the offsets; lanes 8u .. 8u + 7 work out
   // row r0 + u (of a single row: every lane)
@@ -101,10 +109,10 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView&
   for (int p = 0; p < kP; ++p) {
     kx[p] = vx[p] = make_uint4(0u, 0u, 0u, 0u);
     const int64_t r = r0 + (kRows == 4 ? 2 * p + half : 0);
-    if (kRows == 4 && r < b.rows) vx[p] = ld_row(a.v + r * a.v_stride + 8 * ch);
-    if (r < b.rows) kx[p] = ld_row((kRows == 1 && half ? a.v + r * a.v_stride : a.k + r * a.k_stride) + 8 * ch);
+    if (kKv && kRows == 4 && r < b.rows) vx[p] = ld_row(a.v + r * a.v_stride + 8 * ch);
+    if (kKv && r < b.rows) kx[p] = ld_row((kRows == 1 && half ? a.v + r * a.v_stride : a.k + r * a.k_stride) + 8 * ch);
   }
-  if (row < b.rows) own = ld_row(idx + row * a.kidx_stride);
+  if (kIdx && row < b.rows) own = ld_row(idx + row * a.kidx_stride);
   int page = -1, older = 0;  // older: how many of the pool's tokens come before the call's rows
   int64_t pos = 0;
   bool astray = a.reserved != nullptr && __ldg(a.reserved) < 0;
@@ -149,7 +157,7 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView&
   int pg[kP], of[kP];
   RopeChunk kt[kP];
 #pragma unroll
-  for (int p = 0; p < kP; ++p) {
+  for (int p = 0; kKv && p < kP; ++p) {
     const int from = kRows == 4 ? 8 * (2 * p + half) : 0;
     pg[p] = __shfl_sync(0xffffffffu, page, from);
     const int64_t at = __shfl_sync(0xffffffffu, pos, from);
@@ -162,11 +170,11 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView&
   const float* const ci = x.rope_idx.cs;
   const int64_t si = x.rope_idx.stride;
   const bool ends = page >= 0 && (off & 3) == 3;
-  if (kRows == 4) {
+  if (kIdx && kRows == 4) {
     own = turn_chunk(x.rope_idx, own, rope_chunk(x.rope_idx, ci + pos * si, g, page >= 0), g, lane, page >= 0);
     if (page >= 0) *reinterpret_cast<uint4*>(c.k_idx + page * c.kidx_stride + off * kDi + 8 * g) = own;
   }
-  unsigned todo = kRows == 4 ? __ballot_sync(0xffffffffu, ends && g == 0) : 1u;
+  unsigned todo = !kIdx ? 0u : kRows == 4 ? __ballot_sync(0xffffffffu, ends && g == 0) : 1u;
   while (todo != 0u) {
     const int src = __ffs(todo) - 1;  // a lane of the row
     todo &= todo - 1;
@@ -211,7 +219,7 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView&
     if (tok == 1) to[8] = lo;
   }
 #pragma unroll
-  for (int p = 0; p < kP; ++p) {
+  for (int p = 0; kKv && p < kP; ++p) {
     const uint4 y = turn_chunk(x.rope, kx[p], kt[p], ch, lane, pg[p] >= 0 && (kRows == 4 || half == 0));
     if (kRows == 4 || half == 0) kx[p] = y;
     store_row<kFour>(c, pg[p], of[p], kx[p], lane, kRows == 4 || half == 0);
@@ -239,17 +247,29 @@ __device__ __forceinline__ void turn_queries(const BatchView& b, int shift, cons
 }
 
 template <int kRows, bool kFour>
-__global__ void __launch_bounds__(32 * kWarps, 7)
-    append_rope_kernel(const CacheView c, const BatchView b, const RopeAppendArgs x, unsigned append_blocks,
+__global__ void __launch_bounds__(32 * kWarps, kRows == 4 ? 8 : 7)
+    append_rope_kernel(const CacheView c, const BatchView b, const RopeAppendArgs x, unsigned append_blocks, unsigned apart,
                        unsigned* status) {
   pdl_wait();  // launched early: what stands before in the stream has ended
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x < append_blocks) {
-    const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows;
-    if (r0 < b.rows) append_rows<kRows, kFour>(c, b, x, r0, lane, status);
+  // Blocks that append: the first ones, or of many rows every apart-th as long as
+  // there are some, so that their chains run beside the queries' copies (9815 rows
+  // 30.0 us, with the appends first 30.5).
+  unsigned nth = blockIdx.x;
+  bool appends = nth < append_blocks;
+  if constexpr (kRows == 4) {
+    nth = blockIdx.x / apart;
+    appends = blockIdx.x % apart == 0 && nth < append_blocks;
+  }
+  if (appends) {
+    const int64_t r0 = (static_cast<int64_t>(nth >> 1) * kWarps + warp) * kRows;
+    if (r0 >= b.rows) return;
+    if (nth & 1) append_rows<kRows, kFour, true>(c, b, x, r0, lane, status);
+    else append_rows<kRows, kFour, false>(c, b, x, r0, lane, status);
     return;
   }
-  int64_t w = static_cast<int64_t>(blockIdx.x - append_blocks) * kWarps + warp;
+  const unsigned before = kRows == 4 ? min(append_blocks, nth + 1) : append_blocks;
+  int64_t w = static_cast<int64_t>(blockIdx.x - before) * kWarps + warp;
   if (x.q.heads > 0) {
     if (w < b.rows) return turn_queries(b, c.shift, x.rope, x.q, kD, w, x.a.reserved, lane, status);
     w -= b.rows;
@@ -292,19 +312,21 @@ __global__ void __launch_bounds__(32 * kWarps)
 template <int kRows, bool kFour>
 cudaError_t launch_append(const CacheView& c, const BatchView& b, const RopeAppendArgs& x, const LaunchCtx& ctx) {
   const int64_t per = static_cast<int64_t>(kRows) * kWarps;
-  const int64_t ab = (b.rows + per - 1) / per;
+  const int64_t ab = (b.rows + per - 1) / per * 2;
   const int64_t turns = b.rows * ((x.q.heads > 0) + (x.qi.heads > 0));
   const int64_t blocks = ab + (turns + kWarps - 1) / kWarps;
   LaunchCtx early = ctx;
   early.pdl = 1;
   return launch_ex(early, append_rope_kernel<kRows, kFour>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0, c,
-                   b, x, static_cast<unsigned>(ab), ctx.status);
+                   b, x, static_cast<unsigned>(ab), static_cast<unsigned>(blocks / ab), ctx.status);
 }
 
 }  // namespace
 
 cudaError_t launch_append_rope(const CacheView& c, bool four, const BatchView& b, const RopeAppendArgs& x,
                                const LaunchCtx& ctx) {
+  // One row a warp, or four: bf16 64 rows 2.5 / 3.2 us, 1024 rows 4.9 / 5.1, 1536
+  // rows 8.5 / 7.0; in 4 bits 2.5 / 4.5, 4.6 / 6.0, 8.2 / 7.2 (with queries).
   if (b.rows <= 1024)
     return four ? launch_append<1, true>(c, b, x, ctx) : launch_append<1, false>(c, b, x, ctx);
   return four ? launch_append<4, true>(c, b, x, ctx) : launch_append<4, false>(c, b, x, ctx);
