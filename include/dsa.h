@@ -640,8 +640,8 @@ dsa_status_t dsa_paged4_index_topk(const dsa_paged_cache4_t* cache, const dsa_pa
  * and values that the codes stand for, with the same arguments and outputs.
  * Products in fp16 with fp32 sums: codes times scales are exact in fp16, a head's
  * query is scaled into its range by a power of two of its own, and the weights
- * are rounded to it for their product with the values.  Needs no workspace; the
- * same bits on every run.
+ * are rounded to it for their product with the values, relative to a key's weight
+ * that is 1 at any finite logits.  Needs no workspace; the same bits on every run.
  */
 dsa_status_t dsa_paged4_sparse_attn_fwd(const dsa_paged_cache4_t* cache, const dsa_paged_batch_t* batch, const void* q,
                                         const int32_t* pool_idx, int Hq, int D, int topk, float scale, void* o,

@@ -12,8 +12,13 @@
 // fp16's range by a power of two of its own (its largest element between 2^13 and
 // 2^14), which the factor of its logits takes back: elements down to 2^-27 of the
 // largest keep all their bits, and smaller ones are off by 2^-38 of the largest.
-// P is rounded to fp16 for its product with V (2^-12 of each weight; the
-// normaliser sums the unrounded weights), and o once at the end.
+// A head's reference is one of its raw products, and an exponent is a difference of
+// raw products times the head's factor: the reference's own weight is 1 however
+// large its logit (a product and the reference multiplied each for itself would
+// differ by the rounding of either, 16 and more from logits of 2^28 up).
+// P is rounded to fp16 for its product with V (2^-11 of each weight, or 2^-25 of the
+// reference's where that is more; the normaliser sums the unrounded weights), and o
+// once at the end.
 //
 // Layout of the work: a cluster of C CTAs (1 to 8) of four warps per row.  CTA c
 // takes the row's blocks of 16 pools c, c + C, ..., and each warp its own slice of
@@ -34,14 +39,16 @@
 // Measured with 512 pools a row, launches in a graph, keys and values from HBM:
 //   1 row       7.2 us, latency: selection, page, pool (three dependent reads,
 //               0.8 us each), 16 keys a warp at about 0.45 us, the merge.
-//   64 rows     14.0 us: 19 MB, 1.4 TB/s.
-//   512 rows    46 us.
-//   4096 rows   262 us: 262 TFLOP/s, and 4.6 TB/s of pools from L2.  A slice of 16
-//               keys takes 146 clocks of an SM, of which the 32 products have the
-//               tensor pipe for 65; the conversions (64), the scales' products (64)
-//               and the pairing of tokens (16) go to pipes that take an instruction
-//               every two clocks, and the product's issue and theirs overlap by
-//               half only (measured: products' clocks + half of the others').
+//   64 rows     14.1 us: 19 MB, 1.4 TB/s.
+//   512 rows    47 us.
+//   4096 rows   265 us: 259 TFLOP/s, and 4.6 TB/s of pools from L2 (262 us with an
+//               exponent in one FMA of the product and the scaled reference).  A
+//               slice of 16 keys takes 148 clocks of an SM, of which the 32 products
+//               have the tensor pipe for 65; the conversions (64), the scales'
+//               products (64) and the pairing of tokens (16) go to pipes that take
+//               an instruction every two clocks, and the product's issue and theirs
+//               overlap by half only (measured: products' clocks + half of the
+//               others').
 //               More warps an SM (12 or 16), more registers, one or two slices a
 //               step or another order of the instructions moved it by 1 % at most.
 #include <type_traits>
@@ -73,7 +80,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kUnit = 0.0625f;  // what code * scale is to be multiplied by
 // A row's softmax reference moves up only when a score exceeds it by more than
-// this (log2 units): P stays below 2^8, within fp16.
+// this (log2 units): P stays at 2^8 or below, within fp16.
 constexpr float kLag = 8.f;
 
 __device__ __forceinline__ int slab_col(int col) { return (col >> 5) * kRunLd + (col & 31); }
@@ -102,11 +109,11 @@ __device__ __forceinline__ void cluster_st_f32x4(uint32_t a, const float4& v) {
 __device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// (x0, x1) * (f, f) + (c, c), and sums, two at a time
-__device__ __forceinline__ float2 fma2(float x0, float x1, float f, float c) {
+// (x0 + c, x1 + c) * (f, f), and sums, two at a time
+__device__ __forceinline__ float2 addmul2(float x0, float x1, float c, float f) {
   float2 y;
   asm("{\n .reg .b64 x, f, c, y;\n mov.b64 x, {%2, %3};\n mov.b64 f, {%4, %4};\n mov.b64 c, {%5, %5};\n"
-      " fma.rn.f32x2 y, x, f, c;\n mov.b64 {%0, %1}, y;\n}"
+      " add.rn.f32x2 y, x, c;\n mul.rn.f32x2 y, y, f;\n mov.b64 {%0, %1}, y;\n}"
       : "=f"(y.x), "=f"(y.y)
       : "f"(x0), "f"(x1), "f"(f), "f"(c));
   return y;
@@ -206,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
   __shared__ float s_m[kWarps][kHq], s_l[kWarps][kHq];
   // what the cluster's CTAs hand to this one: references, normalisers, partial O
   __shared__ float s_pm[kSplit ? kMaxSplit : 1][kHq], s_pl[kSplit ? kMaxSplit : 1][kHq];
+  __shared__ float s_f[kHq];  // the heads' factors
   __shared__ float4 s_po[kSplit ? kVecs + kMaxSplit : 1];
   __shared__ uint4 s_q[8 * 32];           // Q's fragments, a step's for each lane
 
@@ -340,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
 #pragma unroll
   for (int j = 0; j < 16; ++j) o_acc[j][0] = o_acc[j][1] = o_acc[j][2] = o_acc[j][3] = 0.f;
   float2 l_run[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // even and odd columns
-  // A head's reference m: minus it (0 before the first key), and the raw product
-  // above which it moves up
+  // A head's reference m, a raw product: minus it (0 before the first key), and the
+  // product above which it moves up
   float minus_m[2] = {0.f, 0.f}, rise[2] = {-INFINITY, -INFINITY};
 
   // Where this lane reads.  Column g of the first n-tile is token (g & 1) + 2 (g >> 2)
@@ -438,11 +446,10 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
         for (int off = 1; off <= 2; off <<= 1) mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(0xffffffffu, mx[hh], off));
         al[hh] = 1.f;
         if (mx[hh] > rise[hh]) {
-          const float m = mx[hh] * f;
           // (before the first key there is nothing to rescale)
-          al[hh] = rise[hh] == -INFINITY ? 0.f : ex2_ftz(-minus_m[hh] - m);
-          minus_m[hh] = -m;
-          rise[hh] = (m + kLag) / f;
+          al[hh] = rise[hh] == -INFINITY ? 0.f : ex2_ftz((-minus_m[hh] - mx[hh]) * f);
+          minus_m[hh] = -mx[hh];
+          rise[hh] = __fadd_rd(mx[hh], kLag / f);  // (rounded up it could lie twice the lag above)
         }
         l_run[hh].x *= al[hh];
         l_run[hh].y *= al[hh];
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
     for (int n = 0; n < 2 * kN; ++n)
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        float2 p = fma2(s[n][2 * hh], s[n][2 * hh + 1], hh ? f1 : f0, minus_m[hh]);
+        float2 p = addmul2(s[n][2 * hh], s[n][2 * hh + 1], minus_m[hh], hh ? f1 : f0);
         p.x = ex2_ftz(p.x);
         p.y = ex2_ftz(p.y);
         l_run[hh] = add2(l_run[hh], p);
@@ -533,16 +540,18 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     const int h = g + 8 * hh;
+    const float f = hh ? f1 : f0;
     float M = s_m[0][h];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
     const float Mu = M == -INFINITY ? 0.f : M;  // a CTA without blocks (C > 1 only)
     float L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) L += s_l[w][h] * exp2f(s_m[w][h] - Mu);
-    fac[hh] = exp2f(m_run[hh] - Mu);
+    for (int w = 0; w < kWarps; ++w) L += s_l[w][h] * exp2f((s_m[w][h] - Mu) * f);
+    fac[hh] = exp2f((m_run[hh] - Mu) * f);
     if (!kSplit) fac[hh] *= kUnit / L;
-    if (!kSplit && warp == 0 && t4 == 0) lse[r * kHq + h] = (M + log2f(L)) * kLn2;
+    if (!kSplit && warp == 0 && t4 == 0) lse[r * kHq + h] = __fmaf_rn(M, f, log2f(L)) * kLn2;
+    if (kSplit && warp == 0 && t4 == 0) s_f[h] = f;
     if (kSplit && warp + kWarps * t4 < kC) {  // a lane tells a CTA
       cluster_st_f32(cluster_map(smem_u32(&s_pm[rank][h]), warp + kWarps * t4), M);
       cluster_st_f32(cluster_map(smem_u32(&s_pl[rank][h]), warp + kWarps * t4), L);
@@ -593,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
 #pragma unroll
       for (int u = 0; u < kMaxSplit; ++u) {
         if (u >= kC) continue;
-        const float f = exp2f(cm[u] - M);  // every row has a key of its own: M is finite
+        const float f = exp2f((cm[u] - M) * s_f[h]);  // every row has a key of its own: M is finite
         const float4 y = s_po[u * per + x];
         L += s_pl[u][h] * f;
         acc.x += y.x * f;
@@ -604,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
       const float inv = kUnit / L;
       *reinterpret_cast<uint2*>(orow + e) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-      if (col == 0) lse[r * kHq + h] = (M + log2f(L)) * kLn2;
+      if (col == 0) lse[r * kHq + h] = __fmaf_rn(M, s_f[h], log2f(L)) * kLn2;
     }
   }
 }

@@ -307,6 +307,58 @@ def test_attention_of_queries_of_any_magnitude(rows, power):
     check_attention4(m, q, sel, scale, o, lse)
 
 
+def huge_bounds(o, av, lse, sum_v, keys):
+    """What the arithmetic may be off by where the products are exact: integers whose sums have at most 24 bits.  A weight's
+    exponent is a difference of products times a factor (a rounding each, two in the factor: 2^-22 of an exponent below 64
+    that counts at all, which makes 2^-16 of the weight), taken at most three times (warp, CTA, cluster) with 2^-21 for each
+    exponential: below 2^-14 in all, and for the normaliser as much.  P is rounded to fp16: 2^-11 of it, or 2^-25 where it
+    is subnormal, and the normaliser is at least 1.  Sums of n terms, twice, and o rounded once more.  lse: a product, a
+    sum and a product with rounded constants, six roundings of 2^-24 each."""
+    n = keys[:, None] * 2.0 ** -23
+    rel = 2.0 ** -13 + 2.0 ** -11 + n
+    off = rel[..., None] * av + 2.0 ** -25 * sum_v[:, None] + 1e-30
+    return off + 2.0 ** -8 * (o.abs() + off), 2.0 ** -13 + n + 2.0 ** -21 * lse.abs()
+
+
+# (products reach some 150: logits of 2^7 to 2^107)
+POWERS = [0, 4, 10, 17, 20, 21, 22, 23, 25, 27, 30, 53, 100]
+
+
+@pytest.mark.parametrize("rows,old,topk", [(3, 1020, 200), (40, 700, 120), (100, 200, 50), (300, 200, 40), (500, 60, 12)])
+@pytest.mark.parametrize("power", POWERS)
+def test_attention_of_huge_logits(rows, old, topk, power):
+    """Exact products and any finite logits: the largest one's weight is one, whatever its logit's last bit stands for."""
+    m = f4.Model4([1] * rows, [old + j % 50 for j in range(rows)], 16, seed=61, ints=True)
+    cache, batch = m.to_gpu4(dsa)
+    q, sel, scale = m.fill(m.T, HQ, D), random_selection(m, topk, seed=6), 2.0 ** power
+    o, lse = dsa.dsa_paged4_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV), scale=scale)
+    dsa.dsa_sync_status()
+    ro, rl, av, _ = m.attention(q, sel, scale)
+    bo, bl = huge_bounds(ro, av, rl, *m.abs_values(sel))
+    err = (o.cpu().double() - ro).abs()
+    assert torch.all(err <= bo), (err / bo).max()
+    err = (lse.cpu().double() - rl).abs()
+    assert torch.all(err <= bl), (err / bl).max()
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("power", POWERS)
+def test_weights_of_huge_logits_sum_to_one(rows, power):
+    """Products of any numbers, and values that are all 3: so is every output (the weights' sum and the normaliser agree to
+    2^-11, and bf16's neighbours of 3 are 2^-6 away)."""
+    m = f4.Model4([1] * rows, [300 + j % 50 for j in range(rows)], 16, seed=62)
+    flat = m.kv.view(-1, 576)
+    for t in range(4):
+        _, code, _, scale = f4.places(t)
+        flat[:, code], flat[:, scale] = 0x77, 0x90  # 6 times 8 / 16
+    assert torch.all(f4.read(flat[0])[1] == 3)
+    cache, batch = m.to_gpu4(dsa)
+    q, sel = m.fill(m.T, HQ, D), random_selection(m, 60, seed=7)
+    o, lse = dsa.dsa_paged4_sparse_attn_fwd(cache, batch, q.to(DEV), sel.to(DEV), scale=2.0 ** power)
+    dsa.dsa_sync_status()
+    assert torch.all(o == 3) and torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("rows", [3, 100, 500])
 def test_attention_reads_nothing_it_does_not_attend_to(rows):
     """NaN in every slot that no row attends to, positions behind the last token among them."""
