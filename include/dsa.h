@@ -540,7 +540,10 @@ dsa_status_t dsa_rope(const void* x, int64_t x_stride, int64_t rows, int heads, 
  * Queries that an append turns along: q bf16 [rows, Hq, 128] by the rope of the
  * keys, q_idx bf16 [rows, Hi, 64] by the rope of the indexer's keys, each row at
  * its position.  Hq = 0 or Hi = 0: none.  Strides as in dsa_rope; q_out may be q,
- * and q_idx_out q_idx.  Rows behind the last sequence are not written.
+ * and q_idx_out q_idx.  Rows behind the last sequence are not written, nor are
+ * rows that are not appended (after a reservation that found too few pages, with
+ * offsets that contradict each other, at a position that one of the two tables
+ * does not have, of a page that is none): repeating the call turns no query twice.
  */
 typedef struct {
   const void* q;

@@ -114,7 +114,8 @@ def dsa_cache_append_rope(cache: PagedCache, batch: PagedBatch, k, v, k_idx, rop
     (None: not turned), each row at its position, and with them the step's
     queries: q [rows, Hq, 128] by `rope`, q_idx [rows, Hi, 64] by `rope_idx`.
     Returns (q_out, q_idx_out), None for what was not given; q_out may be q.
-    One launch.  reserved: as in dsa_cache_append."""
+    Queries of rows that are not appended are not written, so that a step may be
+    repeated after an error.  One launch.  reserved: as in dsa_cache_append."""
     _is_cache(cache, False)
     return _append(load().dsa_cache_append_rope, cache, batch, k, v, k_idx, rope, rope_idx, q, q_idx, q_out, q_idx_out,
                    reserved, stream)

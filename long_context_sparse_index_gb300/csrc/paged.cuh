@@ -21,11 +21,15 @@ struct RowAt {
 
 // All lanes of a warp call it together with the same row.  Offsets and lengths
 // of 128 sequences are looked at at once, so that a call of up to 128
-// sequences waits for memory once.
-__device__ __forceinline__ RowAt warp_locate(const BatchView& b, int shift, int64_t row, int lane, unsigned* status) {
+// sequences waits for memory once.  kAll: at all offsets; *astray: some of them
+// contradict each other or the call's rows (then an append writes nothing).
+template <bool kAll = false>
+__device__ __forceinline__ RowAt warp_locate(const BatchView& b, int shift, int64_t row, int lane, unsigned* status,
+                                             bool* astray = nullptr) {
   constexpr int kU = 4;
   RowAt x{-1, -1};
-  for (int j0 = 0; j0 < b.batch && x.seq < 0; j0 += 32 * kU) {
+  bool bad = false;
+  for (int j0 = 0; j0 < b.batch && (kAll || x.seq < 0); j0 += 32 * kU) {
     int c0[kU], c1[kU], len[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -53,7 +57,10 @@ __device__ __forceinline__ RowAt warp_locate(const BatchView& b, int shift, int6
         if (lane == 0) record_status(status, kStatusInternal);
       }
     }
+#pragma unroll
+    for (int u = 0; kAll && u < kU; ++u) bad |= c0[u] < 0 || c1[u] < c0[u] || c1[u] > b.rows;
   }
+  if (kAll) *astray = __any_sync(0xffffffffu, bad) != 0;
   return x;
 }
 

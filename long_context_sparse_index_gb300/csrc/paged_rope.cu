@@ -10,13 +10,15 @@
 // One launch.  Warps of some blocks append kRows rows each, keys and values in
 // one block, indexer keys in the next: 16 lanes hold a row's key and 16 its value,
 // 16 B a lane; 8 lanes hold an indexer key.  The other blocks' warps turn a row's
-// heads each, 4 KB for 16 heads of 128 or 32 of 64, all loads before the first
-// store.
+// heads each, 4 KB for 16 heads of 128 or 32 of 64 in two passes, each with all its
+// loads before its first store.
 // Few rows are bound by the chain offsets -> page and the table's row -> store;
-// many by memory (9815 rows with 48 query heads: 30.0 us, 6.05 TB/s).  A warp for
-// keys, values and indexer keys together needs more registers and twice the
-// chain: 64 rows 2.8 us instead of 2.5 (in 4 bits 3.2 instead of 2.5), 9815 rows
-// 31.8 us.
+// many by memory (9815 rows with 48 query heads: 30.5 us, 5.95 TB/s).  Asking for
+// all offsets and for the page before a query is written costs 64 rows 2.7 us
+// instead of 2.5, and 9815 rows 0.5 us.  A warp for keys, values and indexer keys
+// together needs more registers and twice the chain (measured without that: 64 rows
+// 2.8 us instead of 2.5, in 4 bits 3.2 instead of 2.5; 9815 rows 31.8 instead of
+// 30.0).
 #include "kv4.cuh"
 #include "paged.cuh"
 #include "paged_rope_kernels.h"
@@ -227,23 +229,28 @@ __device__ __forceinline__ void append_rows(const CacheView& c, const BatchView&
   }
 }
 
-// Row r of the queries (or of the indexer's), a warp's work.
-__device__ __forceinline__ void turn_queries(const BatchView& b, int shift, const RopeView& r, const QueryRows& q, int D,
-                                             int64_t row, const int32_t* reserved, int lane, unsigned* status) {
+// A row of the queries (or of the indexer's), a warp's work.  It is turned where
+// append_rows appends it, by the same conditions, so that a step that is repeated
+// after an error turns no query in place twice; append_rows records what is wrong.
+__device__ __forceinline__ void turn_queries(const CacheView& c, const BatchView& b, const RopeAppendArgs& x,
+                                             const RopeView& r, const QueryRows& q, int D, int64_t row, int lane) {
+  int page = -1;
   const auto find = [&]() -> const float* {
-    // (the append records a reservation that found too few pages)
-    if (reserved != nullptr && __ldg(reserved) < 0) return nullptr;
-    const RowAt at = warp_locate(b, shift, row, lane, status);
-    if (at.seq < 0 || at.pos < 0) return nullptr;
-    if (at.pos < r.positions) return r.cs + at.pos * r.stride;
-    if (lane == 0) record_status(status, kStatusInternal);
-    return nullptr;
+    if (x.a.reserved != nullptr && __ldg(x.a.reserved) < 0) return nullptr;
+    bool astray;
+    const RowAt at = warp_locate<true>(b, c.shift, row, lane, nullptr, &astray);
+    if (astray || at.seq < 0 || at.pos < 0 || (x.rope.dims != 0 && at.pos >= x.rope.positions) ||
+        (x.rope_idx.dims != 0 && at.pos >= x.rope_idx.positions))
+      return nullptr;
+    page = __ldg(b.table + at.seq * b.table_stride + (at.pos >> c.shift));
+    return r.cs + at.pos * r.stride;
   };
+  const auto sure = [&] { return static_cast<unsigned>(page) < static_cast<unsigned>(c.num_pages); };
   const __nv_bfloat16* in = q.in + row * q.in_stride;
   __nv_bfloat16* out = q.out + row * q.out_stride;
   const int n = rope_chunk_lanes(r.dims, r.inter);
-  if (r.inter) turn_heads<true>(in, out, q.heads, D, r.dims, n, 1.f, lane, 32, find);
-  else turn_heads<false>(in, out, q.heads, D, r.dims, n, 1.f, lane, 32, find);
+  if (r.inter) turn_heads<true>(in, out, q.heads, D, r.dims, n, 1.f, lane, 32, find, sure);
+  else turn_heads<false>(in, out, q.heads, D, r.dims, n, 1.f, lane, 32, find, sure);
 }
 
 template <int kRows, bool kFour>
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(32 * kWarps, kRows == 4 ? 8 : 7)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // Blocks that append: the first ones, or of many rows every apart-th as long as
   // there are some, so that their chains run beside the queries' copies (9815 rows
-  // 30.0 us, with the appends first 30.5).
+  // 0.5 us less than with the appends first).
   unsigned nth = blockIdx.x;
   bool appends = nth < append_blocks;
   if constexpr (kRows == 4) {
@@ -271,11 +278,10 @@ __global__ void __launch_bounds__(32 * kWarps, kRows == 4 ? 8 : 7)
   const unsigned before = kRows == 4 ? min(append_blocks, nth + 1) : append_blocks;
   int64_t w = static_cast<int64_t>(blockIdx.x - before) * kWarps + warp;
   if (x.q.heads > 0) {
-    if (w < b.rows) return turn_queries(b, c.shift, x.rope, x.q, kD, w, x.a.reserved, lane, status);
+    if (w < b.rows) return turn_queries(c, b, x, x.rope, x.q, kD, w, lane);
     w -= b.rows;
   }
-  if (x.qi.heads > 0 && w < b.rows)
-    turn_queries(b, c.shift, x.rope_idx, x.qi, kDi, w, x.a.reserved, lane, status);
+  if (x.qi.heads > 0 && w < b.rows) turn_queries(c, b, x, x.rope_idx, x.qi, kDi, w, lane);
 }
 
 // ----------------------------------------------------------------- reading back
@@ -326,7 +332,10 @@ cudaError_t launch_append(const CacheView& c, const BatchView& b, const RopeAppe
 cudaError_t launch_append_rope(const CacheView& c, bool four, const BatchView& b, const RopeAppendArgs& x,
                                const LaunchCtx& ctx) {
   // One row a warp, or four: bf16 64 rows 2.5 / 3.2 us, 1024 rows 4.9 / 5.1, 1536
-  // rows 8.5 / 7.0; in 4 bits 2.5 / 4.5, 4.6 / 6.0, 8.2 / 7.2 (with queries).
+  // rows 8.5 / 7.0; in 4 bits 2.5 / 4.5, 4.6 / 6.0, 8.2 / 7.2 (with queries, of one
+  // sequence).  Every warp looks at all offsets, so rows of as many sequences take
+  // longer: 256 rows 4.0 us, 1024 rows 10, 8192 rows 337 (of one sequence 3.1, 4.9
+  // and 26).
   if (b.rows <= 1024)
     return four ? launch_append<1, true>(c, b, x, ctx) : launch_append<1, false>(c, b, x, ctx);
   return four ? launch_append<4, true>(c, b, x, ctx) : launch_append<4, false>(c, b, x, ctx);

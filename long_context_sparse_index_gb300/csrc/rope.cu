@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     return nullptr;
   };
   turn_heads<kInter>(a.x + row * a.x_stride, a.out + row * a.out_stride, a.heads, a.D, r.dims, n, a.dir,
-                     lane & (lanes - 1), lanes, find);
+                     lane & (lanes - 1), lanes, find, [] { return true; });
 }
 
 }  // namespace

@@ -107,10 +107,11 @@ __host__ __device__ inline int rope_chunk_lanes(int dims, bool inter) {
 // lanes: lane `lane` of `lanes` (a power of two, at least n = rope_chunk_lanes).
 // `row()` says which row (null: none, and nothing is written); it is asked after
 // the first heads have been asked for, so that looking up a position costs no time
-// of its own.  `in` and `out` may be the same heads.
-template <bool kInter, typename Row>
+// of its own.  `sure()` is asked after the table's row has been asked for: false,
+// and nothing is written either.  `in` and `out` may be the same heads.
+template <bool kInter, typename Row, typename Sure>
 __device__ __forceinline__ void turn_heads(const __nv_bfloat16* in, __nv_bfloat16* out, int heads, int D, int dims, int n,
-                                           float dir, int lane, int lanes, Row&& row) {
+                                           float dir, int lane, int lanes, Row&& row, Sure&& sure) {
   constexpr int kU = kInter ? 4 : 2;  // heads under way: four 16-byte loads a lane
   const int chunks = kInter ? dims / 8 : dims / 16;  // what a head has for a lane each
   const int j = lane & (n - 1), step = lanes / n;
@@ -130,14 +131,17 @@ __device__ __forceinline__ void turn_heads(const __nv_bfloat16* in, __nv_bfloat1
   const float* cs = row();
   if (cs == nullptr) return;
   const float* sn = cs + dims / 2;
+  constexpr int kV = kInter ? 1 : 2;
+  float4 c[kV], s[kV];
   if (j < chunks) {
-    constexpr int kV = kInter ? 1 : 2;
-    float4 c[kV], s[kV];
 #pragma unroll
     for (int e = 0; e < kV; ++e) {
       c[e] = __ldg(reinterpret_cast<const float4*>(cs) + kV * j + e);
       s[e] = __ldg(reinterpret_cast<const float4*>(sn) + kV * j + e);
     }
+  }
+  if (!sure()) return;
+  if (j < chunks) {
     while (h0 < heads) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {

@@ -362,6 +362,44 @@ def test_append_rope_writes_nothing_after_a_failed_reservation_or_wrong_offsets(
         assert torch.equal(getattr(cache, n).cpu().view(torch.uint8), getattr(m, n).view(torch.uint8)), n
 
 
+@pytest.mark.parametrize("what", ["offsets", "first_offset", "middle_offsets", "reserved", "table", "table_idx", "page"])
+@pytest.mark.parametrize("new", [[3, 2, 1], [1] * 290 + [3], [1500, 3, 2]])
+@pytest.mark.parametrize("four", [False, True])
+def test_queries_of_rows_that_are_not_appended_stay(four, new, what):
+    """Turned in place: a step that is repeated after an error turns no query twice.  Offsets that are wrong anywhere, a
+    failed reservation: no row is appended; a position that one of the tables does not have, a bad page: not that row."""
+    m = f4.Model4(new, [2 + 7 * j % 40 for j in range(len(new))], 16, seed=12)
+    ropes = f4.Turned(128, 64, False, 4000)
+    cache, batch = m.to_gpu4(dsa) if four else m.to_gpu(dsa)
+    call = dsa.dsa_cache4_append if four else dsa.dsa_cache_append_rope
+    kvi = gpu(m.fill(m.T, D), m.fill(m.T, D), m.fill(m.T, DI))
+    q, qi = bf16(m.T, HQ, D, seed=2), bf16(m.T, 6, DI, seed=3)
+    gq, gqi = gpu(q, qi)
+    r, ri = ropes.to_gpu(dsa)
+    pos = torch.tensor([i for _, _, i in m.rows()])
+    done, kw, br, bri, cu, table, end = torch.zeros(m.T, dtype=torch.bool), {}, r, ri, list(m.cu), m.table.clone(), 10
+    if what == "offsets":
+        cu[-1] += 1
+    elif what == "first_offset":
+        cu[0] = -1
+    elif what == "middle_offsets":
+        cu[-2] = cu[-1] + 1
+    elif what == "reserved":
+        kw = dict(reserved=i32([-1]))
+    elif what == "page":
+        table[1, 0] = m.pages
+        done = torch.tensor([b != 1 or i >= 16 for _, b, i in m.rows()])
+    else:
+        done = pos < end
+        br, bri = (dsa.Rope(x.cos_sin[:end].contiguous()) if (what == "table") == (x is r) else x for x in (r, ri))
+    bad = dsa.PagedBatch(table.to(DEV), batch.seq_lens, i32(cu))
+    reported(lambda: call(cache, bad, *kvi, br, bri, q=gq, q_idx=gqi, q_out=gq, q_idx_out=gqi, **kw))
+    for given, got, cs in ((q, gq, ropes.k), (qi, gqi, ropes.idx)):
+        assert same_bits(got.cpu()[~done], given[~done])
+        check_turned(got[done.to(DEV)], given[done], cs[pos[done]], False)
+    assert done.any() == (what in ("table", "table_idx", "page")) and not done.all()
+
+
 def test_serving_with_rotated_positions_is_the_turned_training_forward():
     """A prompt in chunks, then tokens one by one, into a bf16 cache, keys, queries and indexer turned by the append:
     every row's attention is the contiguous layer's on heads that dsa_rope turned (which may round a number the other
