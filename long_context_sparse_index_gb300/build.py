@@ -1,10 +1,12 @@
 """Builds libdsa.so in-tree with nvcc for sm_103a (GB300), and the Python
-binding's extension module _marshal.so with the host compiler.
+binding's extension module _marshal with the host compiler.
 
 Each CUDA translation unit under csrc/ is compiled in parallel to an object
 in _build/, then linked (static CUDA runtime) into libdsa.so next to this
 file.  Rebuilds only when a source or header is newer than the library (the
-extension module also when torch has changed).
+extension module also when torch has changed).  The library does not need the
+extension module: where that cannot be built (no Python headers, another torch, no
+host compiler for it), a warning says why.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -35,8 +38,10 @@ LIB_STAMPS = os.path.join(HERE, "libdsa_stamps.so")
 # (DSA_DEBUG); the arithmetic and results are the default build's
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libdsa_debug.so")
-# the binding's short way into the library (csrc/marshal.cpp), for the torch it was built with
-MARSHAL = os.path.join(HERE, "_marshal.so")
+# the binding's short way into the library (csrc/marshal.cpp), for the Python that its name says and the torch it was
+# built with
+EXT_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX")
+MARSHAL = os.path.join(HERE, "_marshal" + EXT_SUFFIX)
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -64,9 +69,9 @@ def _stale(lib: str) -> bool:
 
 
 def build_marshal(force: bool = False) -> str:
-    """Compile the binding's extension module; returns its path."""
+    """Compile the binding's extension module; returns its path, or raises."""
     import torch
-    stamp = os.path.join(BUILD, "marshal.torch")
+    stamp = os.path.join(BUILD, f"marshal{EXT_SUFFIX}.torch")
     deps = [MARSHAL_SOURCE, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
     if not force and os.path.exists(MARSHAL) and os.path.exists(stamp):
         with open(stamp) as f:
@@ -92,6 +97,26 @@ def build_marshal(force: bool = False) -> str:
     return MARSHAL
 
 
+def _try_marshal(force: bool):
+    """Build the extension module; returns why it could not be built (the Python code then does every call), or None."""
+    plain = os.path.join(os.path.dirname(MARSHAL), "_marshal.so")  # a name that any Python would import
+    if plain != MARSHAL and os.path.exists(plain):
+        os.remove(plain)
+    try:
+        build_marshal(force)
+    except Exception as e:
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)  # made of other sources, or for another torch
+        return e
+    return None
+
+
+def _warn_marshal(why) -> None:
+    if why is not None:
+        warnings.warn(f"the extension module was not built, calls will take more of the host's time: {why}", RuntimeWarning,
+                      stacklevel=3)
+
+
 def build(force: bool = False, verbose: bool = False, trace: bool = False, debug: bool = False,
           stamps: bool = False) -> str:
     """Compile and link libdsa.so (or, with trace=True, the measurement
@@ -105,7 +130,7 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False, debug
         (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
     if not force and not _stale(lib):
         if default:
-            build_marshal()
+            _warn_marshal(_try_marshal(False))
         return lib
     os.makedirs(bdir, exist_ok=True)
     nvcc = _nvcc()
@@ -126,16 +151,16 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False, debug
 
     srcs = sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        marshal = ex.submit(build_marshal, force) if default else None
+        marshal = ex.submit(_try_marshal, force) if default else None
         objs = list(ex.map(compile_one, srcs))
-        if marshal is not None:
-            marshal.result()
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if marshal is not None:
+        _warn_marshal(marshal.result())
     return lib
 
 
