@@ -15,6 +15,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -72,8 +73,14 @@ at::Tensor fresh(at::IntArrayRef shape, c10::ScalarType type, int device) {
                                 std::nullopt);
 }
 
-// The current device, if it is the one that the handles are on.
-bool on_current(long device) { return device >= 0 && c10::cuda::current_device() == device; }
+// Whether the handles are on the current device, and new memory is left as it is
+// (torch's deterministic mode has it filled, which torch.empty does and fresh() does
+// not).
+bool takes(long device) {
+  at::Context& c = at::globalContext();
+  if (c.deterministicAlgorithms() && c.deterministicFillUninitializedMemory()) return false;
+  return device >= 0 && c10::cuda::current_device() == device;
+}
 void* stream_of(int device) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream(); }
 
 template <typename T>
@@ -109,7 +116,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return declined();
     }
     int64_t apart = 0;
-    if (!on_current(device) || !PyBool_Check(a[5])) return declined();
+    if (!takes(device) || !PyBool_Check(a[5])) return declined();
     const int d = static_cast<int>(device);
     const at::Tensor* x = heads_of(a[0], d, &apart);
     const at::Tensor* at = nullptr;
@@ -144,7 +151,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       return declined();
     }
-    if (!on_current(device)) return declined();
+    if (!takes(device)) return declined();
     const int d = static_cast<int>(device);
     int64_t ks = 0, vs = 0, is = 0, qs = 0, qis = 0;
     const at::Tensor *k = rows_of(a[4], 128, d, &ks), *v = rows_of(a[5], 128, d, &vs), *ki = rows_of(a[6], 64, d, &is);
@@ -215,7 +222,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       return declined();
     }
-    if (!on_current(device) || rows < 1 || rows > (1LL << 27)) return declined();
+    if (!takes(device) || rows < 1 || rows > (1LL << 27)) return declined();
     const int d = static_cast<int>(device);
     at::Tensor k = fresh({rows, 128}, at::kBFloat16, d), v = fresh({rows, 128}, at::kBFloat16, d);
     dsa_paged_batch_t b = *address<dsa_paged_batch_t>(a[1]);
@@ -246,7 +253,7 @@ PyObject* attention4(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       return declined();
     }
-    if (!on_current(device)) return declined();
+    if (!takes(device)) return declined();
     const int d = static_cast<int>(device);
     const at::Tensor *q = plain(a[3], at::kBFloat16, 3, d), *sel = plain(a[4], at::kInt, 2, d);
     if (!q || !sel || !q->is_contiguous() || !sel->is_contiguous()) return declined();

@@ -556,3 +556,31 @@ def test_short_way_raises_what_the_library_refuses():
             dsa.dsa_rope(x, rope, q_begin=1)
     gc.collect()
     assert torch.cuda.memory_allocated() <= before  # the outputs of refused calls are given back
+
+
+def test_both_ways_fill_new_memory_where_torch_is_told_to():
+    """In torch's deterministic mode new memory is filled with NaN: what a call leaves unwritten in its outputs reads alike
+    on the extension module's way and on the Python code's."""
+    here = torch.cuda.current_stream()
+    rope = dsa.Rope(f4.table(64, 64).to(DEV))
+    m = f4.Model4([2, 1], [7, 30], 16, seed=12)
+    cache, batch = m.to_gpu4(dsa)
+    rows = m.T + 4  # padding behind the last sequence
+    x, new = bf16(rows, HQ, D).to(DEV), gpu(bf16(rows, D), bf16(rows, D), bf16(rows, DI))
+    sel = torch.full((rows, 4), -1, dtype=torch.int32, device=DEV)
+
+    def every(**kw):
+        yield dsa.dsa_cache4_append(cache, batch, *new, rope, q=x, **kw)[0]
+        yield from dsa.dsa_cache4_read(cache, batch, rows, **kw)
+        yield from dsa.dsa_paged4_sparse_attn_fwd(cache, batch, x, sel, **kw)
+
+    assert not torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        for kw in (dict(), dict(stream=here)):
+            for y in every(**kw):
+                assert torch.isfinite(y[:m.T]).all() and torch.isnan(y[m.T:]).all()
+                y.fill_(1.0)  # (what its memory holds when it is given out again)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    dsa.dsa_sync_status()
