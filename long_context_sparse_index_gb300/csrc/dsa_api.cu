@@ -1689,9 +1689,8 @@ dsa_status_t paged_attn(const char* fn, const Cache* cache, const dsa_paged_batc
   dsa::call_param("batch", b.batch);
   dsa::call_param("topk", topk);
   constexpr bool kFour = in_four(static_cast<const Cache*>(nullptr));
-  dsa::call_variant(kFour ? "a cluster per row: cp.async gather of 4-bit pools through the block table, codes to fp16 in "
-                            "registers, mma.sync, online softmax"
-                          : "a cluster per row: cp.async gather through the block table, mma.sync, online softmax");
+  // (the launch of the 4-bit kernel says how it splits a row)
+  if (!kFour) dsa::call_variant("a cluster per row: cp.async gather through the block table, mma.sync, online softmax");
   cudaError_t e = timed_launch(kFour ? "paged4_attn" : "paged_attn", ctx.stream, [&] {
     return kFour ? dsa::launch_paged4_attn(c, b, q, pool_idx, topk, scale, o, lse, ctx)
                  : dsa::launch_paged_attn(c, b, q, pool_idx, topk, scale, o, lse, ctx);

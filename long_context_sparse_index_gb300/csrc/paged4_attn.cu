@@ -676,6 +676,12 @@ cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q
                            float scale, void* o, float* lse, int split, const LaunchCtx& ctx) {
   const cudaError_t e = allow_smem<kStages, kSplit>();
   if (e != cudaSuccess) return e;
+  call_param("ctas_per_row", split);
+  call_param("ring_blocks", kStages);
+  call_variant(kSplit ? "a cluster per row: cp.async gather of 4-bit pools through the block table, codes to fp16 in "
+                        "registers, mma.sync, online softmax"
+                      : "a CTA per row: cp.async gather of 4-bit pools through the block table, codes to fp16 in "
+                        "registers, mma.sync, online softmax");
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = split_config(attr, b.rows, split, smem_bytes<kStages>(row_blocks(topk), split), ctx.stream);
   return cudaLaunchKernelEx(&cfg, paged4_attn_kernel<kStages, kSplit>, c, b, static_cast<const __nv_bfloat16*>(q),

@@ -359,6 +359,25 @@ def test_weights_of_huge_logits_sum_to_one(rows, power):
     assert torch.all(o == 3) and torch.isfinite(lse).all()
 
 
+def test_attention_records_how_a_row_is_split():
+    """Every number of CTAs a row has, and both lengths of the ring, among the sizes of a device of any width."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    met = set()
+    for topk in (512, 96):
+        for rows in sorted({1, sms // 12, sms // 6, sms // 4, sms * 3 // 8, sms // 2, sms * 2 // 3, sms, sms * 3 // 2, sms * 2,
+                            sms * 3, sms * 3 + 1}):
+            m = f4.Model4([1] * rows, [50] * rows, 16, seed=63)
+            cache, batch = m.to_gpu4(dsa)
+            sel = torch.full((rows, topk), -1, dtype=torch.int32)
+            dsa.dsa_paged4_sparse_attn_fwd(cache, batch, m.fill(rows, HQ, D).to(DEV), sel.to(DEV))
+            c = dsa.last_kernel_config()
+            ctas, ring = c["params"]["ctas_per_row"], c["params"]["ring_blocks"]
+            assert ("cluster" in c["variant"]) == (ctas > 1) and (ring == 6 or rows > 3 * sms)
+            met.add((ctas, ring))
+    dsa.dsa_sync_status()
+    assert met == {(8, 6), (6, 6), (4, 6), (2, 6), (1, 6), (1, 4)}
+
+
 @pytest.mark.parametrize("rows", [3, 100, 500])
 def test_attention_reads_nothing_it_does_not_attend_to(rows):
     """NaN in every slot that no row attends to, positions behind the last token among them."""
