@@ -37,7 +37,7 @@
 // same bits on every run.
 //
 // Measured with 512 pools a row, launches in a graph, keys and values from HBM:
-//   1 row       7.2 us, latency: selection, page, pool (three dependent reads,
+//   1 row       7.3 us, latency: selection, page, pool (three dependent reads,
 //               0.8 us each), 16 keys a warp at about 0.45 us, the merge.
 //   64 rows     14.1 us: 19 MB, 1.4 TB/s.
 //   512 rows    47 us.
@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
 
   // The pools of this CTA's blocks as byte offsets, a pool a thread.  Slot s < nsel
   // holds pool prow[s]; slot nsel is the row's own pool; slots beyond are empty.
-  // An entry that is no eligible pool or breaks ascending order, and a page that
-  // is none, are recorded; nothing is read for them.
+  // An entry that is no eligible pool, and a page that is none, are recorded, and
+  // nothing is read for them; an entry that breaks ascending order is recorded, too,
+  // and attended to as it stands.
   bool bad = false;
   const int pshift = c.shift - 2;  // log2(pools per page)
   const auto pool_of = [&](int e) -> int64_t {  // -1: none
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 4 ? 4 : 3)
   const int64_t* const my_pools = pools + warp * kWarpPools;
   const uint32_t ring = sKV + warp * kWarpStage;
   // (a split row has few slices, and all of them under way at once; a whole row
-  // keeps the pace of its refills: 4096 rows 265 us with a full ring, 261 so)
+  // keeps the pace of its refills: 4096 rows 268 us with a full ring, 265 so)
   constexpr int kFirst = kSplit ? kStages : kStages - 2;
 #pragma unroll
   for (int u = 0; u < kFirst; ++u) {
@@ -693,12 +694,12 @@ cudaError_t launch_variant(const CacheView& c, const BatchView& b, const void* q
 // slow one another down, and the rows' clusters have to be on the device at once
 // (the runtime says how many are: 51 of 8, 74 of 6).  Measured, in us with 1 / 2 / 4 /
 // 6 / 8 CTAs a row, keys and values from HBM:
-//   512 pools   1 row 17.9 / 12.8 / 9.0 / 7.7 / 7.1    16 rows 18.0 / 13.1 / 9.3 / 8.0 / 8.8
-//               32 rows 19.7 / 14.4 / 10.5 / 10.5 / 9.7    40 rows 20.5 / 14.8 / 12.7 / 11.3 / 11.7
-//               64 rows 20.2 / 15.4 / 14.0 / 14.9    100 rows 20.3 / 18.9 / 17.3    228 rows 26.4 / 25.4
-//   255 pools   1 row 10.3 / 9.0 / 7.0 / 6.7 / 6.2    32 rows 10.8 / 9.2 / 7.4 / 8.0 / 7.5
-//               64 rows 11.7 / 10.2 / 9.5 / 9.9    130 rows 11.1 / 11.4
-//   128 pools   1 row 7.8 / 7.6 / 6.3 / 6.0 / 5.8    40 rows 8.0 / 7.9 / 7.7 / 7.4 / 7.7    90 rows 7.8 / 9.8 / 9.7
+//   512 pools   1 row 17.9 / 12.5 / 9.2 / 7.9 / 7.4    16 rows 18.4 / 13.2 / 9.5 / 8.1 / 8.9
+//               32 rows 20.0 / 14.6 / 10.6 / 10.8 / 9.9    40 rows 20.4 / 14.9 / 12.8 / 11.4 / 11.8
+//               64 rows 20.7 / 15.6 / 14.2 / 15.2    100 rows 20.6 / 19.2 / 17.5    228 rows 27.3 / 25.3
+//   255 pools   1 row 10.3 / 8.6 / 6.9 / 6.6 / 6.5    32 rows 10.8 / 9.5 / 7.6 / 8.1 / 7.6
+//               64 rows 11.9 / 10.3 / 9.7 / 10.0    130 rows 11.2 / 11.7
+//   128 pools   1 row 7.7 / 7.3 / 6.5 / 6.1 / 6.1    40 rows 8.2 / 8.0 / 7.8 / 7.4 / 7.8    90 rows 8.2 / 9.3 / 8.8
 int split_wanted(int64_t rows, int blocks, int num_sms) {
   const int64_t sms = num_sms;
   if (blocks < 6) return 1;
@@ -727,8 +728,8 @@ cudaError_t launch_paged4_attn(const CacheView& c, const BatchView& b, const voi
     }
   }
   // A long ring and three CTAs an SM while all rows run at once, else a short one
-  // and four: 300 rows 27.2 us against 29.5, 456 rows 36.7 and 37.9, 512 rows 50.3
-  // and 46.7, 4096 rows 263 and 261.
+  // and four: 300 rows 28.0 us against 30.2, 456 rows 37.3 and 38.2, 512 rows 51.2
+  // and 47.0, 4096 rows 267 and 265.
   if (b.rows <= 3 * static_cast<int64_t>(ctx.num_sms))
     return launch_variant<6, false>(c, b, q, pool_idx, topk, scale, o, lse, 1, ctx);
   return launch_variant<4, false>(c, b, q, pool_idx, topk, scale, o, lse, 1, ctx);

@@ -164,8 +164,9 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : 1)
 
   // Row table of this CTA's blocks, a pool a thread.  Slot s < nsel holds pool
   // prow[s]; slot nsel is the row's own pool; slots beyond are empty.  An entry
-  // that is no eligible pool or breaks ascending order, and a page that is
-  // none, are recorded; nothing is read for them.
+  // that is no eligible pool, and a page that is none, are recorded, and nothing
+  // is read for them; an entry that breaks ascending order is recorded, too, and
+  // attended to as it stands.
   bool bad = false;
   const int pshift = c.shift - 2;  // log2(pools per page)
   for (int e = tid; e < nblk * kBlkPools; e += kThreads) {
