@@ -11,6 +11,7 @@ host compiler for it), a warning says why.
 from __future__ import annotations
 
 import concurrent.futures
+import contextlib
 import glob
 import os
 import shutil
@@ -100,15 +101,19 @@ def build_marshal(force: bool = False) -> str:
 def _try_marshal(force: bool):
     """Build the extension module; returns why it could not be built (the Python code then does every call), or None."""
     plain = os.path.join(os.path.dirname(MARSHAL), "_marshal.so")  # a name that any Python would import
-    if plain != MARSHAL and os.path.exists(plain):
-        os.remove(plain)
+    if plain != MARSHAL:
+        _remove(plain)
     try:
         build_marshal(force)
     except Exception as e:
-        if os.path.exists(MARSHAL):
-            os.remove(MARSHAL)  # made of other sources, or for another torch
+        _remove(MARSHAL)  # made of other sources, or for another torch
         return e
     return None
+
+
+def _remove(path: str) -> None:
+    with contextlib.suppress(FileNotFoundError):  # (another process may build, too)
+        os.remove(path)
 
 
 def _warn_marshal(why) -> None:

@@ -45,6 +45,23 @@ def test_library_is_built_without_the_extension_module(tree, monkeypatch, how):
         assert os.path.exists(b.LIB) and not any("_marshal" in n for n in os.listdir(tree))
 
 
+def test_two_builds_at_once(tree, monkeypatch):
+    """What one of them removes is gone for the other one, which goes on."""
+    real = os.remove
+
+    def late(path):
+        real(path)
+        raise FileNotFoundError(path)
+
+    monkeypatch.setattr(os, "remove", late)
+    monkeypatch.setenv("CXX", "false")
+    for name in ("_marshal.so", os.path.basename(b.MARSHAL)):
+        (tree / name).write_text("of another build")
+    with pytest.warns(RuntimeWarning, match="was not built"):
+        b.build()
+    assert not any("_marshal" in n for n in os.listdir(tree))
+
+
 def test_extension_module_is_built_beside_the_library(tree, monkeypatch):
     """Also where the library is up to date, and for each torch anew; no warning."""
     compiler = tree / "cxx"
